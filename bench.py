@@ -50,7 +50,7 @@ TRAFFIC_PER_FLOP_PRECISE = {("3xtf32", "gemm_precise"): 1.556e-2,
 FALLBACK = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0}
 # the library's kernel classes (ROT_PROF_* in include/rot.h), in id order
 PROF_CLASSES = ["gemm", "elementwise", "qr_panel", "qr_apply", "qr_other", "gemm_precise",
-                "gemm_f16", "gemm_precise_f16"]
+                "gemm_f16", "gemm_precise_f16", "gemm_f8"]
 
 
 def load_peaks():

@@ -294,7 +294,8 @@ uint64_t rot_set_wait_timeout_ns(uint64_t ns);
  * stream around each launch, tagged with its kernel class and algorithmic
  * work.  Host-side state shared by all plans; thread-safe. */
 #define ROT_PROF_GEMM 0        /* tensor-core GEMM (TF32 / 3xTF32); work = 2 M N K flops */
-#define ROT_PROF_ELEMENTWISE 1 /* momentum, Adam, transposes, splits; work = bytes moved */
+#define ROT_PROF_ELEMENTWISE 1 /* momentum, Adam, transposes, splits, and the operators of
+                                  rot_ops.h other than products; work = bytes moved */
 #define ROT_PROF_QR_PANEL 2    /* QR panel factorisation; work = 0 (latency bound) */
 #define ROT_PROF_QR_APPLY 3    /* QR block-reflector updates; work = flops (32-wide panels) */
 #define ROT_PROF_QR_OTHER 4    /* QR set-up, column norms, identity, sign fix; work = 0 */
@@ -302,7 +303,8 @@ uint64_t rot_set_wait_timeout_ns(uint64_t ns);
 #define ROT_PROF_GEMM_F16 6    /* 3xF16 tensor-core GEMM; work = 2 M N K flops */
 #define ROT_PROF_GEMM_PRECISE_F16 7 /* the precise GEMM on scaled fp16 splits (the
                                        refresh products in ROT_PREC_3XF16 mode) */
-#define ROT_PROF_CLASSES 8
+#define ROT_PROF_GEMM_F8 8     /* products of 8-bit matrices (rot_ops.h); work = 2 M N K flops */
+#define ROT_PROF_CLASSES 9
 
 /* Turn event recording on (on != 0) or off.  Returns ROT_OK. */
 int rot_profile_enable(int32_t on);

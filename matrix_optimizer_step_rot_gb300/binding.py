@@ -18,7 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 # build, librot_check.so, in its tests)
 LIB_PATH = os.environ.get("ROT_LIB") or os.path.join(PKG, "librot.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
-HEADERS = [os.path.join(INCLUDE, "rot.h"), os.path.join(INCLUDE, "rot_testing.h")]
+HEADERS = [os.path.join(INCLUDE, h) for h in ("rot.h", "rot_ops.h", "rot_testing.h")]
 
 ROT_OK = 0
 ROT_EINVAL = -1
@@ -37,6 +37,7 @@ ROT_PREC_3XF16 = 5
 ROT_TEST_PREC_3XF16_PRECISE = 16  # rot_test_gemm only: the precise kernel on fp16 splits
 ROT_WHICH_M, ROT_WHICH_V2, ROT_WHICH_U, ROT_WHICH_V = 0, 1, 2, 3
 ROT_STATE_FULL, ROT_STATE_COMPACT = 0, 1
+ROT_TYPE_F32, ROT_TYPE_F16, ROT_TYPE_BF16, ROT_TYPE_E4M3, ROT_TYPE_E5M2 = 0, 1, 2, 3, 4
 
 
 class RotError(RuntimeError):
@@ -53,7 +54,9 @@ _lib: Optional[ctypes.CDLL] = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _u64 = ctypes.c_uint64
+_i64 = ctypes.c_int64
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 _SIGS = {
     "rot_plan_create": (_i32, [ctypes.POINTER(rot_shape), _i32, _u64, ctypes.POINTER(_vp)]),
@@ -90,6 +93,22 @@ _SIGS = {
     "rot_test_check_guards": (_i32, [_vp, _i32, _vp, _vp, _vp]),
     "rot_test_wait_timeout": (_i32, [_u64, _vp, _vp]),
     "rot_test_fail_host_alloc": (_i32, [ctypes.c_int64]),
+    "rot_dropout": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _f64, _u64, _u64,
+                           _vp]),
+    "rot_layer_norm_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _i64,
+                                      _vp, _vp, _i64, _i64, _i32, _f32, _f64, _u64, _u64, _vp]),
+    "rot_layer_norm_work_bytes": (_u64, [_i64, _i64]),
+    "rot_layer_norm_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _vp,
+                                       _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _f64, _u64,
+                                       _u64, _vp, _u64, _vp]),
+    "rot_token_logprobs": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _vp]),
+    "rot_policy_loss": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                               _i64, _i32, _f32, _f32, _f32, _f32, _vp]),
+    "rot_fp8_quantize": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                                _vp, _i64, _vp, _i64, _vp]),
+    "rot_fp8_gemm_work_bytes": (_u64, [_i64, _i64, _i64]),
+    "rot_fp8_gemm": (_i32, [_i64, _i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i64, _i32,
+                            _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _u64, _vp, _vp]),
     "rot_item_work": (_i32, [ctypes.POINTER(rot_shape), _i32, ctypes.POINTER(_u64)]),
     "rot_partition_static": (_i32, [ctypes.POINTER(_u64), _i32, ctypes.POINTER(_i32), _i32, _i32,
                                     ctypes.POINTER(_i32)]),

@@ -1,0 +1,642 @@
+// Dropout and layer norm (include/rot_ops.h).  Both are bound by HBM: one
+// read of every input, one write of every output, the dropout mask computed
+// where it is used.
+#include <algorithm>
+#include <cmath>
+
+#include "ops_common.cuh"
+#include "profile.h"
+
+namespace rot {
+namespace ops {
+
+Drop make_drop(double p, uint64_t seed, uint64_t offset) {
+  Drop d;
+  d.on = p > 0.0;
+  const double bar = std::nearbyint(p * 4294967296.0);
+  d.all = bar >= 4294967296.0;
+  d.bar = d.all ? 0u : (uint32_t)bar;
+  d.scale = d.all ? 0.f : (float)(1.0 / (1.0 - p));
+  d.seed = seed;
+  d.offset = offset;
+  return d;
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// dropout
+// ---------------------------------------------------------------------------
+
+// One run of U consecutive elements of the row-major order per step.  VEC:
+// every run lies in one row and is one 16-byte access (the host checked);
+// otherwise element by element, the run's row found by one division.
+template <class T, int U, bool VEC>
+__global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, const T* res,
+                                                      int64_t ldr, T* y, int64_t ldy,
+                                                      int64_t rows, int64_t cols, Drop d) {
+  const int64_t total = rows * cols, runs = (total + U - 1) / U;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < runs;
+       u += (int64_t)gridDim.x * 256) {
+    const int64_t i0 = u * U;
+    int64_t row = 0, col = i0;
+    if (rows > 1) {
+      row = i0 / cols;
+      col = i0 - row * cols;
+    }
+    if (VEC && i0 + U <= total) {
+      float f[U], r[U];
+      load_run(x + row * ldx + col, f);
+      if (res) load_run(res + row * ldr + col, r);
+      drop_run(d, (uint64_t)i0, f);
+      if (res) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) f[k] = __fadd_rn(r[k], f[k]);
+      }
+      store_run(y + row * ldy + col, f);
+    } else {
+      float f[U], r[U];
+      int64_t rw = row, c = col;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool ok = i0 + k < total;
+        f[k] = ok ? to_f32(x[rw * ldx + c]) : 0.f;
+        r[k] = ok && res ? to_f32(res[rw * ldr + c]) : 0.f;
+        if (++c == cols) {
+          c = 0;
+          ++rw;
+        }
+      }
+      drop_run(d, (uint64_t)i0, f);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (i0 + k < total)
+          y[row * ldy + col] = from_f32<T>(res ? __fadd_rn(r[k], f[k]) : f[k]);
+        if (++col == cols) {
+          col = 0;
+          ++row;
+        }
+      }
+    }
+  }
+}
+
+template <class T>
+int launch_dropout(const void* x, int64_t ldx, const void* res, int64_t ldr, void* y, int64_t ldy,
+                   int64_t rows, int64_t cols, const Drop& d, cudaStream_t s) {
+  constexpr int U = 16 / sizeof(T);
+  if ((ldx == cols || rows == 1) && (ldy == cols || rows == 1) && (!res || ldr == cols || rows == 1)) {
+    cols *= rows;  // one long row
+    rows = 1;
+    ldx = ldy = ldr = cols;
+  }
+  const int64_t total = rows * cols, runs = (total + U - 1) / U;
+  const bool vec = aligned16(x) && aligned16(y) && (!res || aligned16(res)) &&
+                   (rows == 1 || (cols % U == 0 && rows16(x, ldx, sizeof(T)) &&
+                                  rows16(y, ldy, sizeof(T)) && rows16(res, ldr, sizeof(T))));
+  const int grid = (int)std::min<int64_t>((runs + 255) / 256, 16ll * sm_count());
+  ProfScope prof(ROT_PROF_ELEMENTWISE, (double)total * sizeof(T) * (res ? 3 : 2), s);
+  auto k = vec ? dropout_kernel<T, U, true> : dropout_kernel<T, U, false>;
+  k<<<grid, 256, 0, s>>>((const T*)x, ldx, (const T*)res, ldr, (T*)y, ldy, rows, cols, d);
+  return launched();
+}
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+
+struct NormFwd {
+  const void *x, *res, *w, *b;
+  void *h, *y;
+  float *mean, *rstd;
+  int64_t ldx, ldr, ldh, ldy, rows;
+  int cols;
+  int w32;  // weight and bias are float32 (otherwise of the row's type)
+  float eps;
+  Drop d;
+};
+
+struct NormBwd {
+  const void *dy, *h, *w, *dh;
+  const float *mean, *rstd;
+  void *dres, *dx;
+  float* part;  // [parts][2][cols]: dweight, dbias
+  int64_t lddy, ldh, lddh, lddres, lddx, rows;
+  int cols;
+  int w32;
+  Drop d;
+};
+
+template <class T, int U>
+__device__ __forceinline__ void load_weight(const void* w, bool w32, int c, float (&f)[U]) {
+  if (w32) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) f[k] = ((const float*)w)[c + k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < U; ++k) f[k] = to_f32(((const T*)w)[c + k]);
+  }
+}
+
+// Sum of one value over the TPR threads of each row of the block; `red` holds
+// one float per warp.  Calls in a row need different `red` arrays (a thread
+// may still read the last one).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float* red) {
+  x = warp_sum(x);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = x;
+    __syncthreads();
+    const int first = warp / W * W;
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x += red[first + i];
+  }
+  return x;
+}
+
+// A row in the registers of TPR threads, N runs of U elements each.
+template <class T, int U, int TPR, int N>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const NormFwd a) {
+  constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
+  __shared__ float red[2][kBlock / 32];
+  const int t = threadIdx.x % TPR;
+  const float inv = 1.f / (float)a.cols;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
+    const int64_t row = base + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    float h[N][U];
+    float sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      const bool in = live && c < a.cols;
+#pragma unroll
+      for (int k = 0; k < U; ++k) h[n][k] = 0.f;
+      if (in) {
+        load_run((const T*)a.x + row * a.ldx + c, h[n]);
+        float r[U];
+        if (a.res) load_run((const T*)a.res + row * a.ldr + c, r);
+        if (a.h) {
+          drop_run(a.d, (uint64_t)row * a.cols + c, h[n]);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            if (a.res) h[n][k] = __fadd_rn(r[k], h[n][k]);
+            h[n][k] = to_f32(from_f32<T>(h[n][k]));  // the norm reads what is stored
+          }
+          store_run((T*)a.h + row * a.ldh + c, h[n]);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) sum += h[n][k];
+      }
+    }
+    const float mean = row_sum<TPR>(sum, red[0]) * inv;
+    float sq = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if ((n * TPR + t) * U < a.cols) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          h[n][k] -= mean;
+          sq += h[n][k] * h[n][k];
+        }
+      }
+    const float rstd = 1.f / sqrtf(row_sum<TPR>(sq, red[1]) * inv + a.eps);
+    if (live && t == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        float w[U], b[U];
+        load_weight<T>(a.w, a.w32, c, w);
+        if (a.b) load_weight<T>(a.b, a.w32, c, b);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          h[n][k] = h[n][k] * rstd * w[k];
+          if (a.b) h[n][k] += b[k];
+        }
+        store_run((T*)a.y + row * a.ldy + c, h[n]);
+      }
+    }
+  }
+}
+
+// Rows too wide for the registers: a block per row, three passes over it (the
+// second and third out of L2).
+template <class T>
+__global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormFwd a) {
+  __shared__ float red[2][32];
+  const float inv = 1.f / (float)a.cols;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* src = a.h ? (const T*)a.h + row * a.ldh : (const T*)a.x + row * a.ldx;
+    float sum = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      float f[1] = {to_f32(((const T*)a.x)[row * a.ldx + c])};
+      if (a.h) {
+        const float r = a.res ? to_f32(((const T*)a.res)[row * a.ldr + c]) : 0.f;
+        drop_run(a.d, (uint64_t)row * a.cols + c, f);
+        const T v = from_f32<T>(a.res ? __fadd_rn(r, f[0]) : f[0]);
+        ((T*)a.h)[row * a.ldh + c] = v;
+        f[0] = to_f32(v);
+      }
+      sum += f[0];
+    }
+    const float mean = row_sum<1024>(sum, red[0]) * inv;
+    float sq = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      const float f = to_f32(src[c]) - mean;
+      sq += f * f;
+    }
+    const float rstd = 1.f / sqrtf(row_sum<1024>(sq, red[1]) * inv + a.eps);
+    if (threadIdx.x == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      float w[1], b[1] = {0.f};
+      load_weight<T>(a.w, a.w32, c, w);
+      if (a.b) load_weight<T>(a.b, a.w32, c, b);
+      const float y = (to_f32(src[c]) - mean) * rstd * w[0];
+      ((T*)a.y)[row * a.ldy + c] = from_f32<T>(a.b ? y + b[0] : y);
+    }
+  }
+}
+
+// g of one run from its wdy and hat, written out; dropped into dx.
+template <class T, int U>
+__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, float (&g)[U]) {
+  if (a.dh) {
+    float d[U];
+    load_run((const T*)a.dh + row * a.lddh + c, d);
+#pragma unroll
+    for (int k = 0; k < U; ++k) g[k] += d[k];
+  }
+  if (a.dres) store_run((T*)a.dres + row * a.lddres + c, g);
+  drop_run(a.d, (uint64_t)row * a.cols + c, g);
+  store_run((T*)a.dx + row * a.lddx + c, g);
+}
+
+// As the forward kernel; every block walks the rows with a stride and keeps
+// its columns' weight gradients in registers, so that each is written once.
+template <class T, int U, int TPR, int N>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const NormBwd a) {
+  constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
+  __shared__ float red[4][kBlock / 32];
+  __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const float inv = 1.f / (float)a.cols;
+  float dw[N][U], db[N][U];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < U; ++k) dw[n][k] = db[n][k] = 0.f;
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
+    const int64_t row = base + group;
+    const bool live = row < a.rows;
+    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
+    float wdy[N][U], hat[N][U];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        float w[U];
+        load_run((const T*)a.dy + row * a.lddy + c, wdy[n]);
+        load_run((const T*)a.h + row * a.ldh + c, hat[n]);
+        load_weight<T>(a.w, a.w32, c, w);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          hat[n][k] = (hat[n][k] - mean) * rstd;
+          dw[n][k] += wdy[n][k] * hat[n][k];
+          db[n][k] += wdy[n][k];
+          wdy[n][k] *= w[k];
+          s1 += wdy[n][k];
+          s2 += wdy[n][k] * hat[n][k];
+        }
+      }
+    }
+    s1 = row_sum<TPR>(s1, red[turn]) * inv;
+    s2 = row_sum<TPR>(s2, red[turn + 1]) * inv;
+    turn ^= 2;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) wdy[n][k] = rstd * (wdy[n][k] - s1 - hat[n][k] * s2);
+        write_grad<T>(a, row, c, wdy[n]);
+      }
+    }
+  }
+  // this block's part of the weight gradient: the groups' sums in order
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          join[group][(n * TPR + t) * U + k] = which ? db[n][k] : dw[n][k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += kBlock) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < RPB; ++g) sum += join[g][c];
+        part[which * a.cols + c] = sum;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * TPR + t) * U;
+        if (c < a.cols) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) part[which * a.cols + c + k] = which ? db[n][k] : dw[n][k];
+        }
+      }
+    }
+  }
+}
+
+// Rows too wide for the registers: the rows' gradients (two passes over a
+// row) and the columns' partial sums in kernels of their own.
+template <class T>
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormBwd a) {
+  __shared__ float red[4][32];
+  const float inv = 1.f / (float)a.cols;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* h = (const T*)a.h + row * a.ldh;
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      float w[1];
+      load_weight<T>(a.w, a.w32, c, w);
+      const float wdy = to_f32(dy[c]) * w[0];
+      s1 += wdy;
+      s2 += wdy * ((to_f32(h[c]) - mean) * rstd);
+    }
+    s1 = row_sum<1024>(s1, red[turn]) * inv;
+    s2 = row_sum<1024>(s2, red[turn + 1]) * inv;
+    turn ^= 2;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      float w[1];
+      load_weight<T>(a.w, a.w32, c, w);
+      const float hat = (to_f32(h[c]) - mean) * rstd;
+      float g[1] = {rstd * (to_f32(dy[c]) * w[0] - s1 - hat * s2)};
+      write_grad<T>(a, row, c, g);
+    }
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwd a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  float dw = 0.f, db = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float dy = to_f32(((const T*)a.dy)[row * a.lddy + c]);
+    dw += dy * ((to_f32(((const T*)a.h)[row * a.ldh + c]) - a.mean[row]) * a.rstd[row]);
+    db += dy;
+  }
+  float* part = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+  part[c] = dw;
+  part[a.cols + c] = db;
+}
+
+// dweight and dbias: the parts' sums.  32 columns by 32 strided shares of the
+// parts per block, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int parts, int cols,
+                                                         float* dweight, float* dbias) {
+  __shared__ float share[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane, width = 2ll * cols;
+  float sum = 0.f;
+  if (i < width)
+    for (int p = warp; p < parts; p += 32) sum += part[(int64_t)p * width + i];
+  share[warp][lane] = sum;
+  __syncthreads();
+  sum = warp_sum(share[lane][warp]);  // column `warp` of this block
+  const int64_t j = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && j < width) {
+    if (j < cols)
+      dweight[j] = sum;
+    else if (dbias)
+      dbias[j - cols] = sum;
+  }
+}
+
+// Partial sums kept at most (the workspace's size does not depend on the GPU).
+constexpr int kMaxParts = 608;
+
+// Threads per row that hold `cols` in 16 elements each.
+inline int row_threads(int cols) {
+  return cols <= 512 ? 32 : cols <= 2048 ? 128 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
+}
+
+template <class T, int U>
+int launch_fwd(const NormFwd& a, cudaStream_t s) {
+  constexpr int N = 16 / U;
+  const int tpr = row_threads(a.cols);
+  const int rpb = tpr >= 256 ? 1 : 256 / tpr;
+  const unsigned grid = (unsigned)std::min<int64_t>((a.rows + rpb - 1) / rpb, 1 << 20);
+  switch (tpr) {
+    case 32: norm_fwd_kernel<T, U, 32, N><<<grid, 256, 0, s>>>(a); break;
+    case 128: norm_fwd_kernel<T, U, 128, N><<<grid, 256, 0, s>>>(a); break;
+    case 256: norm_fwd_kernel<T, U, 256, N><<<grid, 256, 0, s>>>(a); break;
+    case 512: norm_fwd_kernel<T, U, 512, N><<<grid, 512, 0, s>>>(a); break;
+    default: norm_fwd_kernel<T, U, 1024, N><<<grid, 1024, 0, s>>>(a); break;
+  }
+  return launched();
+}
+
+template <class T>
+int run_fwd(const NormFwd& a, cudaStream_t s) {
+  constexpr int U = 16 / sizeof(T);
+  ProfScope prof(ROT_PROF_ELEMENTWISE,
+                 (double)a.rows * a.cols * sizeof(T) * (2 + (a.res != nullptr) + (a.h != nullptr)), s);
+  if (a.cols > 16384) {
+    norm_fwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
+    return launched();
+  }
+  const bool vec = a.cols % U == 0 && rows16(a.x, a.ldx, sizeof(T)) &&
+                   rows16(a.res, a.ldr, sizeof(T)) && rows16(a.h, a.ldh, sizeof(T)) &&
+                   rows16(a.y, a.ldy, sizeof(T));
+  return vec ? launch_fwd<T, U>(a, s) : launch_fwd<T, 1>(a, s);
+}
+
+template <class T, int U>
+int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
+  constexpr int N = 16 / U;
+  const int tpr = row_threads(a.cols);
+  const int rpb = tpr >= 256 ? 1 : 256 / tpr;
+  const int per_sm = tpr >= 512 ? 1 : 2;
+  *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
+                                  std::min(kMaxParts, per_sm * sm_count()));
+  switch (tpr) {
+    case 32: norm_bwd_kernel<T, U, 32, N><<<*parts, 256, 0, s>>>(a); break;
+    case 128: norm_bwd_kernel<T, U, 128, N><<<*parts, 256, 0, s>>>(a); break;
+    case 256: norm_bwd_kernel<T, U, 256, N><<<*parts, 256, 0, s>>>(a); break;
+    default: norm_bwd_kernel<T, U, 512, N><<<*parts, 512, 0, s>>>(a); break;
+  }
+  return launched();
+}
+
+template <class T>
+int run_bwd(const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
+  constexpr int U = 16 / sizeof(T);
+  int parts = 0, e = ROT_OK;
+  const double bytes = (double)a.rows * a.cols * sizeof(T) *
+                       (3 + (a.dh != nullptr) + (a.dres != nullptr));
+  if (a.cols > 8192) {
+    {
+      ProfScope prof(ROT_PROF_ELEMENTWISE, bytes, s);
+      norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
+      if ((e = launched()) != ROT_OK) return e;
+    }
+    parts = (int)std::min<int64_t>(a.rows, 64);
+    ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
+    norm_bwd_cols_kernel<T><<<dim3((a.cols + 255) / 256, parts), 256, 0, s>>>(a);
+    e = launched();
+  } else {
+    ProfScope prof(ROT_PROF_ELEMENTWISE, bytes, s);
+    const bool vec = a.cols % U == 0 && rows16(a.dy, a.lddy, sizeof(T)) &&
+                     rows16(a.h, a.ldh, sizeof(T)) && rows16(a.dh, a.lddh, sizeof(T)) &&
+                     rows16(a.dres, a.lddres, sizeof(T)) && rows16(a.dx, a.lddx, sizeof(T));
+    e = vec ? launch_bwd<T, U>(a, &parts, s) : launch_bwd<T, 1>(a, &parts, s);
+  }
+  if (e != ROT_OK) return e;
+  ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
+  norm_join_kernel<<<(2 * a.cols + 31) / 32, 1024, 0, s>>>(a.part, parts, a.cols, dweight, dbias);
+  return launched();
+}
+
+template <template <class> class Fn, class... Args>
+int by_type(int32_t type, Args&&... args) {
+  if (type == ROT_TYPE_F32) return Fn<float>::run(args...);
+  if (type == ROT_TYPE_F16) return Fn<__half>::run(args...);
+  return Fn<__nv_bfloat16>::run(args...);
+}
+template <class T>
+struct FwdFn {
+  static int run(const NormFwd& a, cudaStream_t s) { return run_fwd<T>(a, s); }
+};
+template <class T>
+struct BwdFn {
+  static int run(const NormBwd& a, float* dw, float* db, cudaStream_t s) {
+    return run_bwd<T>(a, dw, db, s);
+  }
+};
+template <class T>
+struct DropFn {
+  static int run(const void* x, int64_t ldx, const void* res, int64_t ldr, void* y, int64_t ldy,
+                 int64_t rows, int64_t cols, const Drop& d, cudaStream_t s) {
+    return launch_dropout<T>(x, ldx, res, ldr, y, ldy, rows, cols, d, s);
+  }
+};
+
+inline bool bad_p(double p) { return !(p >= 0.0 && p <= 1.0); }
+
+// rows * cols elements must be countable in 63 bits with room for a pitch
+inline bool bad_size(int64_t rows, int64_t cols) {
+  return rows < 0 || cols < 0 || (cols > 0 && rows > (int64_t(1) << 60) / cols);
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace rot
+
+using namespace rot;
+using namespace rot::ops;
+
+extern "C" {
+
+int rot_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* y,
+                int64_t ldy, int64_t rows, int64_t cols, int32_t type, double p, uint64_t seed,
+                uint64_t offset, void* stream) {
+  if (bad_size(rows, cols) || !float_type(type) || bad_p(p)) return ROT_EINVAL;
+  if (ldx < cols || ldy < cols || (residual && ldr < cols)) return ROT_EINVAL;
+  if (rows == 0 || cols == 0) return ROT_OK;
+  if (!x || !y) return ROT_EINVAL;
+  const int dev = check_device();
+  if (dev != ROT_OK) return dev;
+  return guarded([&] {
+    return by_type<DropFn>(type, x, ldx, residual, ldr, y, ldy, rows, cols,
+                           make_drop(p, seed, offset), static_cast<cudaStream_t>(stream));
+  });
+}
+
+int rot_layer_norm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* weight, const void* bias, int32_t wtype, void* h_out,
+                           int64_t ldh, void* y, int64_t ldy, float* mean, float* rstd,
+                           int64_t rows, int64_t cols, int32_t type, float eps, double p,
+                           uint64_t seed, uint64_t offset, void* stream) {
+  if (rows < 0 || cols < 1 || cols > ROT_MAX_DIM || bad_size(rows, cols)) return ROT_EINVAL;
+  if (!float_type(type) || (wtype != ROT_TYPE_F32 && wtype != type)) return ROT_EINVAL;
+  if (bad_p(p) || !(eps >= 0.f)) return ROT_EINVAL;
+  const bool mixes = residual || p > 0.0;
+  if (ldx < cols || ldy < cols || (residual && ldr < cols) || (mixes && ldh < cols))
+    return ROT_EINVAL;
+  if (rows == 0) return ROT_OK;
+  if (!x || !weight || !y || !mean || !rstd || (mixes && !h_out)) return ROT_EINVAL;
+  const int dev = check_device();
+  if (dev != ROT_OK) return dev;
+  NormFwd a;
+  a.x = x, a.res = residual, a.w = weight, a.b = bias;
+  a.h = mixes ? h_out : nullptr, a.y = y, a.mean = mean, a.rstd = rstd;
+  a.ldx = ldx, a.ldr = ldr, a.ldh = ldh, a.ldy = ldy, a.rows = rows, a.cols = (int)cols;
+  a.w32 = wtype == ROT_TYPE_F32, a.eps = eps, a.d = make_drop(p, seed, offset);
+  return guarded([&] { return by_type<FwdFn>(type, a, static_cast<cudaStream_t>(stream)); });
+}
+
+uint64_t rot_layer_norm_work_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1 || cols > ROT_MAX_DIM) return 0;
+  return align256(8ull * (uint64_t)cols * (uint64_t)std::min<int64_t>(rows, kMaxParts));
+}
+
+int rot_layer_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                            const float* mean, const float* rstd, const void* weight,
+                            int32_t wtype, const void* dh, int64_t lddh, void* dres_out,
+                            int64_t lddres, void* dx, int64_t lddx, float* dweight, float* dbias,
+                            int64_t rows, int64_t cols, int32_t type, double p, uint64_t seed,
+                            uint64_t offset, void* work, uint64_t work_bytes, void* stream) {
+  if (rows < 0 || cols < 1 || cols > ROT_MAX_DIM || bad_size(rows, cols)) return ROT_EINVAL;
+  if (!float_type(type) || (wtype != ROT_TYPE_F32 && wtype != type) || bad_p(p))
+    return ROT_EINVAL;
+  if (lddy < cols || ldh < cols || lddx < cols || (dh && lddh < cols) ||
+      (dres_out && lddres < cols))
+    return ROT_EINVAL;
+  if (!dweight || (p > 0.0 && rows > 0 && !dres_out)) return ROT_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    const int dev = check_device();
+    if (dev != ROT_OK) return dev;
+    if (cudaMemsetAsync(dweight, 0, 4 * cols, s) != cudaSuccess ||
+        (dbias && cudaMemsetAsync(dbias, 0, 4 * cols, s) != cudaSuccess))
+      return ROT_ECUDA;
+    return ROT_OK;
+  }
+  if (!dy || !h || !mean || !rstd || !weight || !dx || !work) return ROT_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(work) & 255) ||
+      work_bytes < rot_layer_norm_work_bytes(rows, cols))
+    return ROT_EINVAL;
+  const int dev = check_device();
+  if (dev != ROT_OK) return dev;
+  NormBwd a;
+  a.dy = dy, a.h = h, a.w = weight, a.dh = dh, a.mean = mean, a.rstd = rstd;
+  a.dres = dres_out, a.dx = dx, a.part = static_cast<float*>(work);
+  a.lddy = lddy, a.ldh = ldh, a.lddh = lddh, a.lddres = lddres, a.lddx = lddx;
+  a.rows = rows, a.cols = (int)cols, a.w32 = wtype == ROT_TYPE_F32;
+  a.d = make_drop(p, seed, offset);
+  return guarded([&] { return by_type<BwdFn>(type, a, dweight, dbias, s); });
+}
+
+}  // extern "C"

@@ -1,0 +1,655 @@
+"""The training operators on the GPU against plain 64-bit restatements
+(tests/operators_ref.py), at the sizes, strides and values where they can go
+wrong.
+
+Tolerances.  u is the unit roundoff of an output's type (2^-24, 2^-11, 2^-8 for
+float32, float16, bfloat16): one rounding of a result costs u |result|.
+Float32 sums of n terms along a chain of c additions cost at most c 2^-24 times
+the sum of the magnitudes; the chains are counted beside each test."""
+
+import numpy as np
+import pytest
+import torch
+
+from matrix_optimizer_step_rot_gb300 import binding as B
+from matrix_optimizer_step_rot_gb300 import build
+from matrix_optimizer_step_rot_gb300 import operators as ops
+from tests import operators_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 1e-44, torch.float16: 2.0 ** -24, torch.bfloat16: 1e-39}
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+E = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    build.build()
+    B.lib()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rows_of(g, rows, cols, pad, dtype, shift=0.0):
+    """rows x cols of a buffer `pad` elements wider, the rest NaN."""
+    x = torch.randn(rows, cols + pad, generator=g, device="cuda") + shift
+    x[:, cols:] = float("nan")
+    return x.to(dtype)[:, :cols]
+
+
+def near(got, want, bound, what=""):
+    """|got - want| <= bound element by element; NaN and infinities in the same places."""
+    got, want = got.double(), want.double()
+    assert got.shape == want.shape, what
+    fine = torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    assert torch.equal(got[~fine & ~torch.isnan(want)], want[~fine & ~torch.isnan(want)]), what
+    over = ((got - want).abs() - bound)[fine]
+    assert over.numel() == 0 or over.max().item() <= 0, f"{what}: beyond its bound by {over.max().item():.3e}"
+
+
+# ---------------------------------------------------------------------------
+# dropout
+# ---------------------------------------------------------------------------
+
+SEED, OFFSET = 0xFEDCBA9876543210, (7 << 33) + 5
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,cols,pad,p,with_res", [
+    (1, 1, 0, 0.5, False), (1, 7, 0, 0.5, True), (3, 5, 2, 0.3, True), (257, 1001, 0, 0.25, False),
+    (64, 128, 0, 0.1, True), (33, 136, 8, 0.1, True), (33, 136, 3, 0.1, True), (2, 4096, 0, 0.0, True),
+    (5, 999, 0, 1.0, True), (1, 65537, 0, 0.5, False), (300, 4, 4, 0.7, False), (300, 2, 6, 0.7, True)])
+def test_dropout(dtype, rows, cols, pad, p, with_res):
+    g = gen(rows + cols)
+    x = rows_of(g, rows, cols, pad, dtype)
+    res = rows_of(g, rows, cols, 0, dtype) if with_res else None
+    y = ops.dropout(x, p, SEED, OFFSET, residual=res)
+    want = ref.dropped(x, p, SEED, OFFSET)
+    # the product rounds once in float32, the sum once, the result once
+    bound = U[dtype] * want.abs() + E * want.abs() + TINY[dtype]
+    if with_res:
+        total = want + res.double()
+        bound = U[dtype] * total.abs() + E * (want.abs() + total.abs()) * 1.01 + TINY[dtype]
+        want = total
+    near(y, want, bound * 1.001)
+    if not with_res:  # the mask itself, exactly
+        assert torch.equal(y == 0, (want == 0) | (x == 0))
+
+
+def test_dropout_ignores_what_it_drops():
+    x = torch.full((64, 64), float("nan"), device="cuda")
+    keep = torch.from_numpy(ref.kept(0, 4096, 0.5, 3, 0)).cuda().view(64, 64)
+    y = ops.dropout(x, 0.5, 3, 0, residual=torch.ones(64, 64, device="cuda"))
+    assert torch.equal(torch.isnan(y), keep) and torch.equal(y[~keep], torch.ones_like(y[~keep]))
+    assert torch.equal(ops.dropout(x, 1.0, 3, 0), torch.zeros_like(x))
+
+
+def test_dropout_mask_depends_on_seed_offset_and_position_alone():
+    x = torch.ones(96, 40, device="cuda")
+    a = ops.dropout(x, 0.5, 11, 4)
+    wide = torch.ones(96, 43, device="cuda")[:, :40]
+    assert torch.equal(a, ops.dropout(wide, 0.5, 11, 4))
+    assert torch.equal(a, ops.dropout(x.view(2, 48, 40), 0.5, 11, 4).view(96, 40))
+    assert torch.equal(a, ops.dropout(x.bfloat16(), 0.5, 11, 4).float())
+    assert torch.equal(a, ops.dropout_backward(x, 0.5, 11, 4))
+    assert not torch.equal(a, ops.dropout(x, 0.5, 12, 4))
+    assert not torch.equal(a, ops.dropout(x, 0.5, 11, 5))
+    y = x.clone()
+    assert ops.dropout(y, 0.5, 11, 4, out=y) is y and torch.equal(a, y)
+
+
+def test_dropout_rate():
+    """2^24 elements: the share kept is within five standard deviations."""
+    y = ops.dropout(torch.ones(1 << 24, device="cuda"), 0.1, 99, 0)
+    share = (y != 0).double().mean().item()
+    assert abs(share - 0.9) <= 5 * (0.1 * 0.9 / 2 ** 24) ** 0.5
+
+
+def test_dropout_beyond_32_bit_counters():
+    """Elements past 2^34 use the counter's upper word."""
+    n = (1 << 34) + 40
+    x = torch.ones(n, dtype=BF16, device="cuda")
+    ops.dropout(x, 0.5, 21, 9, out=x)
+    first = (1 << 34) - 32
+    keep = torch.from_numpy(ref.kept(first, 72, 0.5, 21, 9)).cuda()
+    assert torch.equal(x[first:] != 0, keep)
+    assert torch.equal(x[:64] != 0, torch.from_numpy(ref.kept(0, 64, 0.5, 21, 9)).cuda())
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_dropout_on_another_stream():
+    s = torch.cuda.Stream()
+    x = torch.randn(1000, 77, device="cuda")
+    want = ops.dropout(x, 0.3, 5, 6)
+    s.wait_stream(torch.cuda.current_stream())
+    y = ops.dropout(x, 0.3, 5, 6, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+
+NORM = [  # rows, cols, type, pad, residual, p, weight type, bias
+    (1, 1, F32, 0, False, 0.0, F32, True),
+    (1, 2048, BF16, 0, True, 0.0, F32, True),
+    (5, 33, F32, 2, False, 0.1, F32, False),
+    (9, 512, F16, 0, True, 0.1, F16, True),
+    (7, 513, BF16, 0, True, 0.2, F32, True),
+    (1000, 64, BF16, 8, False, 0.0, BF16, True),
+    (333, 641, F32, 7, False, 0.0, F32, True),
+    (3, 2049, F32, 0, True, 0.1, F32, True),
+    (5, 4096, F16, 16, True, 0.1, F32, False),
+    (3, 4097, BF16, 0, True, 0.0, BF16, True),
+    (700, 2048, BF16, 0, True, 0.1, F32, True),
+    (4, 8192, F32, 0, False, 0.0, F32, True),
+    (3, 8200, BF16, 0, True, 0.1, F32, True),
+    (3, 12289, F16, 0, True, 0.1, F32, True),
+    (40, 12288, BF16, 0, True, 0.1, F32, True),
+    (2, 16384, F32, 0, True, 0.1, F32, True),
+    (2, 16385, BF16, 3, True, 0.1, F32, True),
+    (1, 65536, F32, 0, False, 0.0, F32, True)]
+
+
+def norm_inputs(rows, cols, dtype, pad, residual, wtype, bias, seed):
+    g = gen(seed)
+    x = rows_of(g, rows, cols, pad, dtype, shift=0.5)
+    res = rows_of(g, rows, cols, 0, dtype) if residual else None
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(wtype)
+    b = (0.2 * torch.randn(cols, generator=g, device="cuda")).to(wtype) if bias else None
+    return x, res, w, b
+
+
+def chain(cols):
+    """Additions one after the other in a row's sum: at most 64 in a thread, 5
+    in a warp, 32 over the warps; the mean's rounding and its use on top."""
+    return 64 + 5 + 32 + 4
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pad,residual,p,wtype,bias", NORM)
+def test_layer_norm(rows, cols, dtype, pad, residual, p, wtype, bias):
+    x, res, w, b = norm_inputs(rows, cols, dtype, pad, residual, wtype, bias, rows + cols)
+    y, h, mean, rstd = ops.layer_norm(x, w, b, 1e-5, residual=res, p=p, seed=SEED, offset=OFFSET)
+    drop = ref.dropped(x, p, SEED, OFFSET)
+    want = drop if res is None else drop + res.double()
+    if res is None and p == 0:
+        assert h is x
+    else:
+        near(h, want, (U[dtype] * want.abs() + 2 * E * (drop.abs() + want.abs())) * 1.01 + TINY[dtype], "h")
+    y64, mean64, rstd64, hat = ref.norm(h, w, b, 1e-5)
+    mag = h.double().abs().mean(1)
+    dm = chain(cols) * E * mag  # the mean's error; half of it is also var's relative one
+    near(mean, mean64, dm, "mean")
+    rel = 2 * chain(cols) * E + 2 * (dm * rstd64)
+    near(rstd, rstd64, rel * rstd64, "rstd")
+    err = (dm * rstd64 + 2 * E * mag * rstd64)[:, None] + hat.abs() * (rel + 4 * E)[:, None]
+    bound = err * w.double().abs() * 1.01 + 4 * E * y64.abs() + U[dtype] * y64.abs() * 1.01 + TINY[dtype]
+    near(y, y64, bound, "y")
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pad,residual,p,wtype,bias", NORM)
+def test_layer_norm_backward(rows, cols, dtype, pad, residual, p, wtype, bias):
+    h, dh, w, _ = norm_inputs(rows, cols, dtype, pad, residual, wtype, bias, rows + 3 * cols)
+    dy = rows_of(gen(7), rows, cols, 0, dtype)
+    _, mean, rstd, _ = ref.norm(h, w, None, 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    hat = (h.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    dx, dres, dw, db = ops.layer_norm_backward(dy, h, mean, rstd, w, dh=dh, p=p, seed=SEED,
+                                               offset=OFFSET, bias=bias)
+    g64, dw64, db64 = ref.norm_grad(dy, hat, rstd.double(), w, dh)
+    wdy = (dy.double() * w.double()).abs()
+    # hat rounds three times; each of the two means is a chain as above
+    dhat = 3 * E * (hat.abs() + (h.double().abs() * rstd.double()[:, None]))
+    s1, s2 = wdy.mean(1, keepdim=True), (wdy * hat.abs()).mean(1, keepdim=True)
+    e1 = chain(cols) * E * s1
+    e2 = chain(cols) * E * s2 + (wdy * dhat).mean(1, keepdim=True)
+    err = rstd.double()[:, None] * (e1 + hat.abs() * e2 + dhat * s2 + 6 * E * (wdy + s1 + hat.abs() * s2))
+    bound = err * 1.01 + (U[dtype] + 2 * E) * 1.01 * g64.abs() + TINY[dtype]
+    if dh is not None:
+        bound = bound + 2 * E * dh.double().abs()
+    near(dres, g64, bound, "dresidual")
+    if p == 0:
+        assert dres is dx
+    else:
+        near(dx, ref.dropped(g64, p, SEED, OFFSET), 1.01 * ref.dropped(bound, p, SEED, OFFSET) + TINY[dtype]
+             + 2 * U[dtype] * ref.dropped(g64, p, SEED, OFFSET).abs(), "dx")
+    # a column's sum: a chain of rows per part, at most 608 parts in chains of 19, and the joins
+    c = rows + 19 + 16
+    near(dw, dw64, (c * E * (dy.double() * hat).abs().sum(0) + (dy.double().abs() * dhat).sum(0)) * 1.01 + 1e-37, "dweight")
+    if bias:
+        near(db, db64, c * E * dy.double().abs().sum(0) * 1.01 + 1e-37, "dbias")
+    else:
+        assert db is None
+
+
+def test_layer_norm_gradient_against_differences():
+    """Directional derivatives of the forward kernel: central differences of
+    sum(y r) in float32 with step 2^-6.  Rounding: outputs of magnitude <= 8
+    carry 2^-21 each, 3000 of them at random add up to 55 2^-21 2.6e-5, over
+    2 step: 8.4e-4.  Truncation: step^2 / 6 times the third derivative, at most
+    a few times |v|^3 rstd^3 |r|: 4e-5 times a sum of 3000 random signs: 5e-3
+    allowed."""
+    rows, cols, step = 15, 200, 2.0 ** -6
+    x, res, w, b = norm_inputs(rows, cols, F32, 0, True, F32, True, 5)
+    g = gen(3)
+    r = torch.randn(rows, cols, generator=g, device="cuda")
+    kw = dict(p=0.2, seed=8, offset=2)
+
+    def f(x, res, w, b):
+        y = ops.layer_norm(x, w, b, 1e-5, residual=res, **kw)[0]
+        return (y.double() * r.double()).sum().item()
+
+    _, h, mean, rstd = ops.layer_norm(x, w, b, 1e-5, residual=res, **kw)
+    dx, dres, dw, db = ops.layer_norm_backward(r, h, mean, rstd, w, **kw)
+    args = [x, res, w, b]
+    for i, grad in enumerate((dx, dres, dw, db)):
+        v = torch.randn(args[i].shape, generator=g, device="cuda")
+        v = v / v.norm()
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + step * v, args[i] - step * v
+        num = (f(*up) - f(*down)) / (2 * step)
+        assert abs(num - (grad.double() * v.double()).sum().item()) <= 5e-3, i
+
+
+def test_layer_norm_special_rows():
+    """A constant row (variance 0), a row of zeros, and non-finite values that stay in their row."""
+    x = torch.randn(6, 300, device="cuda")
+    x[1] = 3.0
+    x[2] = 0.0
+    x[3, 5] = float("nan")
+    x[4, 7] = float("inf")
+    w, b = torch.ones(300, device="cuda"), torch.full((300,), 0.25, device="cuda")
+    y, _, mean, rstd = ops.layer_norm(x, w, b, 1e-5)
+    assert torch.equal(y[2], b) and abs(rstd[2].item() - 1e-5 ** -0.5) < 1e-4
+    assert (y[1] - 0.25).abs().max().item() <= 1e-6 * 1e-5 ** -0.5 * 3 * 2
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4]).all()
+    assert torch.isfinite(y[[0, 1, 2, 5]]).all()
+
+
+def test_layer_norm_of_no_rows():
+    w = torch.ones(48, device="cuda")
+    x = torch.empty(0, 48, device="cuda")
+    y, h, mean, rstd = ops.layer_norm(x, w, w)
+    assert y.shape == (0, 48) and mean.shape == (0,)
+    dx, _, dw, db = ops.layer_norm_backward(x, x, mean, rstd, w)
+    assert dx.shape == (0, 48) and not dw.any() and not db.any()
+
+
+def test_layer_norm_in_three_dimensions_and_twice_the_same():
+    x = torch.randn(4, 50, 96, device="cuda", dtype=BF16)
+    w = torch.randn(96, device="cuda")
+    y, h, mean, rstd = ops.layer_norm(x, w, None, residual=x, p=0.1, seed=1)
+    flat = ops.layer_norm(x.view(200, 96), w, None, residual=x.view(200, 96), p=0.1, seed=1)
+    assert y.shape == x.shape and mean.shape == (4, 50)
+    assert torch.equal(y.view(200, 96), flat[0]) and torch.equal(h.view(200, 96), flat[1])
+    a = ops.layer_norm_backward(y, h, mean, rstd, w, p=0.1, seed=1)
+    b = ops.layer_norm_backward(y, h, mean, rstd, w, p=0.1, seed=1)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+# ---------------------------------------------------------------------------
+# policy loss
+# ---------------------------------------------------------------------------
+
+
+def policy_inputs(tokens, vocab, dtype, pad, masked, seed):
+    g = gen(seed)
+    z = rows_of(g, tokens, vocab, pad, F32) * 2
+    targets = torch.randint(vocab, (tokens,), generator=g, device="cuda")
+    full = torch.empty(tokens, vocab + pad, dtype=dtype, device="cuda").fill_(float("nan"))
+    full[:, :vocab] = z.to(dtype)
+    z = full[:, :vocab]
+    logp = torch.log_softmax(z.float(), 1).gather(1, targets[:, None])[:, 0]
+    old = logp + 0.3 * torch.randn(tokens, generator=g, device="cuda")
+    r = logp + 0.3 * torch.randn(tokens, generator=g, device="cuda")
+    adv = torch.randn(tokens, generator=g, device="cuda")
+    w = torch.rand(tokens, generator=g, device="cuda") + 0.5
+    off = torch.rand(tokens, generator=g, device="cuda") < masked
+    w[off], targets[off] = 0.0, -100
+    for t in (old, r, adv):
+        t[off] = float("nan")
+    z[off] = float("nan")
+    return z, targets, old, r, adv, w
+
+
+def policy_bounds(z, targets, old, r, adv, w, lo, hi, kl):
+    """(want, bounds of loss, logp, terms, gradient).  logp's error: the sum of
+    exponentials is relative 2^-21 off (exponential 2 ulp, its argument rounded
+    twice at magnitude <= 32, chains of additions between positive numbers),
+    the logarithm and two subtractions round at its magnitude."""
+    loss, logp, terms, grad = ref.policy(z, targets, old, r, adv, w, lo, hi, kl)
+    on = w != 0
+    # every exponential: argument error 2 * 32 * 2^-24 relative, 2 ulp; chain 300
+    sum_rel = (64 + 4 + 300) * E
+    dlp = torch.where(on, sum_rel + 4 * E * (logp.abs() + 32), 0.0)
+    if old is None:
+        return (loss, logp, terms, grad), dlp
+    ratio = torch.where(on, torch.exp(logp - old.double()), 0.0)
+    er = torch.where(on, torch.exp(r.double() - logp), 0.0) if r is not None else torch.zeros_like(ratio)
+    # a term's slope in logp is |s| <= w (ratio |A| + kl (1 + exp(ref - logp))); its slope's slope the same size
+    steep = torch.where(on, w.double() * (ratio * adv.double().abs() + kl * (1 + er)), 0.0)
+    dterm = steep * (dlp + 16 * E) * 1.1 + 4 * E * terms.abs()
+    s = steep * (dlp + 16 * E) * 1.1
+    p = torch.where(on[:, None], torch.softmax(torch.where(on[:, None], z.double(), 0.0), 1), 0.0)
+    onehot = torch.zeros_like(p).scatter_(1, targets.clamp(min=0)[:, None], 1.0)
+    dgrad = s[:, None] * (p + onehot) + steep[:, None] * p * (sum_rel + 70 * E)
+    return (loss, logp, terms, grad), dlp, dterm, dgrad
+
+
+@pytest.mark.parametrize("tokens,vocab,dtype,pad,masked", [
+    (1, 1, F32, 0, 0.0), (1, 131072, BF16, 0, 0.0), (3, 7, F32, 2, 0.3), (17, 257, F16, 0, 0.5),
+    (64, 1024, BF16, 0, 0.2), (64, 1024, BF16, 8, 0.2), (9, 32768, F32, 0, 0.0), (5, 50021, BF16, 0, 0.2),
+    (33, 4099, F32, 1, 0.2), (2, 151001, F32, 0, 0.0), (700, 600, F16, 0, 0.1), (4, 260000, F32, 0, 0.3)])
+def test_policy_loss(tokens, vocab, dtype, pad, masked):
+    z, targets, old, r, adv, w = policy_inputs(tokens, vocab, dtype, pad, masked, tokens + vocab)
+    lo, hi, kl = 0.2, 0.3, 0.1
+    f = np.float32
+    (loss, logp, terms, grad), dlp, dterm, dgrad = policy_bounds(
+        z, targets, old, r, adv, w, float(f(lo)), float(f(hi)), float(f(kl)))
+    got = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=lo, clip_high=hi, kl_coef=kl)
+    near(got[1], logp, dlp, "logp")
+    # a ratio within rounding of a clip bound may fall on either side: those tokens' gradients are left out
+    ratio = torch.exp(logp - old.double())
+    edge = ((ratio - (1 - lo)).abs() < 1e-5) | ((ratio - (1 + hi)).abs() < 1e-5)
+    near(got[2][~edge], grad[~edge], (dgrad + U[dtype] * grad.abs())[~edge] * 1.01 + TINY[dtype], "dlogits")
+    assert abs(got[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item()) + 1e-30
+    again = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=lo, clip_high=hi, kl_coef=kl)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    only = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=lo, clip_high=hi, kl_coef=kl, grad=False)
+    assert only[2] is None and abs(only[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item()) + 1e-30
+    near(ops.token_logprobs(z, targets, weights=w), logp, dlp, "token_logprobs")
+    if masked == 0:
+        near(ops.token_logprobs(z, targets), logp, dlp, "token_logprobs without weights")
+    doubled = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=lo, clip_high=hi, kl_coef=kl,
+                              grad_scale=4.0)[2]
+    near(doubled[~edge], 4 * grad[~edge], 4 * (dgrad + U[dtype] * grad.abs())[~edge] * 1.01 + 4 * TINY[dtype], "scaled")
+
+
+def test_policy_loss_in_place_and_without_reference():
+    z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
+    want = ops.policy_loss(z, targets, old, adv, w)
+    own = z.clone()
+    got = ops.policy_loss(own, targets, old, adv, w, out=own)
+    assert got[2] is own and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_policy_loss_special_rows():
+    """Masked vocabulary entries (-inf), the type's lowest value, an empty
+    distribution, targets outside the vocabulary, infinite logits: as the
+    formula has it, each in its own row."""
+    lowest = torch.finfo(F32).min
+    z = torch.zeros(8, 40, device="cuda")
+    z[0, 5:] = float("-inf")
+    z[1, 5:] = lowest
+    z[2] = float("-inf")
+    z[3, 3] = float("inf")
+    z[4, 3] = float("nan")
+    z[5, :35] = float("-inf")
+    z[7] = lowest
+    targets = torch.tensor([2, 2, 2, 2, 2, 39, 40, 1], device="cuda")
+    one = torch.ones(8, device="cuda")
+    loss, logp, d = ops.policy_loss(z, targets, -one, one, one, ref_logp=-one, kl_coef=0.1)
+    nan = torch.tensor([False, False, True, True, True, False, True, False], device="cuda")
+    assert torch.equal(torch.isnan(logp), nan) and torch.isnan(loss)
+    assert torch.isnan(d[nan]).all() and torch.isfinite(d[~nan]).all()
+    five = float(np.log(5.0))
+    assert (logp[[0, 1, 5]] + five).abs().max().item() <= 4 * E * five + 8 * E
+    assert abs(logp[7].item() + np.log(40.0)) <= 16 * E
+    assert not d[0, 5:].any() and not d[1, 5:].any() and not d[5, :35].any()
+    keep = torch.where(nan, 0.0, one)
+    loss, logp, d = ops.policy_loss(z, targets, -one, one, keep, ref_logp=-one, kl_coef=0.1)
+    assert torch.isfinite(loss) and not d[nan].any() and not logp[nan].any()
+
+
+def test_policy_gradient_against_differences():
+    """d(loss) along random directions, float32 logits, unclipped tokens only
+    (ratio 1, 20% from a bound): step 2^-7 over vectors of length 1.  Rounding:
+    a loss near 1 carries 2^-22, over 2 step: 1.5e-5; truncation step^2 / 6
+    times a third derivative below 8: 8e-5."""
+    z, targets, old, r, adv, w = policy_inputs(6, 50, F32, 0, 0.0, 4)
+    old = ops.token_logprobs(z, targets)
+    w = w / w.sum()
+    kw = dict(ref_logp=r, kl_coef=0.5)
+    d = ops.policy_loss(z, targets, old, adv, w, **kw)[2]
+    for seed in range(4):
+        v = torch.randn(z.shape, generator=gen(seed), device="cuda")
+        v, step = v / v.norm(), 2.0 ** -7
+        up = ops.policy_loss(z + step * v, targets, old, adv, w, grad=False, **kw)[0].item()
+        down = ops.policy_loss(z - step * v, targets, old, adv, w, grad=False, **kw)[0].item()
+        assert abs((up - down) / (2 * step) - (d.double() * v.double()).sum().item()) <= 1.5e-4
+
+
+def test_policy_loss_of_no_tokens():
+    z = torch.empty(0, 16, device="cuda")
+    e = torch.empty(0, device="cuda")
+    loss, logp, d = ops.policy_loss(z, e.long(), e, e, e)
+    assert loss.item() == 0 and logp.shape == (0,) and d.shape == (0, 16)
+
+
+def test_policy_loss_past_2_31_logits():
+    """20000 x 131072 bfloat16 logits (2.6e9): the last rows, by themselves."""
+    tokens, vocab = 20000, 131072
+    z = torch.zeros(tokens, vocab, dtype=BF16, device="cuda")
+    z[-2:] = torch.randn(2, vocab, generator=gen(2), device="cuda").to(BF16)
+    targets = torch.full((tokens,), vocab - 1, device="cuda")
+    one = torch.ones(tokens, device="cuda")
+    old, w = -11.5 * one, one / tokens
+    _, logp, d = ops.policy_loss(z, targets, old, one, w, out=None)
+    tail = ops.policy_loss(z[-2:], targets[-2:], old[-2:], one[-2:], w[-2:])
+    # two sums of the same row, each within 400 2^-24 of it (policy_bounds), and their roundings
+    near(logp[-2:], tail[1], torch.full((2,), 1000 * E, device="cuda"))
+    near(d[-2:], tail[2], (2 * U[BF16] + 1000 * E) * tail[2].double().abs() * 1.01 + TINY[BF16])
+    assert abs(logp[0].item() + np.log(vocab)) <= 1e-5
+    del z, d
+    torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# 8-bit matrices
+# ---------------------------------------------------------------------------
+
+
+def spread(g, rows, cols, dtype):
+    """Values over many magnitudes, so that blocks differ in scale."""
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    x = x * torch.exp2(torch.randint(-10, 4, (rows, 1), generator=g, device="cuda").float())
+    return x.to(dtype)
+
+
+def check_quantized(m, x, block_rows, dtype):
+    q, scale = ref.quantize(x.double().cpu().numpy(), block_rows, dtype)
+    assert np.array_equal(m.scale.cpu().numpy(), scale)
+    got = m.data.float().double().cpu().numpy()
+    assert np.array_equal(got, q, equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("rows,cols,dtype,block_rows,pad", [
+    (1, 1, F32, 1, 0), (3, 130, BF16, 1, 0), (128, 128, F16, 128, 0), (129, 257, F32, 128, 0), (200, 384, BF16, 1, 8),
+    (65, 127, F16, 1, 1), (300, 136, F32, 128, 4), (1, 2048, BF16, 1, 0), (257, 16, BF16, 128, 0)])
+def test_quantize(fmt, rows, cols, dtype, block_rows, pad):
+    x = spread(gen(rows + cols), rows, cols + pad, dtype)[:, :cols]
+    q, t = ops.fp8_quantize(x, block_rows=block_rows, transposed=True, dtype=fmt)
+    check_quantized(q, x, block_rows, fmt)
+    check_quantized(t, x.t(), block_rows, fmt)
+    only, none = ops.fp8_quantize(x, block_rows=block_rows, dtype=fmt)
+    assert none is None and torch.equal(only.data.view(torch.uint8), q.data.view(torch.uint8))
+    none, only = ops.fp8_quantize(x, block_rows=block_rows, rows=False, transposed=True, dtype=fmt)
+    assert none is None and torch.equal(only.data.view(torch.uint8), t.data.view(torch.uint8))
+
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_special_values(fmt, block_rows):
+    """Blocks of zeros, subnormal and largest floats, values on and beside the
+    scales' steps, NaN and infinities in their own places."""
+    x = torch.randn(256, 256, generator=gen(1), device="cuda")
+    x[:128, :128] = 0.0
+    x[:128, 128:] *= 1e-42
+    x[130, 3], x[131, 200], x[132, 7] = float("nan"), float("inf"), float("-inf")
+    x[140, :] = 448.0
+    x[141, :] = float(np.nextafter(np.float32(448), np.float32(1e9)))
+    x[142, :] = 57344.0
+    x[143, :] = 3.4028234663852886e38
+    x[144, :] = -0.0
+    q, t = ops.fp8_quantize(x, block_rows=block_rows, transposed=True, dtype=fmt)
+    check_quantized(q, x, block_rows, fmt)
+    check_quantized(t, x.t(), block_rows, fmt)
+
+
+PRODUCT = [(1, 1, 1), (1, 6144, 2048), (3, 130, 16), (128, 128, 128), (127, 129, 131), (200, 300, 4096), (64, 2048, 500),
+           (513, 40, 1030), (16, 16, 20000), (1, 128, 70000), (300, 520, 129), (40, 1000, 640)]
+
+
+def product_bound(a, b, K):
+    """Each stretch of K is summed on the tensor cores, whose additions may
+    truncate (2^-23) and align up to 32 products at a time; stretches join in
+    float32."""
+    mag = a.abs() @ b.abs().t()
+    return (64 + K / 512) * 2 * E * mag
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCT)
+@pytest.mark.parametrize("ra,rb,fa,fb", [(1, 128, E4, E4), (1, 1, E5, E4), (128, 128, E4, E5), (128, 1, E5, E5)])
+def test_product(M, N, K, ra, rb, fa, fb):
+    g = gen(M + N + K)
+    a = ops.fp8_quantize(spread(g, M, K, F32), block_rows=ra, dtype=fa)[0]
+    b = ops.fp8_quantize(spread(g, N, K, F32), block_rows=rb, dtype=fb)[0]
+    va, vb = ref.values(a), ref.values(b)
+    want, bound = va @ vb.t(), product_bound(va, vb, K)
+    got = ops.fp8_matmul(a, b)
+    near(got, want, bound, "float32")
+    assert torch.equal(got, ops.fp8_matmul(a, b))
+    if ra == 1 and rb == 128:
+        for dtype in (F16, BF16):
+            small = want.abs() <= 6e4
+            near(torch.where(small, ops.fp8_matmul(a, b, dtype=dtype).double(), 0.0), torch.where(small, want, 0.0),
+                 bound + (want.abs() + bound) * U[dtype] * 1.01 + TINY[dtype], str(dtype))
+        c = torch.randn(M, N + 3, generator=g, device="cuda")
+        before = c.clone()
+        out = c[:, :N]
+        ops.fp8_matmul(a, b, out=out, accumulate=True)
+        near(out, before[:, :N].double() + want, bound + 2 * E * (want.abs() + before[:, :N].abs()), "accumulated")
+        assert torch.equal(c[:, N:], before[:, N:])
+    assert ops.status() == B.ROT_OK
+
+
+def test_product_scales_reach_their_ends():
+    """Scales 2^-127 .. 2^127 whose products stay in range, and a NaN scale,
+    which reaches its row or columns alone."""
+    a = ops.fp8_quantize(torch.randn(200, 300, generator=gen(1), device="cuda"))[0]
+    b = ops.fp8_quantize(torch.randn(260, 300, generator=gen(2), device="cuda"), block_rows=128)[0]
+    a.scale.fill_(0)     # 2^-127
+    b.scale.fill_(254)   # 2^127
+    near(ops.fp8_matmul(a, b), ref.values(a) @ ref.values(b).t(), product_bound(ref.values(a), ref.values(b), 300))
+    a.scale.fill_(127)
+    b.scale.fill_(127)
+    a.scale[1, 7] = 255
+    b.scale[2, 1] = 255
+    got = ops.fp8_matmul(a, b)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[7] = True
+    nan[:, 128:256] = True
+    assert torch.equal(torch.isnan(got), nan)
+
+
+def test_product_nan_elements_stay_in_their_rows():
+    x = torch.randn(140, 200, generator=gen(3), device="cuda")
+    x[130, 150] = float("nan")
+    w = torch.randn(70, 200, generator=gen(4), device="cuda")
+    w[3, 199] = float("inf")
+    got = ops.fp8_matmul(ops.fp8_quantize(x)[0], ops.fp8_quantize(w, block_rows=128)[0])
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[130] = True
+    nan[:, 3] = True
+    assert torch.equal(torch.isnan(got), nan)
+
+
+def test_product_does_not_read_past_its_columns():
+    """The bytes between the columns and the next row are never part of the sums."""
+    a = ops.fp8_quantize(torch.randn(130, 37, generator=gen(5), device="cuda"))[0]
+    full = torch.full((130, 48), 0x7F, dtype=torch.uint8, device="cuda")  # NaN
+    full[:, :37] = a.data.view(torch.uint8)
+    dirty = ops.Fp8Matrix(full.view(E4)[:, :37], a.scale, 1)
+    assert torch.equal(ops.fp8_matmul(dirty, dirty), ops.fp8_matmul(a, a))
+
+
+def test_product_of_nothing():
+    e = ops.fp8_quantize(torch.empty(0, 64, device="cuda"))[0]
+    b = ops.fp8_quantize(torch.randn(10, 64, device="cuda"))[0]
+    assert ops.fp8_matmul(e, b).shape == (0, 10)
+    z = ops.fp8_quantize(torch.empty(10, 0, device="cuda"))[0]
+    assert not ops.fp8_matmul(z, z).any()
+
+
+@pytest.mark.parametrize("tokens,inner,outer,dtype", [(1, 130, 70, BF16), (257, 384, 500, F16), (1030, 256, 129, BF16)])
+def test_linear(tokens, inner, outer, dtype):
+    g = gen(tokens)
+    x = torch.randn(tokens, inner, generator=g, device="cuda").to(dtype)
+    w = torch.randn(outer, inner, generator=g, device="cuda") * 0.02
+    dy = (torch.randn(tokens, outer, generator=g, device="cuda") * 1e-2).to(dtype)
+    q, t = ops.fp8_quantize(w, block_rows=128, transposed=True)
+    y = ops.fp8_linear(x.view(1, tokens, inner), q)
+    assert y.shape == (1, tokens, outer)
+    vx, vw = ref.values(ops.fp8_quantize(x)[0]), ref.values(q)
+    want, bound = vx @ vw.t(), product_bound(vx, vw, inner)
+    near(y[0], want, bound + (want.abs() + bound) * U[dtype] * 1.01 + TINY[dtype], "y")
+    # 8 bits carry 2^-4 of each factor, at random over `inner` terms: an eighth of the result's size
+    true = x.double() @ w.double().t()
+    assert (y[0].double() - true).norm() <= 0.125 * true.norm()
+    dx, dw = ops.fp8_linear_backward(dy, x, t)
+    dq, dqt = ops.fp8_quantize(dy, transposed=True)
+    vd, vdt, vxt = ref.values(dq), ref.values(dqt), ref.values(ops.fp8_quantize(x, rows=False, transposed=True)[1])
+    want, bound = vd @ ref.values(t).t(), product_bound(vd, ref.values(t), outer)
+    near(dx, want, bound + (want.abs() + bound) * U[dtype] * 1.01 + TINY[dtype], "dx")
+    want, bound = vdt @ vxt.t(), product_bound(vdt, vxt, tokens)
+    near(dw, want, bound, "dw")
+    twice = dw.clone()
+    ops.fp8_linear_backward(dy, x, t, dw=twice, accumulate=True)
+    near(twice, 2 * want, 2 * bound + 4 * E * want.abs(), "dw accumulated")
+
+
+# ---------------------------------------------------------------------------
+# refusals of the Python entry points
+# ---------------------------------------------------------------------------
+
+
+def test_refusals():
+    x = torch.randn(8, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    v = torch.zeros(8, device="cuda")
+    t = torch.zeros(8, dtype=torch.int64, device="cuda")
+    q, qt = ops.fp8_quantize(x, transposed=True)
+    raw = torch.zeros(8 * 64 + 16, dtype=torch.uint8, device="cuda").view(E4)
+    for call in (
+            lambda: ops.dropout(x.double(), 0.1, 0), lambda: ops.dropout(x.t(), 0.1, 0),
+            lambda: ops.dropout(x, 1.5, 0), lambda: ops.dropout(x, 0.1, -1), lambda: ops.dropout(x, 0.1, 1 << 64),
+            lambda: ops.dropout(x, 0.1, 0, residual=x[:4]), lambda: ops.dropout(x, 0.1, 0, residual=x.half()),
+            lambda: ops.dropout(w.expand(8, 64), 0.1, 0), lambda: ops.dropout(x, 0.1, 0, out=x[:4]),
+            lambda: ops.layer_norm(x, w[:32]), lambda: ops.layer_norm(x, w.half()),
+            lambda: ops.layer_norm(x, w, w.half()), lambda: ops.layer_norm(x, w, eps=-1.0),
+            lambda: ops.layer_norm(x, None), lambda: ops.layer_norm(x, w.cpu()),
+            lambda: ops.layer_norm_backward(x, x, v[:4], v, w), lambda: ops.layer_norm_backward(x, x.half(), v, v, w),
+            lambda: ops.token_logprobs(x, t.int()), lambda: ops.token_logprobs(x, t[:4]),
+            lambda: ops.policy_loss(x, t, v, v, None), lambda: ops.policy_loss(x, t, v, v, v, kl_coef=0.1),
+            lambda: ops.policy_loss(x, t, v.double(), v, v), lambda: ops.policy_loss(x, t, v, v, v, out=x.half()),
+            lambda: ops.fp8_quantize(x, block_rows=64), lambda: ops.fp8_quantize(x, dtype=torch.uint8),
+            lambda: ops.fp8_quantize(x, rows=False), lambda: ops.fp8_matmul(q, qt),
+            lambda: ops.fp8_matmul(q, ops.Fp8Matrix(q.data, q.scale[:, :4], 1)),
+            lambda: ops.fp8_matmul(q, ops.Fp8Matrix(raw[1:513].view(8, 64), q.scale, 1)),
+            lambda: ops.fp8_matmul(q, ops.Fp8Matrix(raw[:8 * 65].view(8, 65)[:, :64], q.scale, 1)),
+            lambda: ops.fp8_matmul(q, q, accumulate=True), lambda: ops.fp8_matmul(q, q, dtype=torch.int8),
+            lambda: ops.fp8_matmul(q, q, out=torch.empty(8, 9, device="cuda")),
+            lambda: ops.fp8_linear(x, w), lambda: ops.fp8_linear_backward(x, x[:4], qt)):
+        with pytest.raises((ValueError, B.RotError)):
+            call()
