@@ -32,11 +32,11 @@ inline bool float_type(int32_t t) {
 }
 inline int type_bytes(int32_t t) { return t == ROT_TYPE_F32 ? 4 : t <= ROT_TYPE_BF16 ? 2 : 1; }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+__host__ __device__ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Whether 16-byte accesses reach every row's elements: base and row pitch are
 // multiples of 16 bytes (a null matrix does not matter).
-inline bool rows16(const void* p, int64_t ld, int es) {
+__host__ __device__ inline bool rows16(const void* p, int64_t ld, int es) {
   return !p || (aligned16(p) && (ld * es) % 16 == 0);
 }
 

@@ -1,10 +1,11 @@
 // 8-bit matrices with power-of-two block scales (include/rot_ops.h):
-// quantisation and the product.
+// quantisation, and the product's entry point (its kernels: ops_fp8_gemm.cu).
 #include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "ops_common.cuh"
+#include "ops_fp8.h"
 #include "profile.h"
 
 namespace rot {
@@ -182,81 +183,6 @@ int launch_quantize(const Quant& a, cudaStream_t s) {
   return launched();
 }
 
-// ---------------------------------------------------------------------------
-// product
-// ---------------------------------------------------------------------------
-
-struct Prod {
-  const uint8_t *a, *b, *sa, *sb;
-  void* c;
-  int64_t lda, ldb, ldsa, ldsb, ldc;
-  int M, N, K, ctype, accumulate;
-  int a5, b5, ash, bsh;  // formats; scale index = row >> sh
-};
-
-__device__ __forceinline__ float f8_value(uint8_t v, bool e5m2) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, e5m2 ? __NV_E5M2 : __NV_E4M3)));
-}
-__device__ __forceinline__ float scale_value(uint8_t b) {
-  return b == 255 ? NAN : b == 0 ? __uint_as_float(1u << 22) : __uint_as_float((uint32_t)b << 23);
-}
-
-// 64 x 64 of C per CTA, 4 x 4 per thread, K in steps of 16 through shared
-// memory; each block of 128 is summed on its own and joins the total under
-// its two scales.
-__global__ void __launch_bounds__(256) product_kernel(const Prod p) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {}, blk[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += 16) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-      const int r = i / 16, k = i % 16;
-      sa[k][r] = (m0 + r < p.M && k0 + k < p.K) ? f8_value(p.a[(m0 + r) * p.lda + k0 + k], p.a5) : 0.f;
-      sb[k][r] = (n0 + r < p.N && k0 + k < p.K) ? f8_value(p.b[(n0 + r) * p.ldb + k0 + k], p.b5) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) blk[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-    __syncthreads();
-    if ((k0 + 16) % 128 == 0 || k0 + 16 >= p.K) {
-      const int kb = k0 / 128;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty + 16 * i;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + tx + 16 * j;
-          if (m < p.M && n < p.N)
-            acc[i][j] += blk[i][j] * scale_value(p.sa[kb * p.ldsa + (m >> p.ash)]) *
-                         scale_value(p.sb[kb * p.ldsb + (n >> p.bsh)]);
-          blk[i][j] = 0.f;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.M || n >= p.N) continue;
-      const int64_t o = m * p.ldc + n;
-      if (p.ctype == ROT_TYPE_F32) {
-        float* c = (float*)p.c + o;
-        *c = p.accumulate ? *c + acc[i][j] : acc[i][j];
-      } else if (p.ctype == ROT_TYPE_F16) {
-        ((__half*)p.c)[o] = __float2half_rn(acc[i][j]);
-      } else {
-        ((__nv_bfloat16*)p.c)[o] = __float2bfloat16_rn(acc[i][j]);
-      }
-    }
-}
-
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 constexpr int64_t kMost = (int64_t(1) << 31) - 256;
 
@@ -302,8 +228,7 @@ int rot_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int
 }
 
 uint64_t rot_fp8_gemm_work_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M, (void)N, (void)K;
-  return 0;
+  return fp8_work_bytes(M, N, K);
 }
 
 int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
@@ -324,15 +249,15 @@ int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, in
   if (dev != ROT_OK) return dev;
   Prod p = {(const uint8_t*)a, (const uint8_t*)b, a_scale, b_scale, c, lda, ldb, a_lds, b_lds, ldc,
             (int)M, (int)N, (int)K, ctype, accumulate, a_format == ROT_TYPE_E5M2,
-            b_format == ROT_TYPE_E5M2, a_block_rows == 1 ? 0 : 7, b_block_rows == 1 ? 0 : 7};
-  if (up(M, 64) > 65535) return ROT_EINVAL;
-  (void)status;
+            b_format == ROT_TYPE_E5M2, a_block_rows == 1 ? 0 : 7, b_block_rows == 1 ? 0 : 7,
+            static_cast<float*>(work)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return guarded([&] {
-    ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * M * (double)N * K, s);
-    product_kernel<<<dim3((unsigned)up(N, 64), (unsigned)up(M, 64)), 256, 0, s>>>(p);
-    return launched();
-  });
+  if (K == 0)  // all bits zero is 0 in every type
+    return cudaMemset2DAsync(c, ldc * type_bytes(ctype), 0, N * type_bytes(ctype), M, s) ==
+                   cudaSuccess
+               ? ROT_OK
+               : ROT_ECUDA;
+  return guarded([&] { return fp8_product(p, reinterpret_cast<int*>(status), s); });
 }
 
 }  // extern "C"

@@ -1,0 +1,458 @@
+// C = A B^T of 8-bit matrices with power-of-two block scales (rot_fp8_gemm) on
+// the tensor cores: tcgen05 kind::mxf8f6f4, which multiplies each row's 32
+// elements of K by a scale of one byte (UE8M0) as it reads them, so the scales
+// cost nothing in the sums.
+//
+// Bound: the 8-bit tensor rate for large products.  A persistent kernel, one
+// CTA per SM, walks the (tile, share of K) units of C.  Per CTA:
+//   warp 0      one thread issues TMA loads of A (128 x 128 bytes) and B
+//               (192 x 128 bytes) blocks into a five-deep ring
+//   warp 1      allocates TMEM; one thread copies a block's scales to TMEM
+//               and issues its four MMAs of 128 x 192 x 32
+//   warp 2      reads the blocks' scales and lays them out for that copy
+//   warps 4-11  epilogue: each takes 32 rows x 96 columns
+// 128 x 192 is the widest tile whose accumulator fits TMEM twice next to the
+// scales, so that the epilogue overlaps the next tile's MMAs.
+//
+// Accuracy: the tensor cores truncate each partial sum they add to an
+// accumulator, an error that grows with K.  An accumulator therefore takes at
+// most 512 elements of K (16 additions); the epilogue adds these stretches in
+// float32 registers.
+//
+// Few tiles: K is split over units whose float32 parts go to the workspace and
+// are joined in a fixed order by a second kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "ops_common.cuh"
+#include "ops_fp8.h"
+#include "profile.h"
+#include "tc_ptx.cuh"
+
+namespace rot {
+namespace ops {
+namespace {
+
+constexpr int BM = 128, BN = 192, BK = 128;
+constexpr int kStages = 5;
+constexpr int kABytes = BM * BK, kBBytes = BN * BK, kStageBytes = kABytes + kBBytes;
+constexpr int kScaleBytes = 512 + 1024;  // per stage: A's 128 rows, B's 192 (of 256)
+constexpr int kSmem = 1024 + kStages * (kStageBytes + kScaleBytes) + 256;
+static_assert(kSmem <= 232448, "dynamic shared memory above 227 KB");
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8, kEpiCols = BN / 2;
+constexpr int kStretch = 4;  // K blocks an accumulator takes
+constexpr int kScaleCols = 12;  // TMEM columns of a stage's scales: 4 of A, 8 of B
+constexpr int kTmemCols = 512;
+static_assert(2 * BN + kStages * kScaleCols <= kTmemCols, "TMEM");
+
+struct Mx {
+  CUtensorMap a, b;
+  Prod p;
+  int tiles_m, tiles_n, kblocks, splits, per;  // per: K blocks of a unit
+  int64_t units, ldp;
+  int* status;
+  unsigned long long limit_ns;
+};
+
+// Units in order: shares of a tile next to each other, tiles in groups of
+// kGroupM rows of tiles, down a group's columns, so that the CTAs at work at
+// any time share blocks of A and B in L2.
+constexpr int kGroupM = 8;
+
+struct Unit {
+  int m0, n0, k0, k1, split;
+};
+__device__ __forceinline__ Unit unit_of(const Mx& g, int64_t u) {
+  const int64_t tile = u / g.splits;
+  const int per_group = kGroupM * g.tiles_n;
+  const int grp = (int)(tile / per_group), r = (int)(tile - (int64_t)grp * per_group);
+  const int h = min(kGroupM, g.tiles_m - grp * kGroupM);
+  Unit t;
+  t.split = (int)(u - tile * g.splits);
+  t.m0 = (grp * kGroupM + r % h) * BM;
+  t.n0 = r / h * BN;
+  t.k0 = t.split * g.per;
+  t.k1 = min(g.kblocks, t.k0 + g.per);
+  return t;
+}
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  limit_ns = limit_ns > 100000000ull ? limit_ns : 100000000ull;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    if ((it & 63u) == 0u && (ptx::globaltimer_ns() - t0 > limit_ns || it > (1u << 30))) return;
+  }
+}
+
+// 32 columns of one row of C, from column n.
+template <class T>
+__device__ __forceinline__ void store_cols(T* c, const float* acc, int ncol, bool wide,
+                                           bool accumulate) {
+  constexpr int U = 16 / sizeof(T);
+  if (wide && ncol >= 32) {
+#pragma unroll
+    for (int i = 0; i < 32; i += U) {
+      float f[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) f[k] = acc[i + k];
+      if (accumulate) {
+        float o[U];
+        load_run(c + i, o);
+#pragma unroll
+        for (int k = 0; k < U; ++k) f[k] += o[k];
+      }
+      store_run(c + i, f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < ncol) c[i] = from_f32<T>(accumulate ? to_f32(c[i]) + acc[i] : acc[i]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Mx g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* scales = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kStages * kScaleBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = g.limit_ns;
+  const Prod& p = g.p;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 2);  // the loads, the scales
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tfull[a], 1);
+      ptx::mbar_init(&tempty[a], kEpiWarps);
+    }
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ loads
+    ptx::tma_prefetch_desc(&g.a);
+    ptx::tma_prefetch_desc(&g.b);
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const Unit t = unit_of(g, u);
+      for (int kb = t.k0; kb < t.k1; ++kb) {
+        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + stage * kStageBytes;
+        ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
+        ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    for (int s = 0; s < kStages; ++s)
+      if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issue
+    const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const Unit t = unit_of(g, u);
+      for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
+        if (!ptx::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        const int k1 = min(t.k1, kb + kStretch);
+        for (int k = kb; k < k1; ++k) {
+          if (!ptx::mbar_wait(&full[stage], phase, abort_flag, limit)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sc = ptx::smem_u32(scales + stage * kScaleBytes);
+          const uint32_t sfa = tmem + (uint32_t)(2 * BN + stage * kScaleCols), sfb = sfa + 4;
+          ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
+          ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
+          ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
+          const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
+          const uint64_t da = ptx::sw128_kmajor_desc(st);
+          const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
+#pragma unroll
+          for (int i = 0; i < BK / 32; ++i)
+            ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), idesc, sfa, sfb,
+                           (k > kb || i > 0) ? 1u : 0u);
+          ptx::umma_commit(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit(&tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    ptx::umma_commit(done);
+    drain(done, 0, limit);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    // Lane l lays out rows l, 32 + l, 64 + l, .. : four bytes (one for each 32
+    // of the block's K, all the same) for each, which tcgen05.cp puts into
+    // lane l, columns 0, 1, 2, ..  The next stretch's bytes are on their way
+    // while this one's are written.
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const Unit t = unit_of(g, u);
+      for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
+        const int n = min(kStretch, t.k1 - kb);
+        uint32_t va[kStretch][4], vb[kStretch][6];
+#pragma unroll
+        for (int j = 0; j < kStretch; ++j) {
+          if (j < n) {
+            const uint8_t* sa = p.sa + (kb + j) * p.ldsa;
+            const uint8_t* sb = p.sb + (kb + j) * p.ldsb;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int r = t.m0 + 32 * c + lane;
+              va[j][c] = r < p.M ? sa[r >> p.ash] : 127u;
+            }
+#pragma unroll
+            for (int c = 0; c < 6; ++c) {
+              const int r = t.n0 + 32 * c + lane;
+              vb[j][c] = r < p.N ? sb[r >> p.bsh] : 127u;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kStretch; ++j) {
+          if (j < n && ok) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, limit));
+            if (ok) {
+              uint4* s = reinterpret_cast<uint4*>(scales + stage * kScaleBytes);
+              constexpr uint32_t r = 0x01010101u;
+              s[lane] = make_uint4(va[j][0] * r, va[j][1] * r, va[j][2] * r, va[j][3] * r);
+              s[32 + lane] = make_uint4(vb[j][0] * r, vb[j][1] * r, vb[j][2] * r, vb[j][3] * r);
+              s[64 + lane] = make_uint4(vb[j][4] * r, vb[j][5] * r, 127u * r, 127u * r);
+              ptx::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(&full[stage]);
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+          }
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kEpiCols);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const Unit t = unit_of(g, u);
+      float sum[kEpiCols];
+#pragma unroll
+      for (int c = 0; c < kEpiCols; ++c) sum[c] = 0.f;
+      for (int kb = t.k0; kb < t.k1; kb += kStretch) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&tfull[acc], acc_phase, abort_flag, limit))) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kEpiCols; c += 32) {
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(lanes + (uint32_t)(acc * BN + c), r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      const int row = t.m0 + quarter * 32 + lane, n0 = t.n0 + half * kEpiCols;
+      if (!ok || row >= p.M) continue;
+#pragma unroll
+      for (int c = 0; c < kEpiCols; c += 32) {
+        const int n = n0 + c, ncol = p.N - n;
+        if (ncol <= 0) break;
+        if (g.splits > 1) {
+          store_cols(p.part + ((int64_t)t.split * p.M + row) * g.ldp + n, sum + c, ncol, true, false);
+        } else {
+          const int64_t o = (int64_t)row * p.ldc + n;
+          if (p.ctype == ROT_TYPE_F32)
+            store_cols((float*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 4), p.accumulate);
+          else if (p.ctype == ROT_TYPE_F16)
+            store_cols((__half*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 2), false);
+          else
+            store_cols((__nv_bfloat16*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 2), false);
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag && g.status) atomicExch(g.status, ROT_ETIMEOUT);
+}
+
+// C from the parts, added in order of K.
+__global__ void __launch_bounds__(256) fp8_join_kernel(const Prod p, int splits, int64_t ldp) {
+  const int64_t total = (int64_t)p.M * p.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / p.N, n = i - m * p.N;
+    float sum = 0.f;
+    for (int s = 0; s < splits; ++s) sum += p.part[((int64_t)s * p.M + m) * ldp + n];
+    const int64_t o = m * p.ldc + n;
+    if (p.ctype == ROT_TYPE_F32)
+      ((float*)p.c)[o] = p.accumulate ? ((float*)p.c)[o] + sum : sum;
+    else if (p.ctype == ROT_TYPE_F16)
+      ((__half*)p.c)[o] = __float2half_rn(sum);
+    else
+      ((__nv_bfloat16*)p.c)[o] = __float2bfloat16_rn(sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Shares of K for a product of `tiles` tiles: enough units for the 152 SMs
+// while each keeps at least one stretch of K (the workspace's size must not
+// depend on the GPU at hand).
+constexpr int kSms = 152;
+
+struct Shape {
+  int64_t tiles_m, tiles_n, kblocks, splits, per, ldp;
+};
+Shape shape_of(int64_t M, int64_t N, int64_t K) {
+  Shape s;
+  s.tiles_m = (M + BM - 1) / BM;
+  s.tiles_n = (N + BN - 1) / BN;
+  s.kblocks = (K + BK - 1) / BK;
+  const int64_t tiles = s.tiles_m * s.tiles_n;
+  const int64_t most = (s.kblocks + kStretch - 1) / kStretch;
+  const int64_t splits = std::max<int64_t>(1, std::min(most, kSms / std::max<int64_t>(tiles, 1)));
+  // whole stretches per share
+  s.per = (most + splits - 1) / splits * kStretch;
+  s.splits = (s.kblocks + s.per - 1) / s.per;
+  s.ldp = (N + 3) / 4 * 4;
+  return s;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// rows x K bytes at a pitch of ld, boxes of box_rows x 128 with the 128-byte
+// swizzle; bytes past K or past the last row read as 0.
+int encode(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, int64_t ld,
+           int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base),
+                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ROT_OK : ROT_EINVAL;
+}
+
+}  // namespace
+
+uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  const Shape s = shape_of(M, N, K);
+  return s.splits > 1 ? align256(4ull * s.splits * M * s.ldp) : 0;
+}
+
+int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr != cudaSuccess || !encoder()) return ROT_ECUDA;
+  const Shape s = shape_of(p.M, p.N, p.K);
+  Mx g;
+  int e = encode(&g.a, p.a, p.M, p.K, p.lda, BM);
+  if (e == ROT_OK) e = encode(&g.b, p.b, p.N, p.K, p.ldb, BN);
+  if (e != ROT_OK) return e;
+  g.p = p;
+  g.tiles_m = (int)s.tiles_m, g.tiles_n = (int)s.tiles_n, g.kblocks = (int)s.kblocks;
+  g.splits = (int)s.splits, g.per = (int)s.per, g.ldp = s.ldp;
+  g.units = s.tiles_m * s.tiles_n * s.splits;
+  g.status = status;
+  g.limit_ns = g_wait_limit_ns;
+  {
+    ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * p.M * (double)p.N * p.K, stream);
+    fp8_gemm_kernel<<<(unsigned)std::min<int64_t>(g.units, sm_count()), kThreads, kSmem, stream>>>(g);
+    e = launched();
+  }
+  if (e != ROT_OK || s.splits == 1) return e;
+  ProfScope prof(ROT_PROF_ELEMENTWISE, 4.0 * (s.splits + 1) * p.M * (double)p.N, stream);
+  const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+  fp8_join_kernel<<<(unsigned)std::min<int64_t>(blocks, 8ll * sm_count()), 256, 0, stream>>>(
+      p, (int)s.splits, s.ldp);
+  return launched();
+}
+
+}  // namespace ops
+}  // namespace rot
