@@ -90,37 +90,36 @@ __device__ __forceinline__ void store_run(T* p, const float (&f)[U]) {
   *reinterpret_cast<Run<T, U>*>(p) = r;
 }
 
-// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
-// easy as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64 products.
+// Dropout of one call: whether it drops at all, 1 / (1 - p), and what the
+// generator takes.  An element is kept where its word is above `bar`, round(p
+// 2^32) - 1 (p = 1: above 2^32 - 1, which no word is).  Philox4x32-10 (Salmon,
+// Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011)
+// is ten rounds of two 32 x 32 -> 64 products; the rounds' keys depend on the
+// seed alone, so the host works them out and the kernels read them as
+// parameters.
+struct Drop {
+  int on = 0;
+  uint32_t bar = 0;
+  float scale = 1.f;
+  uint32_t offset[2] = {};
+  uint32_t key[10][2] = {};
+};
 struct Words {
   uint32_t w[4];
 };
-__device__ __forceinline__ Words philox(uint64_t counter, uint64_t offset, uint64_t seed) {
+__device__ __forceinline__ Words philox(const Drop& d, uint64_t counter) {
   uint32_t c0 = (uint32_t)counter, c1 = (uint32_t)(counter >> 32);
-  uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
-  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+  uint32_t c2 = d.offset[0], c3 = d.offset[1];
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[r][0];
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[r][1];
     c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return {{c0, c1, c2, c3}};
 }
-
-// Dropout of one call: whether it drops at all, the bar round(p 2^32) and
-// 1 / (1 - p).  p = 1: `bar` would be 2^32, every word is below it.
-struct Drop {
-  int on = 0;
-  int all = 0;
-  uint32_t bar = 0;
-  float scale = 1.f;
-  uint64_t seed = 0, offset = 0;
-};
 Drop make_drop(double p, uint64_t seed, uint64_t offset);
 
 // f[k] (elements i0 .. i0 + U - 1 of the row-major order) <- dropped values.
@@ -131,18 +130,18 @@ __device__ __forceinline__ void drop_run(const Drop& d, uint64_t i0, float (&f)[
   if constexpr (U % 4 == 0) {
 #pragma unroll
     for (int q = 0; q < U / 4; ++q) {
-      const Words w = philox(i0 / 4 + q, d.offset, d.seed);
+      const Words w = philox(d, i0 / 4 + q);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        f[4 * q + k] = (w.w[k] >= d.bar && !d.all) ? __fmul_rn(f[4 * q + k], d.scale) : 0.f;
+        f[4 * q + k] = w.w[k] > d.bar ? __fmul_rn(f[4 * q + k], d.scale) : 0.f;
     }
   } else {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const Words w = philox((i0 + k) / 4, d.offset, d.seed);
+      const Words w = philox(d, (i0 + k) / 4);
       const uint32_t s = (uint32_t)(i0 + k) & 3u;
       const uint32_t word = s == 0 ? w.w[0] : s == 1 ? w.w[1] : s == 2 ? w.w[2] : w.w[3];
-      f[k] = (word >= d.bar && !d.all) ? __fmul_rn(f[k], d.scale) : 0.f;
+      f[k] = word > d.bar ? __fmul_rn(f[k], d.scale) : 0.f;
     }
   }
 }

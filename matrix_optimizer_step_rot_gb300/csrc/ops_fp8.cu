@@ -3,6 +3,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 #include "ops_fp8.h"
@@ -39,135 +40,239 @@ __device__ __forceinline__ float inverse_scale(int byte) {
   return __uint_as_float((uint32_t)(254 - byte) << 23);
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < INFINITY ? a : 0.f;
+// Two values as 8-bit floats, the first in the low byte.
+__device__ __forceinline__ uint32_t pair_f8(float x, float y, bool e5m2) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
 }
 
-// 8 bits of x * inv (at most max in magnitude by choice of inv); NaN and
-// infinities become NaN.
-__device__ __forceinline__ uint32_t to_f8(float x, float inv, bool e5m2) {
-  float v = x * inv;
-  if (!(fabsf(x) < INFINITY)) v = NAN;
-  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+// A thread's 8 x 8 piece as loaded: 16-bit values two to a word (column 2 j in
+// the low half).
+template <class T>
+struct Piece {
+  static constexpr int W = 8 * sizeof(T) / 4;  // words per row
+  uint32_t w[8][W];
+
+  __device__ __forceinline__ float at(int i, int k) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i][k]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float(k & 1 ? w[i][k / 2] & 0xFFFF0000u : w[i][k / 2] << 16);
+    } else {
+      const uint32_t v = w[i][k / 2];
+      return __half2float(__ushort_as_half((unsigned short)(k & 1 ? v >> 16 : v & 0xFFFFu)));
+    }
+  }
+};
+
+// |x| as an ordered whole number of the type's bits, and back as a float.
+template <class T>
+__device__ __forceinline__ float magnitude(uint32_t bits) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(bits << 16);
+  return __half2float(__ushort_as_half((unsigned short)bits));
 }
+template <class T>
+constexpr uint32_t kInfBits = sizeof(T) == 4                             ? 0x7F800000u
+                              : std::is_same<T, __nv_bfloat16>::value ? 0x7F80u
+                                                                      : 0x7C00u;
 
-constexpr int kQ = 128;  // a block's edge
+constexpr int kQ = 128;      // a block's edge
+constexpr int kPitch = 144;  // bytes between the staged rows of the transposed tile
 
-// A 128 x 128 tile per CTA, 256 threads: thread (g = t / 16, v = t % 16) holds
-// rows 8 g .. 8 g + 7 of columns 8 v .. 8 v + 7, so both orientations' 8-bit
-// runs of eight are in one thread.
+// HBM bound (one read of x, one or two bytes written per element).  A 128 x
+// 128 tile per CTA, 256 threads: thread (g = t / 16, v = t % 16) holds rows
+// 8 g .. 8 g + 7 of columns 8 v .. 8 v + 7, so both orientations' runs of
+// eight are in one thread.  Maxima are taken on the bits of |x|; a row's 16
+// threads join by shuffles, a column's through shared memory.  The rows go
+// out as 8 bytes per thread (128 per row), the transposed tile through shared
+// memory as 16.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
-  __shared__ float colmax[16][kQ];
-  __shared__ uint8_t colscale[kQ];
-  __shared__ float wide[8];
+  __shared__ __align__(16) uint32_t colmax[16][kQ];
+  __shared__ __align__(16) uint8_t colscale[kQ];
+  __shared__ uint32_t wide[8];
+  __shared__ __align__(16) uint8_t tile[kQ * kPitch];
+  constexpr int W = Piece<T>::W;
   const int64_t tiles_c = (a.cols + kQ - 1) / kQ;
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;  // tile row, column
   const int64_t r0 = tr * kQ, c0 = tc * kQ;
   const int g = threadIdx.x / 16, v = threadIdx.x % 16;
   const int64_t r = r0 + 8 * g, c = c0 + 8 * v;
-  float x[8][8];
+  Piece<T> x;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+    for (int k = 0; k < W; ++k) x.w[i][k] = 0u;
     if (r + i >= a.rows) continue;
     const T* p = (const T*)a.x + (r + i) * a.ldx + c;
     if (VEC && c + 8 <= a.cols) {
-      constexpr int U = 16 / sizeof(T);
 #pragma unroll
-      for (int k = 0; k < 8; k += U) {
-        float f[U];
-        load_run(p + k, f);
-#pragma unroll
-        for (int j = 0; j < U; ++j) x[i][k + j] = f[j];
+      for (int k = 0; k < W; k += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + k);
+        x.w[i][k] = q.x, x.w[i][k + 1] = q.y, x.w[i][k + 2] = q.z, x.w[i][k + 3] = q.w;
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < a.cols) x[i][k] = to_f32(p[k]);
+        if (c + k < a.cols) {
+          if constexpr (sizeof(T) == 4)
+            x.w[i][k] = __float_as_uint(p[k]);
+          else
+            x.w[i][k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (16 * (k & 1));
+        }
     }
   }
-  float rm[8], cm[8];
+  // largest |x| of each row and column of the piece
+  uint32_t rm[8], cm[8];
+  bool odd;  // a NaN or an infinity in the piece
+  {
+    uint32_t cw[W], all = 0u;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) rm[k] = cm[k] = 0.f;
+    for (int k = 0; k < W; ++k) cw[k] = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float m = finite_abs(x[i][k]);
-      rm[i] = fmaxf(rm[i], m);
-      cm[k] = fmaxf(cm[k], m);
+      for (int k = 0; k < W; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          const uint32_t b = x.w[i][k] & 0x7FFFFFFFu;
+          m = max(m, b);
+          cw[k] = max(cw[k], b);
+        } else {
+          const uint32_t b = x.w[i][k] & 0x7FFF7FFFu;
+          m = __vmaxu2(m, b);
+          cw[k] = __vmaxu2(cw[k], b);
+        }
+      }
+      rm[i] = sizeof(T) == 4 ? m : max(m & 0xFFFFu, m >> 16);
+      all = max(all, rm[i]);
     }
-  int rb[8], cb[8];  // scale bytes of this thread's rows and columns
-  if (a.square) {
-    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, rm[i]);
-    m = warp_max(m);
+    for (int k = 0; k < 8; ++k)
+      cm[k] = sizeof(T) == 4 ? cw[k % W] : (k & 1 ? cw[k / 2 % W] >> 16 : cw[k / 2 % W] & 0xFFFFu);
+    odd = all >= kInfBits<T>;
+    if (odd) {  // over the finite ones
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rm[k] = cm[k] = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t b = sizeof(T) == 4 ? x.w[i][k % W] & 0x7FFFFFFFu
+                                      : x.w[i][k / 2 % W] >> (16 * (k & 1)) & 0x7FFFu;
+          if (b >= kInfBits<T>) b = 0u;
+          rm[i] = max(rm[i], b);
+          cm[k] = max(cm[k], b);
+        }
+    }
+  }
+  float ri[8], ci[8];  // inverse scales of this thread's rows and columns
+  if (a.square) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
     if (threadIdx.x % 32 == 0) wide[threadIdx.x / 32] = m;
     __syncthreads();
     m = wide[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, wide[i]);
-    const int b = scale_byte(m, a.e5m2);
+    for (int i = 1; i < 8; ++i) m = max(m, wide[i]);
+    const int b = scale_byte(magnitude<T>(m), a.e5m2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rb[i] = cb[i] = b;
+    for (int i = 0; i < 8; ++i) ri[i] = ci[i] = inverse_scale(b);
     if (threadIdx.x == 0) {
       if (a.q) a.s[tc * a.lds + tr] = (uint8_t)b;
       if (a.qt) a.st[tr * a.ldst + tc] = (uint8_t)b;
     }
   } else {
+    if (a.qt) {
+      uint4* p = reinterpret_cast<uint4*>(&colmax[g][8 * v]);
+      p[0] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+      p[1] = make_uint4(cm[4], cm[5], cm[6], cm[7]);
+      __syncthreads();
+      if (threadIdx.x < kQ) {
+        uint32_t m = colmax[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = max(m, colmax[i][threadIdx.x]);
+        const int b = scale_byte(magnitude<T>(m), a.e5m2);
+        colscale[threadIdx.x] = (uint8_t)b;
+        if (c0 + threadIdx.x < a.cols) a.st[tr * a.ldst + c0 + threadIdx.x] = (uint8_t)b;
+      }
+    }
     if (a.q) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float m = rm[i];
+        uint32_t m = rm[i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        rb[i] = scale_byte(m, a.e5m2);
-        if (v == 0 && r + i < a.rows)
-          a.s[tc * a.lds + r + i] = (uint8_t)rb[i];
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int b = scale_byte(magnitude<T>(m), a.e5m2);
+        ri[i] = inverse_scale(b);
+        if (v == i && r + i < a.rows) a.s[tc * a.lds + r + i] = (uint8_t)b;
       }
     }
     if (a.qt) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) colmax[g][8 * v + k] = cm[k];
       __syncthreads();
-      if (threadIdx.x < kQ) {
-        float m = colmax[0][threadIdx.x];
+      const uint2 b = *reinterpret_cast<const uint2*>(&colscale[8 * v]);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) m = fmaxf(m, colmax[i][threadIdx.x]);
-        const int b = scale_byte(m, a.e5m2);
-        colscale[threadIdx.x] = (uint8_t)b;
-        if (c0 + threadIdx.x < a.cols)
-          a.st[tr * a.ldst + c0 + threadIdx.x] = (uint8_t)b;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) cb[k] = colscale[8 * v + k];
+      for (int k = 0; k < 8; ++k)
+        ci[k] = inverse_scale((int)((k < 4 ? b.x : b.y) >> (8 * (k & 3)) & 0xFFu));
     }
   }
+  // (the conversion saturates infinities: they become NaN by hand)
+  auto value = [&](int i, int k) {
+    const float f = x.at(i, k);
+    return odd && !(fabsf(f) < INFINITY) ? NAN : f;
+  };
   if (a.q) {
+    const bool run8 = (a.ldq % 8 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (r + i >= a.rows) continue;
-      const float inv = inverse_scale(rb[i]);
-      uint8_t* p = a.q + (r + i) * a.ldq + c;
+      uint32_t o[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < a.cols) p[k] = (uint8_t)to_f8(x[i][k], inv, a.e5m2);
+      for (int h = 0; h < 2; ++h)
+        o[h] = pair_f8(value(i, 4 * h) * ri[i], value(i, 4 * h + 1) * ri[i], a.e5m2) |
+               pair_f8(value(i, 4 * h + 2) * ri[i], value(i, 4 * h + 3) * ri[i], a.e5m2) << 16;
+      uint8_t* p = a.q + (r + i) * a.ldq + c;
+      if (run8 && c + 8 <= a.cols) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k < a.cols) p[k] = (uint8_t)(o[k / 4] >> (8 * (k & 3)));
+      }
     }
   }
   if (a.qt) {
+    // column 8 v + k is staged as row 16 k + v, so that a warp's writes spread
+    // over the banks
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (c + k >= a.cols) continue;
-      const float inv = inverse_scale(cb[k]);
-      uint8_t* p = a.qt + (c + k) * a.ldqt + r;
+      uint32_t o[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r + i < a.rows) p[i] = (uint8_t)to_f8(x[i][k], inv, a.e5m2);
+      for (int h = 0; h < 2; ++h)
+        o[h] = pair_f8(value(4 * h, k) * ci[k], value(4 * h + 1, k) * ci[k], a.e5m2) |
+               pair_f8(value(4 * h + 2, k) * ci[k], value(4 * h + 3, k) * ci[k], a.e5m2) << 16;
+      *reinterpret_cast<uint2*>(&tile[(16 * k + v) * kPitch + 8 * g]) = make_uint2(o[0], o[1]);
+    }
+    __syncthreads();
+    const bool run16 = rows16(a.qt, a.ldqt, 1);
+    const int64_t rr = r0 + 16 * (threadIdx.x % 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = threadIdx.x / 8 + 32 * i;
+      if (c0 + col >= a.cols || rr >= a.rows) continue;
+      const uint4 o = *reinterpret_cast<const uint4*>(
+          &tile[(16 * (col % 8) + col / 8) * kPitch + 16 * (threadIdx.x % 8)]);
+      uint8_t* p = a.qt + (c0 + col) * a.ldqt + rr;
+      if (run16 && rr + 16 <= a.rows) {
+        *reinterpret_cast<uint4*>(p) = o;
+      } else {
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (rr + k < a.rows) p[k] = (uint8_t)(w[k / 4] >> (8 * (k & 3)));
+      }
     }
   }
 }

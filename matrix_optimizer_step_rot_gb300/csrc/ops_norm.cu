@@ -12,13 +12,17 @@ namespace ops {
 
 Drop make_drop(double p, uint64_t seed, uint64_t offset) {
   Drop d;
-  d.on = p > 0.0;
   const double bar = std::nearbyint(p * 4294967296.0);
-  d.all = bar >= 4294967296.0;
-  d.bar = d.all ? 0u : (uint32_t)bar;
-  d.scale = d.all ? 0.f : (float)(1.0 / (1.0 - p));
-  d.seed = seed;
-  d.offset = offset;
+  d.on = bar > 0.0;  // (p below 2^-33 drops nothing, and 1 / (1 - p) rounds to 1)
+  d.bar = d.on ? (uint32_t)(bar - 1.0) : 0u;
+  d.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
+  d.offset[0] = (uint32_t)offset;
+  d.offset[1] = (uint32_t)(offset >> 32);
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+  for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+    d.key[r][0] = k0;
+    d.key[r][1] = k1;
+  }
   return d;
 }
 
@@ -34,7 +38,8 @@ namespace {
 template <class T, int U, bool VEC>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, const T* res,
                                                       int64_t ldr, T* y, int64_t ldy,
-                                                      int64_t rows, int64_t cols, Drop d) {
+                                                      int64_t rows, int64_t cols,
+                                                      const __grid_constant__ Drop d) {
   const int64_t total = rows * cols, runs = (total + U - 1) / U;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < runs;
        u += (int64_t)gridDim.x * 256) {
@@ -159,7 +164,7 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
 
 // A row in the registers of TPR threads, N runs of U elements each.
 template <class T, int U, int TPR, int N>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const NormFwd a) {
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
   __shared__ float red[2][kBlock / 32];
   const int t = threadIdx.x % TPR;
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const N
 // Rows too wide for the registers: a block per row, three passes over it (the
 // second and third out of L2).
 template <class T>
-__global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormFwd a) {
+__global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_constant__ NormFwd a) {
   __shared__ float red[2][32];
   const float inv = 1.f / (float)a.cols;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -284,7 +289,7 @@ __device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c,
 // As the forward kernel; every block walks the rows with a stride and keeps
 // its columns' weight gradients in registers, so that each is written once.
 template <class T, int U, int TPR, int N>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const NormBwd a) {
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
   __shared__ float red[4][kBlock / 32];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const N
 // Rows too wide for the registers: the rows' gradients (two passes over a
 // row) and the columns' partial sums in kernels of their own.
 template <class T>
-__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormBwd a) {
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_constant__ NormBwd a) {
   __shared__ float red[4][32];
   const float inv = 1.f / (float)a.cols;
   int turn = 0;
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormBwd a) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwd a) {
+__global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const __grid_constant__ NormBwd a) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.cols) return;
   float dw = 0.f, db = 0.f;
