@@ -32,15 +32,14 @@ namespace {
 // dropout
 // ---------------------------------------------------------------------------
 
-// One run of U consecutive elements of the row-major order per step.  VEC:
-// every run lies in one row and is one 16-byte access (the host checked);
-// otherwise element by element, the run's row found by one division.
-template <class T, int U, bool VEC>
-__global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, const T* res,
-                                                      int64_t ldr, T* y, int64_t ldy,
-                                                      int64_t rows, int64_t cols,
-                                                      const __grid_constant__ Drop d) {
-  const int64_t total = rows * cols, runs = (total + U - 1) / U;
+// Runs of U consecutive elements of the row-major order, each in one row and
+// one 16-byte access (the host checked); what is left of a single row goes
+// element by element.  Occupancy hides the loads: 6 blocks per SM.
+template <class T, int U>
+__global__ void __launch_bounds__(256, 6)
+    dropout_kernel(const T* x, int64_t ldx, const T* res, int64_t ldr, T* y, int64_t ldy,
+                   int64_t rows, int64_t cols, const __grid_constant__ Drop d) {
+  const int64_t total = rows * cols, runs = total / U;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < runs;
        u += (int64_t)gridDim.x * 256) {
     const int64_t i0 = u * U;
@@ -49,39 +48,54 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, c
       row = i0 / cols;
       col = i0 - row * cols;
     }
-    if (VEC && i0 + U <= total) {
-      float f[U], r[U];
-      load_run(x + row * ldx + col, f);
-      if (res) load_run(res + row * ldr + col, r);
-      drop_run(d, (uint64_t)i0, f);
-      if (res) {
+    const Run<T, U> rx = *reinterpret_cast<const Run<T, U>*>(x + row * ldx + col);
+    Run<T, U> rr;
+    if (res) rr = *reinterpret_cast<const Run<T, U>*>(res + row * ldr + col);
+    float f[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) f[k] = __fadd_rn(r[k], f[k]);
-      }
-      store_run(y + row * ldy + col, f);
-    } else {
-      float f[U], r[U];
-      int64_t rw = row, c = col;
+    for (int k = 0; k < U; ++k) f[k] = to_f32(rx.v[k]);
+    drop_run(d, (uint64_t)i0, f);
+    if (res) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const bool ok = i0 + k < total;
-        f[k] = ok ? to_f32(x[rw * ldx + c]) : 0.f;
-        r[k] = ok && res ? to_f32(res[rw * ldr + c]) : 0.f;
-        if (++c == cols) {
-          c = 0;
-          ++rw;
-        }
-      }
-      drop_run(d, (uint64_t)i0, f);
+      for (int k = 0; k < U; ++k) f[k] = __fadd_rn(to_f32(rr.v[k]), f[k]);
+    }
+    store_run(y + row * ldy + col, f);
+  }
+  // (a single row: others are multiples of U)
+  if (blockIdx.x == 0 && threadIdx.x < total - runs * U) {
+    const int64_t i = runs * U + threadIdx.x;
+    float f[1] = {to_f32(x[i])};
+    drop_run(d, (uint64_t)i, f);
+    y[i] = from_f32<T>(res ? __fadd_rn(to_f32(res[i]), f[0]) : f[0]);
+  }
+}
+
+// Rows that are not 16-byte aligned: four elements of one generator call per
+// step, each found in its row.
+template <class T>
+__global__ void __launch_bounds__(256, 4)
+    dropout_any_kernel(const T* x, int64_t ldx, const T* res, int64_t ldr, T* y, int64_t ldy,
+                       int64_t rows, int64_t cols, const __grid_constant__ Drop d) {
+  const int64_t total = rows * cols, runs = (total + 3) / 4;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < runs;
+       u += (int64_t)gridDim.x * 256) {
+    const int64_t i0 = u * 4;
+    const int64_t row0 = i0 / cols, col0 = i0 - row0 * cols;
+    float f[4], r[4];
+    int64_t row = row0, col = col0;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (i0 + k < total)
-          y[row * ldy + col] = from_f32<T>(res ? __fadd_rn(r[k], f[k]) : f[k]);
-        if (++col == cols) {
-          col = 0;
-          ++row;
-        }
-      }
+    for (int k = 0; k < 4; ++k) {
+      const bool ok = i0 + k < total;
+      f[k] = ok ? to_f32(x[row * ldx + col]) : 0.f;
+      r[k] = ok && res ? to_f32(res[row * ldr + col]) : 0.f;
+      if (++col == cols) col = 0, ++row;
+    }
+    drop_run(d, (uint64_t)i0, f);
+    row = row0, col = col0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k < total) y[row * ldy + col] = from_f32<T>(res ? __fadd_rn(r[k], f[k]) : f[k]);
+      if (++col == cols) col = 0, ++row;
     }
   }
 }
@@ -95,13 +109,13 @@ int launch_dropout(const void* x, int64_t ldx, const void* res, int64_t ldr, voi
     rows = 1;
     ldx = ldy = ldr = cols;
   }
-  const int64_t total = rows * cols, runs = (total + U - 1) / U;
+  const int64_t total = rows * cols, runs = (total + 3) / 4;
   const bool vec = aligned16(x) && aligned16(y) && (!res || aligned16(res)) &&
                    (rows == 1 || (cols % U == 0 && rows16(x, ldx, sizeof(T)) &&
                                   rows16(y, ldy, sizeof(T)) && rows16(res, ldr, sizeof(T))));
-  const int grid = (int)std::min<int64_t>((runs + 255) / 256, 16ll * sm_count());
+  const int grid = (int)std::min<int64_t>((runs + 255) / 256, 24ll * sm_count());
   ProfScope prof(ROT_PROF_ELEMENTWISE, (double)total * sizeof(T) * (res ? 3 : 2), s);
-  auto k = vec ? dropout_kernel<T, U, true> : dropout_kernel<T, U, false>;
+  auto k = vec ? dropout_kernel<T, U> : dropout_any_kernel<T>;
   k<<<grid, 256, 0, s>>>((const T*)x, ldx, (const T*)res, ldr, (T*)y, ldy, rows, cols, d);
   return launched();
 }
@@ -134,26 +148,69 @@ struct NormBwd {
 
 template <class T, int U>
 __device__ __forceinline__ void load_weight(const void* w, bool w32, int c, float (&f)[U]) {
-  if (w32) {
+  if (!w32) {
+    load_run((const T*)w + c, f);
+  } else if constexpr (U > 1) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) f[k] = ((const float*)w)[c + k];
+    for (int k = 0; k < U; k += 4) {
+      const float4 v = *reinterpret_cast<const float4*>((const float*)w + c + k);
+      f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+    }
   } else {
-#pragma unroll
-    for (int k = 0; k < U; ++k) f[k] = to_f32(((const T*)w)[c + k]);
+    f[0] = ((const float*)w)[c];
   }
 }
 
-// Sum of one value over the TPR threads of each row of the block; `red` holds
-// one float per warp.  Calls in a row need different `red` arrays (a thread
-// may still read the last one).
-template <int TPR>
+template <class T, int U>
+__device__ __forceinline__ Run<T, U> raw_run(const void* p, int64_t o) {
+  return *reinterpret_cast<const Run<T, U>*>((const T*)p + o);
+}
+template <class T, int U>
+__device__ __forceinline__ void unpack(const Run<T, U>& r, float (&f)[U]) {
+#pragma unroll
+  for (int k = 0; k < U; ++k) f[k] = to_f32(r.v[k]);
+}
+
+// Waits for the TPR threads of this thread's row (a block may hold several).
+template <int TPR, int BLOCK>
+__device__ __forceinline__ void row_barrier() {
+  if constexpr (TPR == BLOCK)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+}
+
+// Sums of two values over the TPR threads of a row, in one exchange; `red`
+// holds a pair per warp of the block.  Calls in a row need different `red`
+// arrays (a thread may still read the last one).
+template <int TPR, int BLOCK>
+__device__ __forceinline__ float2 row_sum2(float x, float y, float2* red) {
+  x = warp_sum(x);
+  y = warp_sum(y);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(x, y);
+    row_barrier<TPR, BLOCK>();
+    const int first = warp / W * W;
+    x = y = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float2 v = red[first + i];
+      x += v.x;
+      y += v.y;
+    }
+  }
+  return make_float2(x, y);
+}
+template <int TPR, int BLOCK>
 __device__ __forceinline__ float row_sum(float x, float* red) {
   x = warp_sum(x);
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = x;
-    __syncthreads();
+    row_barrier<TPR, BLOCK>();
     const int first = warp / W * W;
     x = 0.f;
 #pragma unroll
@@ -162,33 +219,44 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
   return x;
 }
 
-// A row in the registers of TPR threads, N runs of U elements each.
+constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
+
+// A row in the registers of TPR threads, N runs of U elements each.  Every
+// load of a row is issued before anything is computed or stored (a store may
+// alias a later load as far as the compiler knows).
 template <class T, int U, int TPR, int N>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const __grid_constant__ NormFwd a) {
-  constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
+__global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
+    norm_fwd_kernel(const __grid_constant__ NormFwd a) {
+  constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR;
   __shared__ float red[2][kBlock / 32];
   const int t = threadIdx.x % TPR;
   const float inv = 1.f / (float)a.cols;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
     const int64_t row = base + threadIdx.x / TPR;
     const bool live = row < a.rows;
+    Run<T, U> x[N], r[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        x[n] = raw_run<T, U>(a.x, row * a.ldx + c);
+        if (a.res) r[n] = raw_run<T, U>(a.res, row * a.ldr + c);
+      }
+    }
     float h[N][U];
     float sum = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
-      const bool in = live && c < a.cols;
 #pragma unroll
       for (int k = 0; k < U; ++k) h[n][k] = 0.f;
-      if (in) {
-        load_run((const T*)a.x + row * a.ldx + c, h[n]);
-        float r[U];
-        if (a.res) load_run((const T*)a.res + row * a.ldr + c, r);
+      if (live && c < a.cols) {
+        unpack(x[n], h[n]);
         if (a.h) {
           drop_run(a.d, (uint64_t)row * a.cols + c, h[n]);
 #pragma unroll
           for (int k = 0; k < U; ++k) {
-            if (a.res) h[n][k] = __fadd_rn(r[k], h[n][k]);
+            if (a.res) h[n][k] = __fadd_rn(to_f32(r[n].v[k]), h[n][k]);
             h[n][k] = to_f32(from_f32<T>(h[n][k]));  // the norm reads what is stored
           }
           store_run((T*)a.h + row * a.ldh + c, h[n]);
@@ -197,7 +265,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const _
         for (int k = 0; k < U; ++k) sum += h[n][k];
       }
     }
-    const float mean = row_sum<TPR>(sum, red[0]) * inv;
+    const float mean = row_sum<TPR, kBlock>(sum, red[0]) * inv;
     float sq = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -208,7 +276,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(const _
           sq += h[n][k] * h[n][k];
         }
       }
-    const float rstd = 1.f / sqrtf(row_sum<TPR>(sq, red[1]) * inv + a.eps);
+    const float rstd = 1.f / sqrtf(row_sum<TPR, kBlock>(sq, red[1]) * inv + a.eps);
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -251,13 +319,13 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
       }
       sum += f[0];
     }
-    const float mean = row_sum<1024>(sum, red[0]) * inv;
+    const float mean = row_sum<1024, 1024>(sum, red[0]) * inv;
     float sq = 0.f;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
       const float f = to_f32(src[c]) - mean;
       sq += f * f;
     }
-    const float rstd = 1.f / sqrtf(row_sum<1024>(sq, red[1]) * inv + a.eps);
+    const float rstd = 1.f / sqrtf(row_sum<1024, 1024>(sq, red[1]) * inv + a.eps);
     if (threadIdx.x == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -272,70 +340,121 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
   }
 }
 
-// g of one run from its wdy and hat, written out; dropped into dx.
+// The gradient of one run, g, written out; dropped into dx.  d: the run of
+// dh, already loaded.
 template <class T, int U>
-__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, float (&g)[U]) {
+__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, float (&g)[U],
+                                           const Run<T, U>& d) {
   if (a.dh) {
-    float d[U];
-    load_run((const T*)a.dh + row * a.lddh + c, d);
 #pragma unroll
-    for (int k = 0; k < U; ++k) g[k] += d[k];
+    for (int k = 0; k < U; ++k) g[k] += to_f32(d.v[k]);
   }
   if (a.dres) store_run((T*)a.dres + row * a.lddres + c, g);
   drop_run(a.d, (uint64_t)row * a.cols + c, g);
   store_run((T*)a.dx + row * a.lddx + c, g);
 }
 
-// As the forward kernel; every block walks the rows with a stride and keeps
-// its columns' weight gradients in registers, so that each is written once.
-template <class T, int U, int TPR, int N>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const __grid_constant__ NormBwd a) {
-  constexpr int kBlock = TPR > 256 ? TPR : 256, RPB = kBlock / TPR;
-  __shared__ float red[4][kBlock / 32];
+// As the forward kernel, with the row kept as it was loaded.  A block walks
+// the rows with a stride and sums its columns' weight gradients, in registers
+// or (SMEM: rows of 1024 threads, which leave no registers) in shared memory
+// at places of the thread's own; each block writes one part at its end.  The
+// next row's loads are on their way while this row's two sums are exchanged
+// (where the registers hold two rows).
+template <class T, int U, int TPR, int N, bool SMEM>
+__global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
+    norm_bwd_kernel(const __grid_constant__ NormBwd a) {
+  constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR;
+  extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums
+  __shared__ float2 red[2][kBlock / 32];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.cols;
-  float dw[N][U], db[N][U];
+  float dw[SMEM ? 1 : N][U], db[SMEM ? 1 : N][U];
+  // (SMEM: run n of thread t at (n * TPR + t) * U of each half)
+  constexpr int kHalf = N * TPR * U;
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int k = 0; k < U; ++k) dw[n][k] = db[n][k] = 0.f;
+    for (int k = 0; k < U; ++k) {
+      if constexpr (SMEM)
+        dyn[(n * TPR + t) * U + k] = dyn[kHalf + (n * TPR + t) * U + k] = 0.f;
+      else
+        dw[n][k] = db[n][k] = 0.f;
+    }
+  Run<T, U> dy[N], h[N], dh[N];
+  float mean = 0.f, rstd = 0.f;
+  auto load_row = [&](int64_t row) {
+    if (row >= a.rows) return;
+    mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (c < a.cols) {
+        dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c);
+        h[n] = raw_run<T, U>(a.h, row * a.ldh + c);
+        if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c);
+      }
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
+  if (!SMEM) load_row((int64_t)blockIdx.x * RPB + group);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
     const int64_t row = base + group;
     const bool live = row < a.rows;
-    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
-    float wdy[N][U], hat[N][U];
+    if (SMEM) load_row(row);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
-        float w[U];
-        load_run((const T*)a.dy + row * a.lddy + c, wdy[n]);
-        load_run((const T*)a.h + row * a.ldh + c, hat[n]);
+        float w[U], pw[U], pb[U];
         load_weight<T>(a.w, a.w32, c, w);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          hat[n][k] = (hat[n][k] - mean) * rstd;
-          dw[n][k] += wdy[n][k] * hat[n][k];
-          db[n][k] += wdy[n][k];
-          wdy[n][k] *= w[k];
-          s1 += wdy[n][k];
-          s2 += wdy[n][k] * hat[n][k];
+          const float y = to_f32(dy[n].v[k]), hat = (to_f32(h[n].v[k]) - mean) * rstd;
+          pw[k] = y * hat;
+          pb[k] = y;
+          const float wdy = y * w[k];
+          s1 += wdy;
+          s2 += wdy * hat;
+        }
+        if constexpr (SMEM) {
+          float* q = dyn + (n * TPR + t) * U;
+#pragma unroll
+          for (int k = 0; k < U; ++k) q[k] += pw[k];
+#pragma unroll
+          for (int k = 0; k < U; ++k) q[kHalf + k] += pb[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            dw[n][k] += pw[k];
+            db[n][k] += pb[k];
+          }
         }
       }
     }
-    s1 = row_sum<TPR>(s1, red[turn]) * inv;
-    s2 = row_sum<TPR>(s2, red[turn + 1]) * inv;
-    turn ^= 2;
+    // this row stays for its gradient, the next one comes in
+    Run<T, U> dy0[N], h0[N], dh0[N];
+    const float mean0 = mean, rstd0 = rstd;
+#pragma unroll
+    for (int n = 0; n < N; ++n) dy0[n] = dy[n], h0[n] = h[n], dh0[n] = dh[n];
+    if (!SMEM) load_row(row + step);
+    const float2 s = row_sum2<TPR, kBlock>(s1, s2, red[turn]);
+    s1 = s.x * inv, s2 = s.y * inv;
+    turn ^= 1;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
+        float w[U], g[U];
+        load_weight<T>(a.w, a.w32, c, w);
 #pragma unroll
-        for (int k = 0; k < U; ++k) wdy[n][k] = rstd * (wdy[n][k] - s1 - hat[n][k] * s2);
-        write_grad<T>(a, row, c, wdy[n]);
+        for (int k = 0; k < U; ++k) {
+          const float hat = (to_f32(h0[n].v[k]) - mean0) * rstd0;
+          g[k] = rstd0 * (to_f32(dy0[n].v[k]) * w[k] - s1 - hat * s2);
+        }
+        write_grad<T>(a, row, c, g, dh0[n]);
       }
     }
   }
@@ -363,7 +482,12 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const _
         const int c = (n * TPR + t) * U;
         if (c < a.cols) {
 #pragma unroll
-          for (int k = 0; k < U; ++k) part[which * a.cols + c + k] = which ? db[n][k] : dw[n][k];
+          for (int k = 0; k < U; ++k) {
+            if constexpr (SMEM)
+              part[which * a.cols + c + k] = dyn[which * kHalf + c + k];
+            else
+              part[which * a.cols + c + k] = which ? db[n][k] : dw[n][k];
+          }
         }
       }
     }
@@ -374,7 +498,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(const _
 // row) and the columns' partial sums in kernels of their own.
 template <class T>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_constant__ NormBwd a) {
-  __shared__ float red[4][32];
+  __shared__ float2 red[2][32];
   const float inv = 1.f / (float)a.cols;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -389,15 +513,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
       s1 += wdy;
       s2 += wdy * ((to_f32(h[c]) - mean) * rstd);
     }
-    s1 = row_sum<1024>(s1, red[turn]) * inv;
-    s2 = row_sum<1024>(s2, red[turn + 1]) * inv;
-    turn ^= 2;
+    const float2 s = row_sum2<1024, 1024>(s1, s2, red[turn]);
+    s1 = s.x * inv, s2 = s.y * inv;
+    turn ^= 1;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
       float w[1];
       load_weight<T>(a.w, a.w32, c, w);
       const float hat = (to_f32(h[c]) - mean) * rstd;
       float g[1] = {rstd * (to_f32(dy[c]) * w[0] - s1 - hat * s2)};
-      write_grad<T>(a, row, c, g);
+      Run<T, 1> d;
+      if (a.dh) d = raw_run<T, 1>(a.dh, row * a.lddh + c);
+      write_grad<T>(a, row, c, g, d);
     }
   }
 }
@@ -442,23 +568,32 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int 
 // Partial sums kept at most (the workspace's size does not depend on the GPU).
 constexpr int kMaxParts = 608;
 
-// Threads per row that hold `cols` in 16 elements each.
-inline int row_threads(int cols) {
-  return cols <= 512 ? 32 : cols <= 2048 ? 128 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
+// A thread's share of a row: 32 bytes in two 16-byte runs, or 8 elements one
+// by one where the rows are not 16-byte aligned.
+template <class T, int U>
+constexpr int kRuns = U > 1 ? 2 : 8;
+
+// Threads per row that hold `cols` in their shares; 0: too wide.
+template <class T, int U>
+int row_threads(int cols) {
+  for (int t : {32, 128, 256, 512, 1024})
+    if (cols <= t * U * kRuns<T, U>) return t;
+  return 0;
 }
 
 template <class T, int U>
 int launch_fwd(const NormFwd& a, cudaStream_t s) {
-  constexpr int N = 16 / U;
-  const int tpr = row_threads(a.cols);
-  const int rpb = tpr >= 256 ? 1 : 256 / tpr;
+  constexpr int N = kRuns<T, U>;
+  const int tpr = row_threads<T, U>(a.cols);
+  const int rpb = tpr >= 256 || !tpr ? 1 : 256 / tpr;
   const unsigned grid = (unsigned)std::min<int64_t>((a.rows + rpb - 1) / rpb, 1 << 20);
   switch (tpr) {
     case 32: norm_fwd_kernel<T, U, 32, N><<<grid, 256, 0, s>>>(a); break;
     case 128: norm_fwd_kernel<T, U, 128, N><<<grid, 256, 0, s>>>(a); break;
     case 256: norm_fwd_kernel<T, U, 256, N><<<grid, 256, 0, s>>>(a); break;
     case 512: norm_fwd_kernel<T, U, 512, N><<<grid, 512, 0, s>>>(a); break;
-    default: norm_fwd_kernel<T, U, 1024, N><<<grid, 1024, 0, s>>>(a); break;
+    case 1024: norm_fwd_kernel<T, U, 1024, N><<<grid, 1024, 0, s>>>(a); break;
+    default: norm_fwd_wide_kernel<T><<<grid, 1024, 0, s>>>(a); break;
   }
   return launched();
 }
@@ -468,30 +603,43 @@ int run_fwd(const NormFwd& a, cudaStream_t s) {
   constexpr int U = 16 / sizeof(T);
   ProfScope prof(ROT_PROF_ELEMENTWISE,
                  (double)a.rows * a.cols * sizeof(T) * (2 + (a.res != nullptr) + (a.h != nullptr)), s);
-  if (a.cols > 16384) {
-    norm_fwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
-    return launched();
-  }
   const bool vec = a.cols % U == 0 && rows16(a.x, a.ldx, sizeof(T)) &&
                    rows16(a.res, a.ldr, sizeof(T)) && rows16(a.h, a.ldh, sizeof(T)) &&
-                   rows16(a.y, a.ldy, sizeof(T));
+                   rows16(a.y, a.ldy, sizeof(T)) && aligned16(a.w) && (!a.b || aligned16(a.b));
   return vec ? launch_fwd<T, U>(a, s) : launch_fwd<T, 1>(a, s);
+}
+
+template <class T, int U, int TPR, bool SMEM>
+int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
+  constexpr int N = kRuns<T, U>, block = block_of(TPR), rpb = block / TPR;
+  constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : 0;
+  auto k = norm_bwd_kernel<T, U, TPR, N, SMEM>;
+  if constexpr (SMEM) {
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (attr != cudaSuccess) return ROT_ECUDA;
+  }
+  *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
+                                  std::min(kMaxParts, (TPR >= 512 ? 1 : 2) * sm_count()));
+  k<<<*parts, block, smem, s>>>(a);
+  return launched();
 }
 
 template <class T, int U>
 int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
-  constexpr int N = 16 / U;
-  const int tpr = row_threads(a.cols);
-  const int rpb = tpr >= 256 ? 1 : 256 / tpr;
-  const int per_sm = tpr >= 512 ? 1 : 2;
-  *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
-                                  std::min(kMaxParts, per_sm * sm_count()));
-  switch (tpr) {
-    case 32: norm_bwd_kernel<T, U, 32, N><<<*parts, 256, 0, s>>>(a); break;
-    case 128: norm_bwd_kernel<T, U, 128, N><<<*parts, 256, 0, s>>>(a); break;
-    case 256: norm_bwd_kernel<T, U, 256, N><<<*parts, 256, 0, s>>>(a); break;
-    default: norm_bwd_kernel<T, U, 512, N><<<*parts, 512, 0, s>>>(a); break;
+  switch (row_threads<T, U>(a.cols)) {
+    case 32: return launch_bwd_rows<T, U, 32, false>(a, parts, s);
+    case 128: return launch_bwd_rows<T, U, 128, false>(a, parts, s);
+    case 256: return launch_bwd_rows<T, U, 256, false>(a, parts, s);
+    case 512: return launch_bwd_rows<T, U, 512, false>(a, parts, s);
+    case 1024: return launch_bwd_rows<T, U, 1024, true>(a, parts, s);
   }
+  norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
+  const int e = launched();
+  if (e != ROT_OK) return e;
+  *parts = (int)std::min<int64_t>(a.rows, 64);
+  ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
+  norm_bwd_cols_kernel<T><<<dim3((a.cols + 255) / 256, *parts), 256, 0, s>>>(a);
   return launched();
 }
 
@@ -499,23 +647,14 @@ template <class T>
 int run_bwd(const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
   constexpr int U = 16 / sizeof(T);
   int parts = 0, e = ROT_OK;
-  const double bytes = (double)a.rows * a.cols * sizeof(T) *
-                       (3 + (a.dh != nullptr) + (a.dres != nullptr));
-  if (a.cols > 8192) {
-    {
-      ProfScope prof(ROT_PROF_ELEMENTWISE, bytes, s);
-      norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
-      if ((e = launched()) != ROT_OK) return e;
-    }
-    parts = (int)std::min<int64_t>(a.rows, 64);
-    ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
-    norm_bwd_cols_kernel<T><<<dim3((a.cols + 255) / 256, parts), 256, 0, s>>>(a);
-    e = launched();
-  } else {
-    ProfScope prof(ROT_PROF_ELEMENTWISE, bytes, s);
+  {
+    ProfScope prof(ROT_PROF_ELEMENTWISE,
+                   (double)a.rows * a.cols * sizeof(T) *
+                       (3 + (a.dh != nullptr) + (a.dres != nullptr)), s);
     const bool vec = a.cols % U == 0 && rows16(a.dy, a.lddy, sizeof(T)) &&
                      rows16(a.h, a.ldh, sizeof(T)) && rows16(a.dh, a.lddh, sizeof(T)) &&
-                     rows16(a.dres, a.lddres, sizeof(T)) && rows16(a.dx, a.lddx, sizeof(T));
+                     rows16(a.dres, a.lddres, sizeof(T)) && rows16(a.dx, a.lddx, sizeof(T)) &&
+                     aligned16(a.w);
     e = vec ? launch_bwd<T, U>(a, &parts, s) : launch_bwd<T, 1>(a, &parts, s);
   }
   if (e != ROT_OK) return e;
