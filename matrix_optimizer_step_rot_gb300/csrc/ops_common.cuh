@@ -90,6 +90,88 @@ __device__ __forceinline__ void store_run(T* p, const float (&f)[U]) {
   *reinterpret_cast<Run<T, U>*>(p) = r;
 }
 
+// Pairs of float32 operations as one instruction (each half rounds as the
+// single operation does).
+__device__ __forceinline__ unsigned long long bits2(float2 x) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+  return r;
+}
+__device__ __forceinline__ float2 float2_of(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A run of U elements as float32: pairs, or one alone (y unused, 0).
+template <int U>
+struct Vec {
+  static constexpr int P = (U + 1) / 2;
+  float2 p[P];
+};
+__device__ __forceinline__ float2 unpack2(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 unpack2(__half a, __half b) {
+  return __half22float2(__halves2half2(a, b));
+}
+__device__ __forceinline__ float2 unpack2(__nv_bfloat16 a, __nv_bfloat16 b) {
+  return __bfloat1622float2(__halves2bfloat162(a, b));
+}
+template <class T, int U>
+__device__ __forceinline__ Vec<U> unpack(const Run<T, U>& r) {
+  Vec<U> v;
+  if constexpr (U == 1) {
+    v.p[0] = make_float2(to_f32(r.v[0]), 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < U / 2; ++i) v.p[i] = unpack2(r.v[2 * i], r.v[2 * i + 1]);
+  }
+  return v;
+}
+__device__ __forceinline__ void pack2(float2 x, float& a, float& b) { a = x.x, b = x.y; }
+__device__ __forceinline__ void pack2(float2 x, __half& a, __half& b) {
+  const __half2 h = __float22half2_rn(x);
+  a = __low2half(h), b = __high2half(h);
+}
+__device__ __forceinline__ void pack2(float2 x, __nv_bfloat16& a, __nv_bfloat16& b) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(x);
+  a = __low2bfloat16(h), b = __high2bfloat16(h);
+}
+template <class T, int U>
+__device__ __forceinline__ Run<T, U> pack(const Vec<U>& v) {
+  Run<T, U> r;
+  if constexpr (U == 1) {
+    r.v[0] = from_f32<T>(v.p[0].x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < U / 2; ++i) pack2(v.p[i], r.v[2 * i], r.v[2 * i + 1]);
+  }
+  return r;
+}
+template <class T, int U>
+__device__ __forceinline__ Run<T, U> raw_run(const void* p, int64_t o) {
+  return *reinterpret_cast<const Run<T, U>*>((const T*)p + o);
+}
+template <class T, int U>
+__device__ __forceinline__ void put_run(void* p, int64_t o, const Run<T, U>& r) {
+  *reinterpret_cast<Run<T, U>*>((T*)p + o) = r;
+}
+
 // Dropout of one call: whether it drops at all, 1 / (1 - p), and what the
 // generator takes.  An element is kept where its word is above `bar`, round(p
 // 2^32) - 1 (p = 1: above 2^32 - 1, which no word is).  Philox4x32-10 (Salmon,
@@ -101,18 +183,22 @@ struct Drop {
   int on = 0;
   uint32_t bar = 0;
   float scale = 1.f;
-  uint32_t offset[2] = {};
-  uint32_t key[10][2] = {};
+  // round 0 with its constants (offset and key) worked in: {hi(offset low *
+  // M1) ^ key, lo of the same, offset high ^ key}
+  uint32_t first[3] = {};
+  uint32_t key[9][2] = {};  // of rounds 1 to 9
 };
 struct Words {
   uint32_t w[4];
 };
+constexpr uint32_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u;
 __device__ __forceinline__ Words philox(const Drop& d, uint64_t counter) {
-  uint32_t c0 = (uint32_t)counter, c1 = (uint32_t)(counter >> 32);
-  uint32_t c2 = d.offset[0], c3 = d.offset[1];
+  const uint64_t first = (uint64_t)(uint32_t)counter * kPhiloxM0;
+  uint32_t c0 = d.first[0] ^ (uint32_t)(counter >> 32), c1 = d.first[1];
+  uint32_t c2 = (uint32_t)(first >> 32) ^ d.first[2], c3 = (uint32_t)first;
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+  for (int r = 0; r < 9; ++r) {
+    const uint64_t a = (uint64_t)c0 * kPhiloxM0, b = (uint64_t)c2 * kPhiloxM1;
     c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[r][0];
     c1 = (uint32_t)b;
     c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[r][1];
@@ -122,27 +208,28 @@ __device__ __forceinline__ Words philox(const Drop& d, uint64_t counter) {
 }
 Drop make_drop(double p, uint64_t seed, uint64_t offset);
 
-// f[k] (elements i0 .. i0 + U - 1 of the row-major order) <- dropped values.
-// Runs of 4 or more start on a multiple of 4.
+// Elements i0 .. i0 + U - 1 of the row-major order <- dropped values.  Runs of
+// 4 or more start on a multiple of 4.
 template <int U>
-__device__ __forceinline__ void drop_run(const Drop& d, uint64_t i0, float (&f)[U]) {
+__device__ __forceinline__ void drop_run(const Drop& d, uint64_t i0, Vec<U>& f) {
   if (!d.on) return;
   if constexpr (U % 4 == 0) {
 #pragma unroll
     for (int q = 0; q < U / 4; ++q) {
       const Words w = philox(d, i0 / 4 + q);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        f[4 * q + k] = w.w[k] > d.bar ? __fmul_rn(f[4 * q + k], d.scale) : 0.f;
+      for (int k = 0; k < 2; ++k) {
+        const float2 s = mul2(f.p[2 * q + k], both(d.scale));
+        f.p[2 * q + k].x = w.w[2 * k] > d.bar ? s.x : 0.f;
+        f.p[2 * q + k].y = w.w[2 * k + 1] > d.bar ? s.y : 0.f;
+      }
     }
   } else {
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const Words w = philox(d, (i0 + k) / 4);
-      const uint32_t s = (uint32_t)(i0 + k) & 3u;
-      const uint32_t word = s == 0 ? w.w[0] : s == 1 ? w.w[1] : s == 2 ? w.w[2] : w.w[3];
-      f[k] = word > d.bar ? __fmul_rn(f[k], d.scale) : 0.f;
-    }
+    static_assert(U == 1, "runs of one element or of a multiple of four");
+    const Words w = philox(d, i0 / 4);
+    const uint32_t s = (uint32_t)i0 & 3u;
+    const uint32_t word = s == 0 ? w.w[0] : s == 1 ? w.w[1] : s == 2 ? w.w[2] : w.w[3];
+    f.p[0].x = word > d.bar ? __fmul_rn(f.p[0].x, d.scale) : 0.f;
   }
 }
 

@@ -16,12 +16,14 @@ Drop make_drop(double p, uint64_t seed, uint64_t offset) {
   d.on = bar > 0.0;  // (p below 2^-33 drops nothing, and 1 / (1 - p) rounds to 1)
   d.bar = d.on ? (uint32_t)(bar - 1.0) : 0u;
   d.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
-  d.offset[0] = (uint32_t)offset;
-  d.offset[1] = (uint32_t)(offset >> 32);
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
-  for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
-    d.key[r][0] = k0;
-    d.key[r][1] = k1;
+  const uint64_t b = (uint64_t)(uint32_t)offset * kPhiloxM1;
+  d.first[0] = (uint32_t)(b >> 32) ^ k0;
+  d.first[1] = (uint32_t)b;
+  d.first[2] = (uint32_t)(offset >> 32) ^ k1;
+  for (int r = 0; r < 9; ++r) {
+    d.key[r][0] = k0 += 0x9E3779B9u;
+    d.key[r][1] = k1 += 0xBB67AE85u;
   }
   return d;
 }
@@ -48,25 +50,24 @@ __global__ void __launch_bounds__(256, 6)
       row = i0 / cols;
       col = i0 - row * cols;
     }
-    const Run<T, U> rx = *reinterpret_cast<const Run<T, U>*>(x + row * ldx + col);
+    const Run<T, U> rx = raw_run<T, U>(x, row * ldx + col);
     Run<T, U> rr;
-    if (res) rr = *reinterpret_cast<const Run<T, U>*>(res + row * ldr + col);
-    float f[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) f[k] = to_f32(rx.v[k]);
+    if (res) rr = raw_run<T, U>(res, row * ldr + col);
+    Vec<U> f = unpack(rx);
     drop_run(d, (uint64_t)i0, f);
     if (res) {
+      const Vec<U> r = unpack(rr);
 #pragma unroll
-      for (int k = 0; k < U; ++k) f[k] = __fadd_rn(to_f32(rr.v[k]), f[k]);
+      for (int k = 0; k < Vec<U>::P; ++k) f.p[k] = add2(r.p[k], f.p[k]);
     }
-    store_run(y + row * ldy + col, f);
+    put_run(y, row * ldy + col, pack<T>(f));
   }
   // (a single row: others are multiples of U)
   if (blockIdx.x == 0 && threadIdx.x < total - runs * U) {
     const int64_t i = runs * U + threadIdx.x;
-    float f[1] = {to_f32(x[i])};
+    Vec<1> f = {{make_float2(to_f32(x[i]), 0.f)}};
     drop_run(d, (uint64_t)i, f);
-    y[i] = from_f32<T>(res ? __fadd_rn(to_f32(res[i]), f[0]) : f[0]);
+    y[i] = from_f32<T>(res ? __fadd_rn(to_f32(res[i]), f.p[0].x) : f.p[0].x);
   }
 }
 
@@ -81,12 +82,13 @@ __global__ void __launch_bounds__(256, 4)
        u += (int64_t)gridDim.x * 256) {
     const int64_t i0 = u * 4;
     const int64_t row0 = i0 / cols, col0 = i0 - row0 * cols;
-    float f[4], r[4];
+    Vec<4> f;
+    float r[4];
     int64_t row = row0, col = col0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool ok = i0 + k < total;
-      f[k] = ok ? to_f32(x[row * ldx + col]) : 0.f;
+      (k & 1 ? f.p[k / 2].y : f.p[k / 2].x) = ok ? to_f32(x[row * ldx + col]) : 0.f;
       r[k] = ok && res ? to_f32(res[row * ldr + col]) : 0.f;
       if (++col == cols) col = 0, ++row;
     }
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(256, 4)
     row = row0, col = col0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (i0 + k < total) y[row * ldy + col] = from_f32<T>(res ? __fadd_rn(r[k], f[k]) : f[k]);
+      const float v = k & 1 ? f.p[k / 2].y : f.p[k / 2].x;
+      if (i0 + k < total) y[row * ldy + col] = from_f32<T>(res ? __fadd_rn(r[k], v) : v);
       if (++col == cols) col = 0, ++row;
     }
   }
@@ -147,28 +150,19 @@ struct NormBwd {
 };
 
 template <class T, int U>
-__device__ __forceinline__ void load_weight(const void* w, bool w32, int c, float (&f)[U]) {
-  if (!w32) {
-    load_run((const T*)w + c, f);
-  } else if constexpr (U > 1) {
+__device__ __forceinline__ Vec<U> load_weight(const void* w, bool w32, int c) {
+  if (!w32) return unpack(raw_run<T, U>(w, c));
+  Vec<U> f;
+  if constexpr (U > 1) {
 #pragma unroll
-    for (int k = 0; k < U; k += 4) {
-      const float4 v = *reinterpret_cast<const float4*>((const float*)w + c + k);
-      f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+    for (int k = 0; k < U / 2; k += 2) {
+      const float4 v = *reinterpret_cast<const float4*>((const float*)w + c + 2 * k);
+      f.p[k] = make_float2(v.x, v.y), f.p[k + 1] = make_float2(v.z, v.w);
     }
   } else {
-    f[0] = ((const float*)w)[c];
+    f.p[0] = make_float2(((const float*)w)[c], 0.f);
   }
-}
-
-template <class T, int U>
-__device__ __forceinline__ Run<T, U> raw_run(const void* p, int64_t o) {
-  return *reinterpret_cast<const Run<T, U>*>((const T*)p + o);
-}
-template <class T, int U>
-__device__ __forceinline__ void unpack(const Run<T, U>& r, float (&f)[U]) {
-#pragma unroll
-  for (int k = 0; k < U; ++k) f[k] = to_f32(r.v[k]);
+  return f;
 }
 
 // Waits for the TPR threads of this thread's row (a block may hold several).
@@ -243,40 +237,44 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
         if (a.res) r[n] = raw_run<T, U>(a.res, row * a.ldr + c);
       }
     }
-    float h[N][U];
-    float sum = 0.f;
+    Vec<U> h[N];
+    float2 sum = both(0.f);
+    constexpr int P = Vec<U>::P;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
 #pragma unroll
-      for (int k = 0; k < U; ++k) h[n][k] = 0.f;
+      for (int k = 0; k < P; ++k) h[n].p[k] = both(0.f);
       if (live && c < a.cols) {
-        unpack(x[n], h[n]);
+        h[n] = unpack(x[n]);
         if (a.h) {
           drop_run(a.d, (uint64_t)row * a.cols + c, h[n]);
+          if (a.res) {
+            const Vec<U> v = unpack(r[n]);
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            if (a.res) h[n][k] = __fadd_rn(to_f32(r[n].v[k]), h[n][k]);
-            h[n][k] = to_f32(from_f32<T>(h[n][k]));  // the norm reads what is stored
+            for (int k = 0; k < P; ++k) h[n].p[k] = add2(v.p[k], h[n].p[k]);
           }
-          store_run((T*)a.h + row * a.ldh + c, h[n]);
+          const Run<T, U> stored = pack<T>(h[n]);
+          put_run(a.h, row * a.ldh + c, stored);
+          h[n] = unpack(stored);  // the norm reads what is stored
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) sum += h[n][k];
+        for (int k = 0; k < P; ++k) sum = add2(sum, h[n].p[k]);
       }
     }
-    const float mean = row_sum<TPR, kBlock>(sum, red[0]) * inv;
-    float sq = 0.f;
+    const float mean = row_sum<TPR, kBlock>(sum.x + sum.y, red[0]) * inv;
+    float2 sq = both(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
       if ((n * TPR + t) * U < a.cols) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          h[n][k] -= mean;
-          sq += h[n][k] * h[n][k];
+        for (int k = 0; k < P; ++k) {
+          h[n].p[k] = add2(h[n].p[k], both(-mean));
+          if (U == 1) h[n].p[k].y = 0.f;
+          sq = fma2(h[n].p[k], h[n].p[k], sq);
         }
       }
-    const float rstd = 1.f / sqrtf(row_sum<TPR, kBlock>(sq, red[1]) * inv + a.eps);
+    const float rstd = 1.f / sqrtf(row_sum<TPR, kBlock>(sq.x + sq.y, red[1]) * inv + a.eps);
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -285,15 +283,14 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
-        float w[U], b[U];
-        load_weight<T>(a.w, a.w32, c, w);
-        if (a.b) load_weight<T>(a.b, a.w32, c, b);
+        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c);
+        Vec<U> b;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          h[n][k] = h[n][k] * rstd * w[k];
-          if (a.b) h[n][k] += b[k];
-        }
-        store_run((T*)a.y + row * a.ldy + c, h[n]);
+        for (int k = 0; k < P; ++k) b.p[k] = both(0.f);
+        if (a.b) b = load_weight<T, U>(a.b, a.w32, c);
+#pragma unroll
+        for (int k = 0; k < P; ++k) h[n].p[k] = fma2(mul2(h[n].p[k], both(rstd)), w.p[k], b.p[k]);
+        put_run(a.y, row * a.ldy + c, pack<T>(h[n]));
       }
     }
   }
@@ -309,15 +306,15 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
     const T* src = a.h ? (const T*)a.h + row * a.ldh : (const T*)a.x + row * a.ldx;
     float sum = 0.f;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      float f[1] = {to_f32(((const T*)a.x)[row * a.ldx + c])};
+      Vec<1> f = {{make_float2(to_f32(((const T*)a.x)[row * a.ldx + c]), 0.f)}};
       if (a.h) {
         const float r = a.res ? to_f32(((const T*)a.res)[row * a.ldr + c]) : 0.f;
         drop_run(a.d, (uint64_t)row * a.cols + c, f);
-        const T v = from_f32<T>(a.res ? __fadd_rn(r, f[0]) : f[0]);
+        const T v = from_f32<T>(a.res ? __fadd_rn(r, f.p[0].x) : f.p[0].x);
         ((T*)a.h)[row * a.ldh + c] = v;
-        f[0] = to_f32(v);
+        f.p[0].x = to_f32(v);
       }
-      sum += f[0];
+      sum += f.p[0].x;
     }
     const float mean = row_sum<1024, 1024>(sum, red[0]) * inv;
     float sq = 0.f;
@@ -331,11 +328,9 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
       a.rstd[row] = rstd;
     }
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      float w[1], b[1] = {0.f};
-      load_weight<T>(a.w, a.w32, c, w);
-      if (a.b) load_weight<T>(a.b, a.w32, c, b);
-      const float y = (to_f32(src[c]) - mean) * rstd * w[0];
-      ((T*)a.y)[row * a.ldy + c] = from_f32<T>(a.b ? y + b[0] : y);
+      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0].x;
+      const float b = a.b ? load_weight<T, 1>(a.b, a.w32, c).p[0].x : 0.f;
+      ((T*)a.y)[row * a.ldy + c] = from_f32<T>((to_f32(src[c]) - mean) * rstd * w + b);
     }
   }
 }
@@ -343,15 +338,21 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
 // The gradient of one run, g, written out; dropped into dx.  d: the run of
 // dh, already loaded.
 template <class T, int U>
-__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, float (&g)[U],
+__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, Vec<U>& g,
                                            const Run<T, U>& d) {
   if (a.dh) {
+    const Vec<U> v = unpack(d);
 #pragma unroll
-    for (int k = 0; k < U; ++k) g[k] += to_f32(d.v[k]);
+    for (int k = 0; k < Vec<U>::P; ++k) g.p[k] = add2(g.p[k], v.p[k]);
   }
-  if (a.dres) store_run((T*)a.dres + row * a.lddres + c, g);
+  if (a.dres) put_run(a.dres, row * a.lddres + c, pack<T>(g));
   drop_run(a.d, (uint64_t)row * a.cols + c, g);
-  store_run((T*)a.dx + row * a.lddx + c, g);
+  put_run(a.dx, row * a.lddx + c, pack<T>(g));
+}
+
+template <int U>
+__device__ __forceinline__ float at(const Vec<U>& v, int k) {
+  return k & 1 ? v.p[k / 2].y : v.p[k / 2].x;
 }
 
 // As the forward kernel, with the row kept as it was loaded.  A block walks
@@ -369,17 +370,21 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.cols;
-  float dw[SMEM ? 1 : N][U], db[SMEM ? 1 : N][U];
-  // (SMEM: run n of thread t at (n * TPR + t) * U of each half)
-  constexpr int kHalf = N * TPR * U;
+  constexpr int P = Vec<U>::P;
+  Vec<U> dw[SMEM ? 1 : N], db[SMEM ? 1 : N];
+  // (SMEM: run n of thread t at element (n * TPR + t) * U of each half)
+  float2* sums = reinterpret_cast<float2*>(dyn);
+  constexpr int kHalf = N * TPR * U / 2;  // pairs
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if constexpr (SMEM)
-        dyn[(n * TPR + t) * U + k] = dyn[kHalf + (n * TPR + t) * U + k] = 0.f;
+    for (int k = 0; k < P; ++k) {
+      if constexpr (!SMEM)
+        dw[n].p[k] = db[n].p[k] = both(0.f);
+      else if constexpr (U > 1)
+        sums[(n * TPR + t) * P + k] = sums[kHalf + (n * TPR + t) * P + k] = both(0.f);
       else
-        dw[n][k] = db[n][k] = 0.f;
+        dyn[n * TPR + t] = dyn[2 * kHalf + n * TPR + t] = 0.f;
     }
   Run<T, U> dy[N], h[N], dh[N];
   float mean = 0.f, rstd = 0.f;
@@ -403,33 +408,29 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
     const int64_t row = base + group;
     const bool live = row < a.rows;
     if (SMEM) load_row(row);
-    float s1 = 0.f, s2 = 0.f;
+    float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
-        float w[U], pw[U], pb[U];
-        load_weight<T>(a.w, a.w32, c, w);
+        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy[n]), x = unpack(h[n]);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const float y = to_f32(dy[n].v[k]), hat = (to_f32(h[n].v[k]) - mean) * rstd;
-          pw[k] = y * hat;
-          pb[k] = y;
-          const float wdy = y * w[k];
-          s1 += wdy;
-          s2 += wdy * hat;
-        }
-        if constexpr (SMEM) {
-          float* q = dyn + (n * TPR + t) * U;
-#pragma unroll
-          for (int k = 0; k < U; ++k) q[k] += pw[k];
-#pragma unroll
-          for (int k = 0; k < U; ++k) q[kHalf + k] += pb[k];
-        } else {
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            dw[n][k] += pw[k];
-            db[n][k] += pb[k];
+        for (int k = 0; k < P; ++k) {
+          const float2 hat = mul2(add2(x.p[k], both(-mean)), both(rstd));
+          const float2 wdy = mul2(y.p[k], w.p[k]);
+          s1 = add2(s1, wdy);
+          s2 = fma2(wdy, hat, s2);
+          if constexpr (!SMEM) {
+            dw[n].p[k] = fma2(y.p[k], hat, dw[n].p[k]);
+            db[n].p[k] = add2(db[n].p[k], y.p[k]);
+          } else if constexpr (U > 1) {
+            float2* q = sums + (n * TPR + t) * P + k;
+            q[0] = fma2(y.p[k], hat, q[0]);
+            q[kHalf] = add2(q[kHalf], y.p[k]);
+          } else {
+            float* q = dyn + n * TPR + t;
+            q[0] += y.p[k].x * hat.x;
+            q[2 * kHalf] += y.p[k].x;
           }
         }
       }
@@ -440,21 +441,24 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
 #pragma unroll
     for (int n = 0; n < N; ++n) dy0[n] = dy[n], h0[n] = h[n], dh0[n] = dh[n];
     if (!SMEM) load_row(row + step);
-    const float2 s = row_sum2<TPR, kBlock>(s1, s2, red[turn]);
-    s1 = s.x * inv, s2 = s.y * inv;
+    // (one element alone: the second half of its pairs is 0 times something)
+    const float2 s = U > 1 ? row_sum2<TPR, kBlock>(s1.x + s1.y, s2.x + s2.y, red[turn])
+                           : row_sum2<TPR, kBlock>(s1.x, s2.x, red[turn]);
+    const float m1 = s.x * inv, m2 = s.y * inv;
     turn ^= 1;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
-        float w[U], g[U];
-        load_weight<T>(a.w, a.w32, c, w);
+        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy0[n]), x = unpack(h0[n]);
+        Vec<U> g;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const float hat = (to_f32(h0[n].v[k]) - mean0) * rstd0;
-          g[k] = rstd0 * (to_f32(dy0[n].v[k]) * w[k] - s1 - hat * s2);
+        for (int k = 0; k < P; ++k) {
+          const float2 hat = mul2(add2(x.p[k], both(-mean0)), both(rstd0));
+          g.p[k] = fma2(y.p[k], w.p[k], both(-m1));
+          g.p[k] = mul2(fma2(hat, both(-m2), g.p[k]), both(rstd0));
         }
-        write_grad<T>(a, row, c, g, dh0[n]);
+        write_grad(a, row, c, g, dh0[n]);
       }
     }
   }
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
       for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          join[group][(n * TPR + t) * U + k] = which ? db[n][k] : dw[n][k];
+          join[group][(n * TPR + t) * U + k] = at<U>(which ? db[n] : dw[n], k);
       __syncthreads();
       for (int c = threadIdx.x; c < a.cols; c += kBlock) {
         float sum = 0.f;
@@ -484,9 +488,9 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             if constexpr (SMEM)
-              part[which * a.cols + c + k] = dyn[which * kHalf + c + k];
+              part[which * a.cols + c + k] = dyn[which * 2 * kHalf + c + k];
             else
-              part[which * a.cols + c + k] = which ? db[n][k] : dw[n][k];
+              part[which * a.cols + c + k] = at<U>(which ? db[n] : dw[n], k);
           }
         }
       }
@@ -507,9 +511,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
     const T* h = (const T*)a.h + row * a.ldh;
     float s1 = 0.f, s2 = 0.f;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      float w[1];
-      load_weight<T>(a.w, a.w32, c, w);
-      const float wdy = to_f32(dy[c]) * w[0];
+      const float wdy = to_f32(dy[c]) * load_weight<T, 1>(a.w, a.w32, c).p[0].x;
       s1 += wdy;
       s2 += wdy * ((to_f32(h[c]) - mean) * rstd);
     }
@@ -517,13 +519,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
     s1 = s.x * inv, s2 = s.y * inv;
     turn ^= 1;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      float w[1];
-      load_weight<T>(a.w, a.w32, c, w);
+      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0].x;
       const float hat = (to_f32(h[c]) - mean) * rstd;
-      float g[1] = {rstd * (to_f32(dy[c]) * w[0] - s1 - hat * s2)};
+      Vec<1> g = {{make_float2(rstd * (to_f32(dy[c]) * w - s1 - hat * s2), 0.f)}};
       Run<T, 1> d;
       if (a.dh) d = raw_run<T, 1>(a.dh, row * a.lddh + c);
-      write_grad<T>(a, row, c, g, d);
+      write_grad(a, row, c, g, d);
     }
   }
 }
