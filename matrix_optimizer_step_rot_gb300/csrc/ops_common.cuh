@@ -117,13 +117,32 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
   return float2_of(r);
 }
+// the same on one value, for runs of one element
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float add2(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ float mul2(float a, float b) { return __fmul_rn(a, b); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+template <class E>
+__device__ __forceinline__ E all_of(float x);
+template <>
+__device__ __forceinline__ float2 all_of<float2>(float x) { return make_float2(x, x); }
+template <>
+__device__ __forceinline__ float all_of<float>(float x) { return x; }
+__device__ __forceinline__ float total(float2 x) { return x.x + x.y; }
+__device__ __forceinline__ float total(float x) { return x; }
 
-// A run of U elements as float32: pairs, or one alone (y unused, 0).
+// A run of U elements as float32, in pairs or one alone.
 template <int U>
 struct Vec {
-  static constexpr int P = (U + 1) / 2;
-  float2 p[P];
+  using E = float2;
+  static constexpr int P = U / 2;
+  E p[P];
+};
+template <>
+struct Vec<1> {
+  using E = float;
+  static constexpr int P = 1;
+  E p[1];
 };
 __device__ __forceinline__ float2 unpack2(float a, float b) { return make_float2(a, b); }
 __device__ __forceinline__ float2 unpack2(__half a, __half b) {
@@ -136,7 +155,7 @@ template <class T, int U>
 __device__ __forceinline__ Vec<U> unpack(const Run<T, U>& r) {
   Vec<U> v;
   if constexpr (U == 1) {
-    v.p[0] = make_float2(to_f32(r.v[0]), 0.f);
+    v.p[0] = to_f32(r.v[0]);
   } else {
 #pragma unroll
     for (int i = 0; i < U / 2; ++i) v.p[i] = unpack2(r.v[2 * i], r.v[2 * i + 1]);
@@ -156,7 +175,7 @@ template <class T, int U>
 __device__ __forceinline__ Run<T, U> pack(const Vec<U>& v) {
   Run<T, U> r;
   if constexpr (U == 1) {
-    r.v[0] = from_f32<T>(v.p[0].x);
+    r.v[0] = from_f32<T>(v.p[0]);
   } else {
 #pragma unroll
     for (int i = 0; i < U / 2; ++i) pack2(v.p[i], r.v[2 * i], r.v[2 * i + 1]);
@@ -191,18 +210,25 @@ struct Drop {
 struct Words {
   uint32_t w[4];
 };
+__device__ __forceinline__ uint2 mul_wide(uint32_t a, uint32_t b) {  // (low, high)
+  uint2 r;
+  asm("{\n\t.reg .b64 t;\n\tmul.wide.u32 t, %2, %3;\n\tmov.b64 {%0, %1}, t;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(a), "r"(b));
+  return r;
+}
 constexpr uint32_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u;
 __device__ __forceinline__ Words philox(const Drop& d, uint64_t counter) {
-  const uint64_t first = (uint64_t)(uint32_t)counter * kPhiloxM0;
+  const uint2 first = mul_wide((uint32_t)counter, kPhiloxM0);
   uint32_t c0 = d.first[0] ^ (uint32_t)(counter >> 32), c1 = d.first[1];
-  uint32_t c2 = (uint32_t)(first >> 32) ^ d.first[2], c3 = (uint32_t)first;
+  uint32_t c2 = first.y ^ d.first[2], c3 = first.x;
 #pragma unroll
   for (int r = 0; r < 9; ++r) {
-    const uint64_t a = (uint64_t)c0 * kPhiloxM0, b = (uint64_t)c2 * kPhiloxM1;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[r][0];
-    c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[r][1];
-    c3 = (uint32_t)a;
+    const uint2 a = mul_wide(c0, kPhiloxM0), b = mul_wide(c2, kPhiloxM1);
+    c0 = b.y ^ c1 ^ d.key[r][0];
+    c1 = b.x;
+    c2 = a.y ^ c3 ^ d.key[r][1];
+    c3 = a.x;
   }
   return {{c0, c1, c2, c3}};
 }
@@ -229,7 +255,7 @@ __device__ __forceinline__ void drop_run(const Drop& d, uint64_t i0, Vec<U>& f) 
     const Words w = philox(d, i0 / 4);
     const uint32_t s = (uint32_t)i0 & 3u;
     const uint32_t word = s == 0 ? w.w[0] : s == 1 ? w.w[1] : s == 2 ? w.w[2] : w.w[3];
-    f.p[0].x = word > d.bar ? __fmul_rn(f.p[0].x, d.scale) : 0.f;
+    f.p[0] = word > d.bar ? __fmul_rn(f.p[0], d.scale) : 0.f;
   }
 }
 

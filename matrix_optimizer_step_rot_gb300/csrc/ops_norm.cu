@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(256, 6)
   // (a single row: others are multiples of U)
   if (blockIdx.x == 0 && threadIdx.x < total - runs * U) {
     const int64_t i = runs * U + threadIdx.x;
-    Vec<1> f = {{make_float2(to_f32(x[i]), 0.f)}};
+    Vec<1> f = {{to_f32(x[i])}};
     drop_run(d, (uint64_t)i, f);
-    y[i] = from_f32<T>(res ? __fadd_rn(to_f32(res[i]), f.p[0].x) : f.p[0].x);
+    y[i] = from_f32<T>(res ? __fadd_rn(to_f32(res[i]), f.p[0]) : f.p[0]);
   }
 }
 
@@ -160,9 +160,18 @@ __device__ __forceinline__ Vec<U> load_weight(const void* w, bool w32, int c) {
       f.p[k] = make_float2(v.x, v.y), f.p[k + 1] = make_float2(v.z, v.w);
     }
   } else {
-    f.p[0] = make_float2(((const float*)w)[c], 0.f);
+    f.p[0] = ((const float*)w)[c];
   }
   return f;
+}
+
+// 1 / sqrt(v): the approximation and one Newton step (as exact as the two
+// rounded operations, at a few instructions); the plain operations at the ends
+// of the range.
+__device__ __forceinline__ float inverse_root(float v) {
+  const float r = rsqrtf(v);
+  if (!(v > 1e-36f && v < 1e36f)) return 1.f / sqrtf(v);
+  return r * fmaf(-0.5f * v * r, r, 1.5f);
 }
 
 // Waits for the TPR threads of this thread's row (a block may hold several).
@@ -179,21 +188,26 @@ __device__ __forceinline__ void row_barrier() {
 // arrays (a thread may still read the last one).
 template <int TPR, int BLOCK>
 __device__ __forceinline__ float2 row_sum2(float x, float y, float2* red) {
-  x = warp_sum(x);
-  y = warp_sum(y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float2 v = make_float2(__shfl_xor_sync(0xffffffffu, x, o),
+                                 __shfl_xor_sync(0xffffffffu, y, o));
+    const float2 w = add2(make_float2(x, y), v);
+    x = w.x, y = w.y;
+  }
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = make_float2(x, y);
     row_barrier<TPR, BLOCK>();
-    const int first = warp / W * W;
-    x = y = 0.f;
+    const float4* p = reinterpret_cast<const float4*>(red + warp / W * W);
+    float2 sum = both(0.f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 v = red[first + i];
-      x += v.x;
-      y += v.y;
+    for (int i = 0; i < W / 2; ++i) {
+      const float4 v = p[i];
+      sum = add2(sum, add2(make_float2(v.x, v.y), make_float2(v.z, v.w)));
     }
+    return sum;
   }
   return make_float2(x, y);
 }
@@ -205,28 +219,32 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = x;
     row_barrier<TPR, BLOCK>();
-    const int first = warp / W * W;
-    x = 0.f;
+    const float4* p = reinterpret_cast<const float4*>(red + warp / W * W);
+    float2 sum = both(0.f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) x += red[first + i];
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 v = p[i];
+      sum = add2(sum, add2(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+    }
+    return sum.x + sum.y;
   }
   return x;
 }
 
-constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
+constexpr int block_of(int tpr) { return tpr > 128 ? tpr : 128; }
 
 // A row in the registers of TPR threads, N runs of U elements each.  Every
 // load of a row is issued before anything is computed or stored (a store may
 // alias a later load as far as the compiler knows).
 template <class T, int U, int TPR, int N>
-__global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
+__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 640 / block_of(TPR))
     norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR;
-  __shared__ float red[2][kBlock / 32];
+  __shared__ __align__(16) float red[2][kBlock / 32];
   const int t = threadIdx.x % TPR;
   const float inv = 1.f / (float)a.cols;
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
-    const int64_t row = base + threadIdx.x / TPR;
+  {
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     const bool live = row < a.rows;
     Run<T, U> x[N], r[N];
 #pragma unroll
@@ -238,13 +256,14 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
       }
     }
     Vec<U> h[N];
-    float2 sum = both(0.f);
+    using E = typename Vec<U>::E;
     constexpr int P = Vec<U>::P;
+    E sum = all_of<E>(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
 #pragma unroll
-      for (int k = 0; k < P; ++k) h[n].p[k] = both(0.f);
+      for (int k = 0; k < P; ++k) h[n].p[k] = all_of<E>(0.f);
       if (live && c < a.cols) {
         h[n] = unpack(x[n]);
         if (a.h) {
@@ -262,19 +281,18 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
         for (int k = 0; k < P; ++k) sum = add2(sum, h[n].p[k]);
       }
     }
-    const float mean = row_sum<TPR, kBlock>(sum.x + sum.y, red[0]) * inv;
-    float2 sq = both(0.f);
+    const float mean = row_sum<TPR, kBlock>(total(sum), red[0]) * inv;
+    E sq = all_of<E>(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
       if ((n * TPR + t) * U < a.cols) {
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          h[n].p[k] = add2(h[n].p[k], both(-mean));
-          if (U == 1) h[n].p[k].y = 0.f;
+          h[n].p[k] = add2(h[n].p[k], all_of<E>(-mean));
           sq = fma2(h[n].p[k], h[n].p[k], sq);
         }
       }
-    const float rstd = 1.f / sqrtf(row_sum<TPR, kBlock>(sq.x + sq.y, red[1]) * inv + a.eps);
+    const float rstd = inverse_root(row_sum<TPR, kBlock>(total(sq), red[1]) * inv + a.eps);
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -286,10 +304,10 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
         const Vec<U> w = load_weight<T, U>(a.w, a.w32, c);
         Vec<U> b;
 #pragma unroll
-        for (int k = 0; k < P; ++k) b.p[k] = both(0.f);
+        for (int k = 0; k < P; ++k) b.p[k] = all_of<E>(0.f);
         if (a.b) b = load_weight<T, U>(a.b, a.w32, c);
 #pragma unroll
-        for (int k = 0; k < P; ++k) h[n].p[k] = fma2(mul2(h[n].p[k], both(rstd)), w.p[k], b.p[k]);
+        for (int k = 0; k < P; ++k) h[n].p[k] = fma2(mul2(h[n].p[k], all_of<E>(rstd)), w.p[k], b.p[k]);
         put_run(a.y, row * a.ldy + c, pack<T>(h[n]));
       }
     }
@@ -300,21 +318,21 @@ __global__ void __launch_bounds__(block_of(TPR), TPR > 256 ? 1024 / TPR : 3)
 // second and third out of L2).
 template <class T>
 __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_constant__ NormFwd a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   const float inv = 1.f / (float)a.cols;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* src = a.h ? (const T*)a.h + row * a.ldh : (const T*)a.x + row * a.ldx;
     float sum = 0.f;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      Vec<1> f = {{make_float2(to_f32(((const T*)a.x)[row * a.ldx + c]), 0.f)}};
+      Vec<1> f = {{to_f32(((const T*)a.x)[row * a.ldx + c])}};
       if (a.h) {
         const float r = a.res ? to_f32(((const T*)a.res)[row * a.ldr + c]) : 0.f;
         drop_run(a.d, (uint64_t)row * a.cols + c, f);
-        const T v = from_f32<T>(a.res ? __fadd_rn(r, f.p[0].x) : f.p[0].x);
+        const T v = from_f32<T>(a.res ? __fadd_rn(r, f.p[0]) : f.p[0]);
         ((T*)a.h)[row * a.ldh + c] = v;
-        f.p[0].x = to_f32(v);
+        f.p[0] = to_f32(v);
       }
-      sum += f.p[0].x;
+      sum += f.p[0];
     }
     const float mean = row_sum<1024, 1024>(sum, red[0]) * inv;
     float sq = 0.f;
@@ -322,14 +340,14 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
       const float f = to_f32(src[c]) - mean;
       sq += f * f;
     }
-    const float rstd = 1.f / sqrtf(row_sum<1024, 1024>(sq, red[1]) * inv + a.eps);
+    const float rstd = inverse_root(row_sum<1024, 1024>(sq, red[1]) * inv + a.eps);
     if (threadIdx.x == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0].x;
-      const float b = a.b ? load_weight<T, 1>(a.b, a.w32, c).p[0].x : 0.f;
+      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
+      const float b = a.b ? load_weight<T, 1>(a.b, a.w32, c).p[0] : 0.f;
       ((T*)a.y)[row * a.ldy + c] = from_f32<T>((to_f32(src[c]) - mean) * rstd * w + b);
     }
   }
@@ -352,63 +370,102 @@ __device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c,
 
 template <int U>
 __device__ __forceinline__ float at(const Vec<U>& v, int k) {
-  return k & 1 ? v.p[k / 2].y : v.p[k / 2].x;
+  if constexpr (U == 1)
+    return v.p[0];
+  else
+    return k & 1 ? v.p[k / 2].y : v.p[k / 2].x;
 }
 
-// As the forward kernel, with the row kept as it was loaded.  A block walks
-// the rows with a stride and sums its columns' weight gradients, in registers
-// or (SMEM: rows of 1024 threads, which leave no registers) in shared memory
-// at places of the thread's own; each block writes one part at its end.  The
-// next row's loads are on their way while this row's two sums are exchanged
-// (where the registers hold two rows).
+// A block walks the rows with a stride and sums its columns' weight gradients,
+// in registers or (SMEM: rows of 1024 threads, which leave no registers) in
+// shared memory at places of the thread's own; each block writes one part at
+// its end.
+//
+// 16-byte runs (U > 1) come through shared memory by asynchronous copies of
+// kDepth rows ahead; a thread copies and reads its own runs alone, so that no
+// thread waits for another's, and the registers are left to the sums.
+template <int U, bool SMEM>
+constexpr int kDepth = U > 1 && !SMEM ? 2 : 0;
+
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(smem)),
+               "l"(global)
+               : "memory");
+}
+
 template <class T, int U, int TPR, int N, bool SMEM>
-__global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
+__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_of(TPR))
     norm_bwd_kernel(const __grid_constant__ NormBwd a) {
-  constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR;
-  extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums
-  __shared__ float2 red[2][kBlock / 32];
+  constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR, D = kDepth<U, SMEM>;
+  extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums; else the rows ahead
+  __shared__ __align__(16) float2 red[2][kBlock / 32];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.cols;
+  using E = typename Vec<U>::E;
   constexpr int P = Vec<U>::P;
   Vec<U> dw[SMEM ? 1 : N], db[SMEM ? 1 : N];
   // (SMEM: run n of thread t at element (n * TPR + t) * U of each half)
-  float2* sums = reinterpret_cast<float2*>(dyn);
-  constexpr int kHalf = N * TPR * U / 2;  // pairs
+  E* sums = reinterpret_cast<E*>(dyn);
+  constexpr int kHalf = N * TPR * P;
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      if constexpr (!SMEM)
-        dw[n].p[k] = db[n].p[k] = both(0.f);
-      else if constexpr (U > 1)
-        sums[(n * TPR + t) * P + k] = sums[kHalf + (n * TPR + t) * P + k] = both(0.f);
+      if constexpr (SMEM)
+        sums[(n * TPR + t) * P + k] = sums[kHalf + (n * TPR + t) * P + k] = all_of<E>(0.f);
       else
-        dyn[n * TPR + t] = dyn[2 * kHalf + n * TPR + t] = 0.f;
+        dw[n].p[k] = db[n].p[k] = all_of<E>(0.f);
     }
-  Run<T, U> dy[N], h[N], dh[N];
-  float mean = 0.f, rstd = 0.f;
-  auto load_row = [&](int64_t row) {
-    if (row >= a.rows) return;
-    mean = a.mean[row], rstd = a.rstd[row];
+  // rows ahead: [slot][array][run][thread]
+  Run<T, U>* ahead = reinterpret_cast<Run<T, U>*>(dyn) + threadIdx.x;
+  auto slot_of = [&](int slot, int array, int n) {
+    return ahead + ((slot * 3 + array) * N + n) * kBlock;
+  };
+  auto fetch = [&](int slot, int64_t row) {
+    if (row < a.rows) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (c < a.cols) {
-        dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c);
-        h[n] = raw_run<T, U>(a.h, row * a.ldh + c);
-        if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c);
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * TPR + t) * U;
+        if (c < a.cols) {
+          copy16(slot_of(slot, 0, n), (const T*)a.dy + row * a.lddy + c);
+          copy16(slot_of(slot, 1, n), (const T*)a.h + row * a.ldh + c);
+          if (a.dh) copy16(slot_of(slot, 2, n), (const T*)a.dh + row * a.lddh + c);
+        }
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  int turn = 0;
-  if (!SMEM) load_row((int64_t)blockIdx.x * RPB + group);
+  const int64_t first = (int64_t)blockIdx.x * RPB + group;
+  if constexpr (D > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, first + d * step);
+  }
+  int turn = 0, slot = 0;
+  float mean = first < a.rows ? a.mean[first] : 0.f, rstd = first < a.rows ? a.rstd[first] : 0.f;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
     const int64_t row = base + group;
     const bool live = row < a.rows;
-    if (SMEM) load_row(row);
-    float2 s1 = both(0.f), s2 = both(0.f);
+    if constexpr (D > 0) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    Run<T, U> dy[N], h[N], dh[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        if constexpr (D > 0) {
+          dy[n] = *slot_of(slot, 0, n);
+          h[n] = *slot_of(slot, 1, n);
+        } else {
+          dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c);
+          h[n] = raw_run<T, U>(a.h, row * a.ldh + c);
+          if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c);
+        }
+      }
+    }
+    E s1 = all_of<E>(0.f), s2 = all_of<E>(0.f);
+    Vec<U> hat[N], wdy[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
@@ -416,50 +473,45 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
         const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy[n]), x = unpack(h[n]);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          const float2 hat = mul2(add2(x.p[k], both(-mean)), both(rstd));
-          const float2 wdy = mul2(y.p[k], w.p[k]);
-          s1 = add2(s1, wdy);
-          s2 = fma2(wdy, hat, s2);
-          if constexpr (!SMEM) {
-            dw[n].p[k] = fma2(y.p[k], hat, dw[n].p[k]);
-            db[n].p[k] = add2(db[n].p[k], y.p[k]);
-          } else if constexpr (U > 1) {
-            float2* q = sums + (n * TPR + t) * P + k;
-            q[0] = fma2(y.p[k], hat, q[0]);
+          hat[n].p[k] = mul2(add2(x.p[k], all_of<E>(-mean)), all_of<E>(rstd));
+          wdy[n].p[k] = mul2(y.p[k], w.p[k]);
+          s1 = add2(s1, wdy[n].p[k]);
+          s2 = fma2(wdy[n].p[k], hat[n].p[k], s2);
+          if constexpr (SMEM) {
+            E* q = sums + (n * TPR + t) * P + k;
+            q[0] = fma2(y.p[k], hat[n].p[k], q[0]);
             q[kHalf] = add2(q[kHalf], y.p[k]);
           } else {
-            float* q = dyn + n * TPR + t;
-            q[0] += y.p[k].x * hat.x;
-            q[2 * kHalf] += y.p[k].x;
+            dw[n].p[k] = fma2(y.p[k], hat[n].p[k], dw[n].p[k]);
+            db[n].p[k] = add2(db[n].p[k], y.p[k]);
           }
         }
       }
     }
-    // this row stays for its gradient, the next one comes in
-    Run<T, U> dy0[N], h0[N], dh0[N];
-    const float mean0 = mean, rstd0 = rstd;
-#pragma unroll
-    for (int n = 0; n < N; ++n) dy0[n] = dy[n], h0[n] = h[n], dh0[n] = dh[n];
-    if (!SMEM) load_row(row + step);
-    // (one element alone: the second half of its pairs is 0 times something)
-    const float2 s = U > 1 ? row_sum2<TPR, kBlock>(s1.x + s1.y, s2.x + s2.y, red[turn])
-                           : row_sum2<TPR, kBlock>(s1.x, s2.x, red[turn]);
+    const float rstd0 = rstd;
+    if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
+    const float2 s = row_sum2<TPR, kBlock>(total(s1), total(s2), red[turn]);
     const float m1 = s.x * inv, m2 = s.y * inv;
     turn ^= 1;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * TPR + t) * U;
       if (live && c < a.cols) {
-        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy0[n]), x = unpack(h0[n]);
+        if constexpr (D > 0) {
+          if (a.dh) dh[n] = *slot_of(slot, 2, n);
+        }
         Vec<U> g;
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          const float2 hat = mul2(add2(x.p[k], both(-mean0)), both(rstd0));
-          g.p[k] = fma2(y.p[k], w.p[k], both(-m1));
-          g.p[k] = mul2(fma2(hat, both(-m2), g.p[k]), both(rstd0));
+          g.p[k] = add2(wdy[n].p[k], all_of<E>(-m1));
+          g.p[k] = mul2(fma2(hat[n].p[k], all_of<E>(-m2), g.p[k]), all_of<E>(rstd0));
         }
-        write_grad(a, row, c, g, dh0[n]);
+        write_grad(a, row, c, g, dh[n]);
       }
+    }
+    if constexpr (D > 0) {
+      fetch(slot, row + D * step);
+      slot = slot + 1 == D ? 0 : slot + 1;
     }
   }
   // this block's part of the weight gradient: the groups' sums in order
@@ -488,7 +540,7 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             if constexpr (SMEM)
-              part[which * a.cols + c + k] = dyn[which * 2 * kHalf + c + k];
+              part[which * a.cols + c + k] = dyn[which * N * TPR * U + c + k];
             else
               part[which * a.cols + c + k] = at<U>(which ? db[n] : dw[n], k);
           }
@@ -502,7 +554,7 @@ __global__ void __launch_bounds__(block_of(TPR), TPR >= 512 ? 1 : 2)
 // row) and the columns' partial sums in kernels of their own.
 template <class T>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_constant__ NormBwd a) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   const float inv = 1.f / (float)a.cols;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -511,7 +563,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
     const T* h = (const T*)a.h + row * a.ldh;
     float s1 = 0.f, s2 = 0.f;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float wdy = to_f32(dy[c]) * load_weight<T, 1>(a.w, a.w32, c).p[0].x;
+      const float wdy = to_f32(dy[c]) * load_weight<T, 1>(a.w, a.w32, c).p[0];
       s1 += wdy;
       s2 += wdy * ((to_f32(h[c]) - mean) * rstd);
     }
@@ -519,9 +571,9 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
     s1 = s.x * inv, s2 = s.y * inv;
     turn ^= 1;
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0].x;
+      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
       const float hat = (to_f32(h[c]) - mean) * rstd;
-      Vec<1> g = {{make_float2(rstd * (to_f32(dy[c]) * w - s1 - hat * s2), 0.f)}};
+      Vec<1> g = {{rstd * (to_f32(dy[c]) * w - s1 - hat * s2)}};
       Run<T, 1> d;
       if (a.dh) d = raw_run<T, 1>(a.dh, row * a.lddh + c);
       write_grad(a, row, c, g, d);
@@ -569,28 +621,33 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int 
 // Partial sums kept at most (the workspace's size does not depend on the GPU).
 constexpr int kMaxParts = 608;
 
-// A thread's share of a row: 32 bytes in two 16-byte runs, or 8 elements one
-// by one where the rows are not 16-byte aligned.
-template <class T, int U>
-constexpr int kRuns = U > 1 ? 2 : 8;
+// A thread's share of a row: `runs` 16-byte runs (four, so that what a thread
+// does once per row weighs little; two in the backward pass, which keeps two
+// sums for each element), or 8 elements one by one where the rows are not
+// 16-byte aligned.
+template <int U>
+constexpr int kFwdRuns = U > 1 ? 4 : 8;
+template <int U>
+constexpr int kBwdRuns = U > 1 ? 2 : 8;
 
-// Threads per row that hold `cols` in their shares; 0: too wide.
-template <class T, int U>
-int row_threads(int cols) {
+// Threads per row that hold `cols` in shares of `share` elements; 0: too wide.
+inline int row_threads(int cols, int share) {
   for (int t : {32, 128, 256, 512, 1024})
-    if (cols <= t * U * kRuns<T, U>) return t;
+    if (cols <= t * share) return t;
   return 0;
 }
 
 template <class T, int U>
 int launch_fwd(const NormFwd& a, cudaStream_t s) {
-  constexpr int N = kRuns<T, U>;
-  const int tpr = row_threads<T, U>(a.cols);
-  const int rpb = tpr >= 256 || !tpr ? 1 : 256 / tpr;
-  const unsigned grid = (unsigned)std::min<int64_t>((a.rows + rpb - 1) / rpb, 1 << 20);
+  constexpr int N = kFwdRuns<U>;
+  const int tpr = row_threads(a.cols, U * N);
+  const int rpb = tpr == 32 ? 4 : 1;
+  const int64_t blocks = (a.rows + rpb - 1) / rpb;
+  if (blocks > 0x7FFFFFFF) return ROT_EINVAL;
+  const unsigned grid = (unsigned)blocks;
   switch (tpr) {
-    case 32: norm_fwd_kernel<T, U, 32, N><<<grid, 256, 0, s>>>(a); break;
-    case 128: norm_fwd_kernel<T, U, 128, N><<<grid, 256, 0, s>>>(a); break;
+    case 32: norm_fwd_kernel<T, U, 32, N><<<grid, 128, 0, s>>>(a); break;
+    case 128: norm_fwd_kernel<T, U, 128, N><<<grid, 128, 0, s>>>(a); break;
     case 256: norm_fwd_kernel<T, U, 256, N><<<grid, 256, 0, s>>>(a); break;
     case 512: norm_fwd_kernel<T, U, 512, N><<<grid, 512, 0, s>>>(a); break;
     case 1024: norm_fwd_kernel<T, U, 1024, N><<<grid, 1024, 0, s>>>(a); break;
@@ -612,23 +669,24 @@ int run_fwd(const NormFwd& a, cudaStream_t s) {
 
 template <class T, int U, int TPR, bool SMEM>
 int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
-  constexpr int N = kRuns<T, U>, block = block_of(TPR), rpb = block / TPR;
-  constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : 0;
+  constexpr int N = kBwdRuns<U>, block = block_of(TPR), rpb = block / TPR;
+  constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : kDepth<U, SMEM> * 3 * N * block * 16;
   auto k = norm_bwd_kernel<T, U, TPR, N, SMEM>;
-  if constexpr (SMEM) {
+  if constexpr (smem > 0) {
     static const cudaError_t attr =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return ROT_ECUDA;
   }
+  const int per_sm = TPR == 1024 ? 1 : 512 / block;
   *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
-                                  std::min(kMaxParts, (TPR >= 512 ? 1 : 2) * sm_count()));
+                                  std::min(kMaxParts, per_sm * sm_count()));
   k<<<*parts, block, smem, s>>>(a);
   return launched();
 }
 
 template <class T, int U>
 int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
-  switch (row_threads<T, U>(a.cols)) {
+  switch (row_threads(a.cols, U * kBwdRuns<U>)) {
     case 32: return launch_bwd_rows<T, U, 32, false>(a, parts, s);
     case 128: return launch_bwd_rows<T, U, 128, false>(a, parts, s);
     case 256: return launch_bwd_rows<T, U, 256, false>(a, parts, s);
