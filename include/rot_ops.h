@@ -193,6 +193,39 @@ int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, in
                  int32_t b_block_rows, void* c, int64_t ldc, int32_t ctype, int32_t accumulate,
                  void* work, uint64_t work_bytes, int32_t* status, void* stream);
 
+/* ---- linear layers in 8 bits ---------------------------------------------
+ *
+ * y = x W^T with x (tokens x inner, F32, F16 or BF16) quantised by rows
+ * (E4M3, blocks of 1 x 128) and W (outer x inner) kept in 8 bits by the
+ * caller; and its gradients.  One call runs quantisation and products; the
+ * results are those of rot_fp8_quantize and rot_fp8_gemm.
+ */
+
+/* Workspace bytes (256-byte aligned device memory); 0 for sizes that are
+ * refused. */
+uint64_t rot_fp8_linear_work_bytes(int64_t tokens, int64_t inner, int64_t outer);
+uint64_t rot_fp8_linear_backward_work_bytes(int64_t tokens, int64_t inner, int64_t outer);
+
+/* y: tokens x outer of x's type.  w, w_scale: W as rot_fp8_gemm takes it.
+ * Errors: as rot_fp8_quantize and rot_fp8_gemm. */
+int rot_fp8_linear(int64_t tokens, int64_t inner, int64_t outer, const void* x, int64_t ldx,
+                   int32_t type, const void* w, int64_t ldw, int32_t w_format,
+                   const uint8_t* w_scale, int64_t w_lds, int32_t w_block_rows, void* y,
+                   int64_t ldy, void* work, uint64_t work_bytes, int32_t* status, void* stream);
+
+/* dx (tokens x inner of dy's type) = dy W, from W's transpose wt (inner x
+ * outer in 8 bits), dy quantised by rows; dw (outer x inner, float32: the
+ * optimizer's gradient) = dy^T x, or += with accumulate != 0, both operands
+ * quantised along the tokens.  dy: tokens x outer, x: tokens x inner, of one
+ * type.  tokens == 0 gives dw = 0 (or leaves it, accumulating).
+ * Errors: as rot_fp8_linear. */
+int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const void* dy,
+                            int64_t lddy, const void* x, int64_t ldx, int32_t type,
+                            const void* wt, int64_t ldwt, int32_t wt_format,
+                            const uint8_t* wt_scale, int64_t wt_lds, int32_t wt_block_rows,
+                            void* dx, int64_t lddx, float* dw, int64_t lddw, int32_t accumulate,
+                            void* work, uint64_t work_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -109,6 +109,13 @@ _SIGS = {
     "rot_fp8_gemm_work_bytes": (_u64, [_i64, _i64, _i64]),
     "rot_fp8_gemm": (_i32, [_i64, _i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i64, _i32,
                             _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _u64, _vp, _vp]),
+    "rot_fp8_linear_work_bytes": (_u64, [_i64, _i64, _i64]),
+    "rot_fp8_linear": (_i32, [_i64, _i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i64, _i32,
+                              _vp, _i64, _vp, _u64, _vp, _vp]),
+    "rot_fp8_linear_backward_work_bytes": (_u64, [_i64, _i64, _i64]),
+    "rot_fp8_linear_backward": (_i32, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64,
+                                       _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp,
+                                       _u64, _vp, _vp]),
     "rot_item_work": (_i32, [ctypes.POINTER(rot_shape), _i32, ctypes.POINTER(_u64)]),
     "rot_partition_static": (_i32, [ctypes.POINTER(_u64), _i32, ctypes.POINTER(_i32), _i32, _i32,
                                     ctypes.POINTER(_i32)]),

@@ -40,6 +40,32 @@ __host__ __device__ inline bool rows16(const void* p, int64_t ld, int es) {
   return !p || (aligned16(p) && (ld * es) % 16 == 0);
 }
 
+// Launches a kernel that begins with wait_for_prior(): its blocks may start
+// (set-up, no reads of earlier results) while the stream's kernel before it
+// ends.
+template <class... P, class... A>
+int launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                  cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  if (cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess) return ROT_OK;
+  cudaGetLastError();
+  return ROT_ECUDA;
+}
+// Waits until the stream's earlier kernels have ended and their writes are
+// visible.
+__device__ __forceinline__ void wait_for_prior() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The number of SMs of the current device (set up once, as rot.h states).
 inline int sm_count() {
   static const int n = [] {

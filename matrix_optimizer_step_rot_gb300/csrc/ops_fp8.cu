@@ -24,22 +24,6 @@ struct Quant {
   int e5m2, square;  // square: blocks of 128 x 128
 };
 
-// The scale's byte for a block whose largest finite magnitude is `amax`: the
-// least e >= -127 with amax <= max 2^e.  max is 1.75 2^top (448: top 8;
-// 57344: top 15), amax is m 2^k with m in [1, 2), so e = k - top, plus one
-// where m > 1.75.  Subnormal amax (and 0) end at -127.
-__device__ __forceinline__ int scale_byte(float amax, bool e5m2) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int k = (int)(bits >> 23) - 127;
-  const int e = k - (e5m2 ? 15 : 8) + ((bits & 0x7FFFFFu) > 0x600000u);
-  return max(e, -127) + 127;
-}
-// 2^-(byte - 127), a normal number for every byte up to 253 (scale_byte ends
-// at 247)
-__device__ __forceinline__ float inverse_scale(int byte) {
-  return __uint_as_float((uint32_t)(254 - byte) << 23);
-}
-
 // Two values as 8-bit floats, the first in the low byte.
 __device__ __forceinline__ uint32_t pair_f8(float x, float y, bool e5m2) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
@@ -333,7 +317,7 @@ int rot_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int
 }
 
 uint64_t rot_fp8_gemm_work_bytes(int64_t M, int64_t N, int64_t K) {
-  return fp8_work_bytes(M, N, K);
+  return fp8_few(M, K) ? 0 : fp8_work_bytes(M, N, K);
 }
 
 int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
@@ -362,7 +346,125 @@ int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, in
                    cudaSuccess
                ? ROT_OK
                : ROT_ECUDA;
-  return guarded([&] { return fp8_product(p, reinterpret_cast<int*>(status), s); });
+  return guarded([&] {
+    if (fp8_few(M, K)) return fp8_few_product(p, a, lda, a_format, s);
+    return fp8_product(p, reinterpret_cast<int*>(status), s);
+  });
+}
+
+namespace {
+
+// An 8-bit matrix in a workspace: rows x cols, one scale per row and 128
+// columns.
+struct Held {
+  uint8_t *q, *s;
+  int64_t ld, lds;
+};
+struct Carve {
+  char* base;
+  uint64_t at = 0;
+  char* take(uint64_t bytes) {
+    char* p = base ? base + at : nullptr;
+    at += align256(bytes);
+    return p;
+  }
+  Held matrix(int64_t rows, int64_t cols) {
+    Held h;
+    h.ld = up(cols, 16) * 16;
+    h.lds = rows;
+    h.q = reinterpret_cast<uint8_t*>(take((uint64_t)rows * h.ld));
+    h.s = reinterpret_cast<uint8_t*>(take((uint64_t)rows * up(cols, kQ)));
+    return h;
+  }
+};
+
+bool bad_layer(int64_t tokens, int64_t inner, int64_t outer) {
+  return tokens < 0 || inner < 0 || outer < 0 || tokens > kMost || inner > kMost || outer > kMost;
+}
+bool bad_work(const void* work, uint64_t have, uint64_t need) {
+  return need > 0 && (!work || have < need || (reinterpret_cast<uintptr_t>(work) & 255));
+}
+
+}  // namespace
+
+uint64_t rot_fp8_linear_work_bytes(int64_t tokens, int64_t inner, int64_t outer) {
+  if (bad_layer(tokens, inner, outer) || outer == 0 || fp8_few(tokens, inner)) return 0;
+  Carve c = {nullptr};
+  c.matrix(tokens, inner);
+  c.take(fp8_work_bytes(tokens, outer, inner));
+  return c.at;
+}
+
+int rot_fp8_linear(int64_t tokens, int64_t inner, int64_t outer, const void* x, int64_t ldx,
+                   int32_t type, const void* w, int64_t ldw, int32_t w_format,
+                   const uint8_t* w_scale, int64_t w_lds, int32_t w_block_rows, void* y,
+                   int64_t ldy, void* work, uint64_t work_bytes, int32_t* status, void* stream) {
+  if (bad_layer(tokens, inner, outer) || !float_type(type) || ldx < inner || ldy < outer ||
+      (tokens > 0 && inner > 0 && !x) ||
+      bad_operand(w, ldw, w_format, w_scale, w_lds, w_block_rows, outer, inner) ||
+      (tokens > 0 && outer > 0 && !y) ||
+      bad_work(work, work_bytes, rot_fp8_linear_work_bytes(tokens, inner, outer)))
+    return ROT_EINVAL;
+  if (tokens == 0 || outer == 0) return ROT_OK;
+  if (fp8_few(tokens, inner) && inner > 0) {
+    const int dev = check_device();
+    if (dev != ROT_OK) return dev;
+    Prod p = {nullptr, (const uint8_t*)w, nullptr, w_scale, y, 0, ldw, 0, w_lds, ldy,
+              (int)tokens, (int)outer, (int)inner, type, 0, 0, w_format == ROT_TYPE_E5M2,
+              0, w_block_rows == 1 ? 0 : 7, nullptr};
+    return guarded([&] { return fp8_few_product(p, x, ldx, type, static_cast<cudaStream_t>(stream)); });
+  }
+  Carve c = {static_cast<char*>(work)};
+  const Held q = c.matrix(tokens, inner);
+  const uint64_t more = fp8_work_bytes(tokens, outer, inner);
+  int e = rot_fp8_quantize(x, ldx, tokens, inner, type, ROT_TYPE_E4M3, 1, q.q, q.ld, q.s, q.lds,
+                           nullptr, 0, nullptr, 0, stream);
+  if (e != ROT_OK) return e;
+  return rot_fp8_gemm(tokens, outer, inner, q.q, q.ld, ROT_TYPE_E4M3, q.s, q.lds, 1, w, ldw,
+                      w_format, w_scale, w_lds, w_block_rows, y, ldy, type, 0, c.take(more), more,
+                      status, stream);
+}
+
+uint64_t rot_fp8_linear_backward_work_bytes(int64_t tokens, int64_t inner, int64_t outer) {
+  if (bad_layer(tokens, inner, outer)) return 0;
+  Carve c = {nullptr};
+  c.matrix(tokens, outer);
+  c.matrix(outer, tokens);
+  c.matrix(inner, tokens);
+  c.take(std::max(fp8_work_bytes(tokens, inner, outer), fp8_work_bytes(outer, inner, tokens)));
+  return c.at;
+}
+
+int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const void* dy,
+                            int64_t lddy, const void* x, int64_t ldx, int32_t type,
+                            const void* wt, int64_t ldwt, int32_t wt_format,
+                            const uint8_t* wt_scale, int64_t wt_lds, int32_t wt_block_rows,
+                            void* dx, int64_t lddx, float* dw, int64_t lddw, int32_t accumulate,
+                            void* work, uint64_t work_bytes, int32_t* status, void* stream) {
+  if (bad_layer(tokens, inner, outer) || !float_type(type) || lddy < outer || ldx < inner ||
+      lddx < inner || lddw < inner || (tokens > 0 && outer > 0 && !dy) ||
+      (tokens > 0 && inner > 0 && (!x || !dx)) || (inner > 0 && outer > 0 && !dw) ||
+      bad_operand(wt, ldwt, wt_format, wt_scale, wt_lds, wt_block_rows, inner, outer) ||
+      bad_work(work, work_bytes, rot_fp8_linear_backward_work_bytes(tokens, inner, outer)))
+    return ROT_EINVAL;
+  Carve c = {static_cast<char*>(work)};
+  const Held d = c.matrix(tokens, outer), dt = c.matrix(outer, tokens), xt = c.matrix(inner, tokens);
+  const uint64_t more =
+      std::max(fp8_work_bytes(tokens, inner, outer), fp8_work_bytes(outer, inner, tokens));
+  char* part = c.take(more);
+  int e = rot_fp8_quantize(dy, lddy, tokens, outer, type, ROT_TYPE_E4M3, 1, d.q, d.ld, d.s, d.lds,
+                           dt.q, dt.ld, dt.s, dt.lds, stream);
+  if (e == ROT_OK)
+    e = rot_fp8_quantize(x, ldx, tokens, inner, type, ROT_TYPE_E4M3, 1, nullptr, 0, nullptr, 0,
+                         xt.q, xt.ld, xt.s, xt.lds, stream);
+  if (e == ROT_OK)
+    e = rot_fp8_gemm(tokens, inner, outer, d.q, d.ld, ROT_TYPE_E4M3, d.s, d.lds, 1, wt, ldwt,
+                     wt_format, wt_scale, wt_lds, wt_block_rows, dx, lddx, type, 0, part, more,
+                     status, stream);
+  if (e != ROT_OK) return e;
+  return rot_fp8_gemm(outer, inner, tokens, dt.q, dt.ld, ROT_TYPE_E4M3, dt.s, dt.lds, 1, xt.q,
+                      xt.ld, ROT_TYPE_E4M3, xt.s, xt.lds, 1, dw, lddw, ROT_TYPE_F32, accumulate,
+                      part, more, status, stream);
 }
 
 }  // extern "C"

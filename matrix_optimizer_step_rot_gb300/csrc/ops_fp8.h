@@ -2,7 +2,9 @@
 // kernels (ops_fp8_gemm.cu).
 #pragma once
 
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 namespace rot {
@@ -20,8 +22,42 @@ struct Prod {
   float* part;   // workspace
 };
 
+// Products with few rows (ops_fp8_few.cu), from x in 8 bits (its scales in p) or
+// in a float type, which is then rounded as rot_fp8_quantize does.
+bool fp8_few(int64_t M, int64_t K);
+int fp8_few_product(const Prod& p, const void* x, int64_t ldx, int32_t xtype, cudaStream_t stream);
+
 uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K);
 int fp8_product(const Prod& p, int* status, cudaStream_t stream);
+
+// The scale's byte for a block whose largest finite magnitude is `amax`: the
+// least e >= -127 with amax <= max 2^e.  max is 1.75 2^top (448: top 8;
+// 57344: top 15), amax is m 2^k with m in [1, 2), so e = k - top, plus one
+// where m > 1.75.  Subnormal amax (and 0) end at -127.
+__device__ __forceinline__ int scale_byte(float amax, bool e5m2) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int k = (int)(bits >> 23) - 127;
+  const int e = k - (e5m2 ? 15 : 8) + ((bits & 0x7FFFFFu) > 0x600000u);
+  return max(e, -127) + 127;
+}
+// 2^-(byte - 127), a normal number for every byte up to 253 (scale_byte ends
+// at 247)
+__device__ __forceinline__ float inverse_scale(int byte) {
+  return __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;
+}
+
+// 8 bits of x * inv (at most max in magnitude by choice of inv); NaN and
+// infinities become NaN.
+__device__ __forceinline__ uint32_t to_f8(float x, float inv, bool e5m2) {
+  float v = x * inv;
+  if (!(fabsf(x) < INFINITY)) v = NAN;
+  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
 
 }  // namespace ops
 }  // namespace rot

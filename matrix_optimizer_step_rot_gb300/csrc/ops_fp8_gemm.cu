@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_prior();  // (the operands may come from the kernel before)
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ loads
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 // C from the parts, added in order of K.
 __global__ void __launch_bounds__(256) fp8_join_kernel(const Prod p, int splits, int64_t ldp) {
   const int64_t total = (int64_t)p.M * p.N;
+  wait_for_prior();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / p.N, n = i - m * p.N;
@@ -443,15 +445,14 @@ int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
   g.limit_ns = g_wait_limit_ns;
   {
     ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * p.M * (double)p.N * p.K, stream);
-    fp8_gemm_kernel<<<(unsigned)std::min<int64_t>(g.units, sm_count()), kThreads, kSmem, stream>>>(g);
-    e = launched();
+    e = launch_behind(fp8_gemm_kernel, (unsigned)std::min<int64_t>(g.units, sm_count()), kThreads,
+                      kSmem, stream, g);
   }
   if (e != ROT_OK || s.splits == 1) return e;
   ProfScope prof(ROT_PROF_ELEMENTWISE, 4.0 * (s.splits + 1) * p.M * (double)p.N, stream);
   const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
-  fp8_join_kernel<<<(unsigned)std::min<int64_t>(blocks, 8ll * sm_count()), 256, 0, stream>>>(
-      p, (int)s.splits, s.ldp);
-  return launched();
+  return launch_behind(fp8_join_kernel, (unsigned)std::min<int64_t>(blocks, 8ll * sm_count()), 256, 0,
+                       stream, p, (int)s.splits, s.ldp);
 }
 
 }  // namespace ops

@@ -243,73 +243,71 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 640 / block_o
   __shared__ __align__(16) float red[2][kBlock / 32];
   const int t = threadIdx.x % TPR;
   const float inv = 1.f / (float)a.cols;
-  {
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    const bool live = row < a.rows;
-    Run<T, U> x[N], r[N];
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = row < a.rows;
+  Run<T, U> x[N], r[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (live && c < a.cols) {
-        x[n] = raw_run<T, U>(a.x, row * a.ldx + c);
-        if (a.res) r[n] = raw_run<T, U>(a.res, row * a.ldr + c);
-      }
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * TPR + t) * U;
+    if (live && c < a.cols) {
+      x[n] = raw_run<T, U>(a.x, row * a.ldx + c);
+      if (a.res) r[n] = raw_run<T, U>(a.res, row * a.ldr + c);
     }
-    Vec<U> h[N];
-    using E = typename Vec<U>::E;
-    constexpr int P = Vec<U>::P;
-    E sum = all_of<E>(0.f);
+  }
+  Vec<U> h[N];
+  using E = typename Vec<U>::E;
+  constexpr int P = Vec<U>::P;
+  E sum = all_of<E>(0.f);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * TPR + t) * U;
 #pragma unroll
-      for (int k = 0; k < P; ++k) h[n].p[k] = all_of<E>(0.f);
-      if (live && c < a.cols) {
-        h[n] = unpack(x[n]);
-        if (a.h) {
-          drop_run(a.d, (uint64_t)row * a.cols + c, h[n]);
-          if (a.res) {
-            const Vec<U> v = unpack(r[n]);
+    for (int k = 0; k < P; ++k) h[n].p[k] = all_of<E>(0.f);
+    if (live && c < a.cols) {
+      h[n] = unpack(x[n]);
+      if (a.h) {
+        drop_run(a.d, (uint64_t)row * a.cols + c, h[n]);
+        if (a.res) {
+          const Vec<U> v = unpack(r[n]);
 #pragma unroll
-            for (int k = 0; k < P; ++k) h[n].p[k] = add2(v.p[k], h[n].p[k]);
-          }
-          const Run<T, U> stored = pack<T>(h[n]);
-          put_run(a.h, row * a.ldh + c, stored);
-          h[n] = unpack(stored);  // the norm reads what is stored
+          for (int k = 0; k < P; ++k) h[n].p[k] = add2(v.p[k], h[n].p[k]);
         }
+        const Run<T, U> stored = pack<T>(h[n]);
+        put_run(a.h, row * a.ldh + c, stored);
+        h[n] = unpack(stored);  // the norm reads what is stored
+      }
 #pragma unroll
-        for (int k = 0; k < P; ++k) sum = add2(sum, h[n].p[k]);
+      for (int k = 0; k < P; ++k) sum = add2(sum, h[n].p[k]);
+    }
+  }
+  const float mean = row_sum<TPR, kBlock>(total(sum), red[0]) * inv;
+  E sq = all_of<E>(0.f);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if ((n * TPR + t) * U < a.cols) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        h[n].p[k] = add2(h[n].p[k], all_of<E>(-mean));
+        sq = fma2(h[n].p[k], h[n].p[k], sq);
       }
     }
-    const float mean = row_sum<TPR, kBlock>(total(sum), red[0]) * inv;
-    E sq = all_of<E>(0.f);
+  const float rstd = inverse_root(row_sum<TPR, kBlock>(total(sq), red[1]) * inv + a.eps);
+  if (live && t == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if ((n * TPR + t) * U < a.cols) {
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * TPR + t) * U;
+    if (live && c < a.cols) {
+      const Vec<U> w = load_weight<T, U>(a.w, a.w32, c);
+      Vec<U> b;
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          h[n].p[k] = add2(h[n].p[k], all_of<E>(-mean));
-          sq = fma2(h[n].p[k], h[n].p[k], sq);
-        }
-      }
-    const float rstd = inverse_root(row_sum<TPR, kBlock>(total(sq), red[1]) * inv + a.eps);
-    if (live && t == 0) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
+      for (int k = 0; k < P; ++k) b.p[k] = all_of<E>(0.f);
+      if (a.b) b = load_weight<T, U>(a.b, a.w32, c);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (live && c < a.cols) {
-        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c);
-        Vec<U> b;
-#pragma unroll
-        for (int k = 0; k < P; ++k) b.p[k] = all_of<E>(0.f);
-        if (a.b) b = load_weight<T, U>(a.b, a.w32, c);
-#pragma unroll
-        for (int k = 0; k < P; ++k) h[n].p[k] = fma2(mul2(h[n].p[k], all_of<E>(rstd)), w.p[k], b.p[k]);
-        put_run(a.y, row * a.ldy + c, pack<T>(h[n]));
-      }
+      for (int k = 0; k < P; ++k) h[n].p[k] = fma2(mul2(h[n].p[k], all_of<E>(rstd)), w.p[k], b.p[k]);
+      put_run(a.y, row * a.ldy + c, pack<T>(h[n]));
     }
   }
 }
@@ -601,6 +599,7 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const __grid_constan
 __global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int parts, int cols,
                                                          float* dweight, float* dbias) {
   __shared__ float share[32][33];
+  wait_for_prior();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * 32 + lane, width = 2ll * cols;
   float sum = 0.f;
@@ -718,8 +717,8 @@ int run_bwd(const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
   }
   if (e != ROT_OK) return e;
   ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
-  norm_join_kernel<<<(2 * a.cols + 31) / 32, 1024, 0, s>>>(a.part, parts, a.cols, dweight, dbias);
-  return launched();
+  return launch_behind(norm_join_kernel, (2 * a.cols + 31) / 32, 1024, 0, s, a.part, parts, a.cols,
+                       dweight, dbias);
 }
 
 template <template <class> class Fn, class... Args>

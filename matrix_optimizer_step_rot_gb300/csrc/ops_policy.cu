@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kRow, 2) policy_kernel(const __grid_constant__
 __global__ void __launch_bounds__(1024) policy_sum_kernel(const float* terms, int64_t tokens,
                                                           float* loss) {
   __shared__ double red[32];
+  wait_for_prior();
   double sum = 0.0;
   for (int64_t i = threadIdx.x; i < tokens; i += 1024) sum += terms[i];
 #pragma unroll
@@ -352,8 +353,7 @@ int rot_policy_loss(const void* logits, int64_t ldl, const int64_t* targets, con
     const int e = launch_policy(a, type, s);
     if (e != ROT_OK) return e;
     ProfScope prof(ROT_PROF_ELEMENTWISE, 4.0 * tokens, s);
-    policy_sum_kernel<<<1, 1024, 0, s>>>(terms, tokens, loss);
-    return launched();
+    return launch_behind(policy_sum_kernel, 1, 1024, 0, s, terms, tokens, loss);
   });
 }
 

@@ -59,6 +59,11 @@ CALLS = {
                              qt=P, ldqt=16, st=P, ldst=8, stream=0),
     "rot_fp8_gemm": dict(M=4, N=8, K=16, a=P, lda=16, fa=E4M3, sa=P, ldsa=4, ra=1, b=P, ldb=16, fb=E4M3, sb=P, ldsb=1,
                          rb=128, c=P, ldc=8, ctype=F32, accumulate=0, work=P, work_bytes=1 << 30, status=0, stream=0),
+    "rot_fp8_linear": dict(tokens=40, inner=16, outer=8, x=P, ldx=16, type=BF16, w=P, ldw=16, fw=E4M3, sw=P, ldsw=1,
+                           rw=128, y=P, ldy=8, work=P, work_bytes=1 << 30, status=0, stream=0),
+    "rot_fp8_linear_backward": dict(tokens=40, inner=16, outer=8, dy=P, lddy=8, x=P, ldx=16, type=BF16, wt=P, ldwt=16,
+                                    fw=E4M3, sw=P, ldsw=1, rw=128, dx=P, lddx=16, dw=P, lddw=16, accumulate=0, work=P,
+                                    work_bytes=1 << 30, status=0, stream=0),
 }
 
 REFUSED = {
@@ -87,6 +92,13 @@ REFUSED = {
                      dict(a=P + 8), dict(b=P + 1), dict(lda=15), dict(lda=24), dict(ldb=8), dict(fa=F32), dict(fb=9),
                      dict(ra=2), dict(rb=64), dict(ldsa=3), dict(ldsb=0), dict(ldc=7), dict(ctype=E4M3),
                      dict(ctype=BF16, accumulate=1), dict(M=1 << 31)],
+    "rot_fp8_linear": [dict(tokens=-1), dict(inner=-1), dict(outer=-1), dict(x=0), dict(w=0), dict(sw=0), dict(y=0),
+                       dict(y=0, tokens=1), dict(ldx=15), dict(ldy=7), dict(ldw=8), dict(w=P + 4), dict(type=E4M3),
+                       dict(fw=F32), dict(rw=3), dict(ldsw=0), dict(work=0), dict(work=P + 64), dict(work_bytes=64)],
+    "rot_fp8_linear_backward": [dict(tokens=-1), dict(inner=-1), dict(outer=-1), dict(dy=0), dict(x=0), dict(wt=0),
+                                dict(sw=0), dict(dx=0), dict(dw=0), dict(lddy=7), dict(ldx=15), dict(lddx=15),
+                                dict(lddw=15), dict(ldwt=0), dict(type=9), dict(fw=F32), dict(rw=0), dict(work=0),
+                                dict(work=P + 64), dict(work_bytes=64)],
 }
 
 
@@ -110,7 +122,8 @@ def test_valid_calls_are_refused_for_want_of_a_gpu_alone(name):
     ("rot_layer_norm_forward", dict(rows=0, x=0, y=0, mean=0, rstd=0)),
     ("rot_token_logprobs", dict(tokens=0, logits=0, targets=0, logp=0)),
     ("rot_fp8_quantize", dict(rows=0, x=0)), ("rot_fp8_gemm", dict(M=0, a=0, sa=0)),
-    ("rot_fp8_gemm", dict(N=0, b=0, sb=0)), ("rot_fp8_gemm", dict(K=0, accumulate=1))])
+    ("rot_fp8_gemm", dict(N=0, b=0, sb=0)), ("rot_fp8_gemm", dict(K=0, accumulate=1)),
+    ("rot_fp8_linear", dict(tokens=0, x=0, y=0, work=0)), ("rot_fp8_linear", dict(outer=0, w=0, sw=0, y=0))])
 def test_nothing_to_do_needs_no_device(name, change):
     assert getattr(B.lib(), name)(*dict(CALLS[name], **change).values()) == B.ROT_OK
 

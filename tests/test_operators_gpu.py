@@ -544,6 +544,40 @@ def test_product(M, N, K, ra, rb, fa, fb):
     assert ops.status() == B.ROT_OK
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 1), (37, 2048), (700, 513), (6144, 640), (5, 12288)])
+def test_product_of_few_rows(M, N, K):
+    """Either side of the row count where another kernel takes over; a layer's
+    own rounding of x gives what fp8_quantize gives."""
+    g = gen(M + N + K)
+    x = spread(g, M, K, BF16)
+    a = ops.fp8_quantize(x)[0]
+    b = ops.fp8_quantize(spread(g, N, K, F32), block_rows=128)[0]
+    va, vb = ref.values(a), ref.values(b)
+    want, bound = va @ vb.t(), product_bound(va, vb, K)
+    near(ops.fp8_matmul(a, b), want, bound, "8-bit rows")
+    y = ops.fp8_linear(x, b)
+    near(y, want, bound + (want.abs() + bound) * U[BF16] * 1.01 + TINY[BF16], "layer")
+    c = torch.ones(M, N, device="cuda")
+    ops.fp8_matmul(a, b, out=c, accumulate=True)
+    near(c, 1 + want, bound + 2 * E * (want.abs() + 1), "accumulated")
+
+
+def test_layer_reads_a_weight_written_just_before():
+    """Back to back on one stream, each call's operands from the call before."""
+    g = gen(9)
+    for tokens in (1, 8, 300):
+        x = torch.randn(tokens, 2048, generator=g, device="cuda").to(BF16)
+        w = torch.randn(2048, 2048, generator=g, device="cuda") * 0.02
+        want = ops.fp8_linear(x, ops.fp8_quantize(w, block_rows=128)[0])
+        torch.cuda.synchronize()
+        for _ in range(20):
+            q = ops.fp8_quantize(torch.zeros_like(w), block_rows=128)[0]
+            y = ops.fp8_linear(x, ops.fp8_quantize(w, block_rows=128)[0])
+            y2 = ops.fp8_linear(x, q)
+        assert torch.equal(y, want) and not y2.any()
+
+
 def test_product_scales_reach_their_ends():
     """Scales 2^-127 .. 2^127 whose products stay in range, and a NaN scale,
     which reaches its row or columns alone."""
@@ -552,6 +586,9 @@ def test_product_scales_reach_their_ends():
     a.scale.fill_(0)     # 2^-127
     b.scale.fill_(254)   # 2^127
     near(ops.fp8_matmul(a, b), ref.values(a) @ ref.values(b).t(), product_bound(ref.values(a), ref.values(b), 300))
+    few = ops.Fp8Matrix(a.data[:3], a.scale[:, :3].contiguous(), 1)
+    near(ops.fp8_matmul(few, b), ref.values(few) @ ref.values(b).t(),
+         product_bound(ref.values(few), ref.values(b), 300))
     a.scale.fill_(127)
     b.scale.fill_(127)
     a.scale[1, 7] = 255
@@ -561,6 +598,8 @@ def test_product_scales_reach_their_ends():
     nan[7] = True
     nan[:, 128:256] = True
     assert torch.equal(torch.isnan(got), nan)
+    few = ops.Fp8Matrix(a.data[5:9], a.scale[:, 5:9].contiguous(), 1)
+    assert torch.equal(torch.isnan(ops.fp8_matmul(few, b)), nan[5:9])
 
 
 def test_product_nan_elements_stay_in_their_rows():
@@ -568,11 +607,13 @@ def test_product_nan_elements_stay_in_their_rows():
     x[130, 150] = float("nan")
     w = torch.randn(70, 200, generator=gen(4), device="cuda")
     w[3, 199] = float("inf")
-    got = ops.fp8_matmul(ops.fp8_quantize(x)[0], ops.fp8_quantize(w, block_rows=128)[0])
+    q, wq = ops.fp8_quantize(x)[0], ops.fp8_quantize(w, block_rows=128)[0]
+    got = ops.fp8_matmul(q, wq)
     nan = torch.zeros_like(got, dtype=torch.bool)
     nan[130] = True
     nan[:, 3] = True
     assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(torch.isnan(ops.fp8_linear(x[128:132], wq)), nan[128:132])
 
 
 def test_product_does_not_read_past_its_columns():
@@ -582,6 +623,8 @@ def test_product_does_not_read_past_its_columns():
     full[:, :37] = a.data.view(torch.uint8)
     dirty = ops.Fp8Matrix(full.view(E4)[:, :37], a.scale, 1)
     assert torch.equal(ops.fp8_matmul(dirty, dirty), ops.fp8_matmul(a, a))
+    few, clean = (ops.Fp8Matrix(m.data[:2], m.scale[:, :2].contiguous(), 1) for m in (dirty, a))
+    assert torch.equal(ops.fp8_matmul(few, dirty), ops.fp8_matmul(clean, a))
 
 
 def test_product_of_nothing():
