@@ -317,7 +317,7 @@ int rot_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int
 }
 
 uint64_t rot_fp8_gemm_work_bytes(int64_t M, int64_t N, int64_t K) {
-  return fp8_few(M, K) ? 0 : fp8_work_bytes(M, N, K);
+  return fp8_few(M, N, K) ? 0 : fp8_work_bytes(M, N, K);
 }
 
 int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
@@ -347,7 +347,7 @@ int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, in
                ? ROT_OK
                : ROT_ECUDA;
   return guarded([&] {
-    if (fp8_few(M, K)) return fp8_few_product(p, a, lda, a_format, s);
+    if (fp8_few(M, N, K)) return fp8_few_product(p, a, lda, a_format, s);
     return fp8_product(p, reinterpret_cast<int*>(status), s);
   });
 }
@@ -388,10 +388,10 @@ bool bad_work(const void* work, uint64_t have, uint64_t need) {
 }  // namespace
 
 uint64_t rot_fp8_linear_work_bytes(int64_t tokens, int64_t inner, int64_t outer) {
-  if (bad_layer(tokens, inner, outer) || outer == 0 || fp8_few(tokens, inner)) return 0;
+  if (bad_layer(tokens, inner, outer) || outer == 0 || fp8_self_rounded(tokens, outer, inner)) return 0;
   Carve c = {nullptr};
   c.matrix(tokens, inner);
-  c.take(fp8_work_bytes(tokens, outer, inner));
+  c.take(rot_fp8_gemm_work_bytes(tokens, outer, inner));
   return c.at;
 }
 
@@ -406,7 +406,7 @@ int rot_fp8_linear(int64_t tokens, int64_t inner, int64_t outer, const void* x, 
       bad_work(work, work_bytes, rot_fp8_linear_work_bytes(tokens, inner, outer)))
     return ROT_EINVAL;
   if (tokens == 0 || outer == 0) return ROT_OK;
-  if (fp8_few(tokens, inner) && inner > 0) {
+  if (fp8_self_rounded(tokens, outer, inner) && inner > 0) {
     const int dev = check_device();
     if (dev != ROT_OK) return dev;
     Prod p = {nullptr, (const uint8_t*)w, nullptr, w_scale, y, 0, ldw, 0, w_lds, ldy,
@@ -416,7 +416,7 @@ int rot_fp8_linear(int64_t tokens, int64_t inner, int64_t outer, const void* x, 
   }
   Carve c = {static_cast<char*>(work)};
   const Held q = c.matrix(tokens, inner);
-  const uint64_t more = fp8_work_bytes(tokens, outer, inner);
+  const uint64_t more = rot_fp8_gemm_work_bytes(tokens, outer, inner);
   int e = rot_fp8_quantize(x, ldx, tokens, inner, type, ROT_TYPE_E4M3, 1, q.q, q.ld, q.s, q.lds,
                            nullptr, 0, nullptr, 0, stream);
   if (e != ROT_OK) return e;
@@ -431,7 +431,7 @@ uint64_t rot_fp8_linear_backward_work_bytes(int64_t tokens, int64_t inner, int64
   c.matrix(tokens, outer);
   c.matrix(outer, tokens);
   c.matrix(inner, tokens);
-  c.take(std::max(fp8_work_bytes(tokens, inner, outer), fp8_work_bytes(outer, inner, tokens)));
+  c.take(std::max(rot_fp8_gemm_work_bytes(tokens, inner, outer), rot_fp8_gemm_work_bytes(outer, inner, tokens)));
   return c.at;
 }
 
@@ -450,7 +450,7 @@ int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const 
   Carve c = {static_cast<char*>(work)};
   const Held d = c.matrix(tokens, outer), dt = c.matrix(outer, tokens), xt = c.matrix(inner, tokens);
   const uint64_t more =
-      std::max(fp8_work_bytes(tokens, inner, outer), fp8_work_bytes(outer, inner, tokens));
+      std::max(rot_fp8_gemm_work_bytes(tokens, inner, outer), rot_fp8_gemm_work_bytes(outer, inner, tokens));
   char* part = c.take(more);
   int e = rot_fp8_quantize(dy, lddy, tokens, outer, type, ROT_TYPE_E4M3, 1, d.q, d.ld, d.s, d.lds,
                            dt.q, dt.ld, dt.s, dt.lds, stream);

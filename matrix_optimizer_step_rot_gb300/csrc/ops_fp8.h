@@ -22,9 +22,11 @@ struct Prod {
   float* part;   // workspace
 };
 
-// Products with few rows (ops_fp8_few.cu), from x in 8 bits (its scales in p) or
-// in a float type, which is then rounded as rot_fp8_quantize does.
-bool fp8_few(int64_t M, int64_t K);
+// Products with few rows of A (ops_fp8_few.cu): fp8_few where that kernel
+// takes them in 8 bits (their scales in p), fp8_self_rounded where it takes
+// them in a float type too and rounds them as rot_fp8_quantize does.
+bool fp8_few(int64_t M, int64_t N, int64_t K);
+bool fp8_self_rounded(int64_t M, int64_t N, int64_t K);
 int fp8_few_product(const Prod& p, const void* x, int64_t ldx, int32_t xtype, cudaStream_t stream);
 
 uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K);
