@@ -39,10 +39,12 @@ constexpr int BM = 128, BN = 192, BK = 128;
 constexpr int kStages = 5;
 constexpr int kABytes = BM * BK, kBBytes = BN * BK, kStageBytes = kABytes + kBBytes;
 constexpr int kScaleBytes = 512 + 1024;  // per stage: A's 128 rows, B's 192 (of 256)
-constexpr int kSmem = 1024 + kStages * (kStageBytes + kScaleBytes) + 256;
-static_assert(kSmem <= 232448, "dynamic shared memory above 227 KB");
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8, kEpiCols = BN / 2;
+constexpr int kStagingBytes = 32 * 64;  // per epilogue warp
+constexpr int kSmem =
+    1024 + kStages * (kStageBytes + kScaleBytes) + kEpiWarps * kStagingBytes + 256;
+static_assert(kSmem <= 232448, "dynamic shared memory above 227 KB");
 constexpr int kStretch = 4;  // K blocks an accumulator takes
 constexpr int kScaleCols = 12;  // TMEM columns of a stage's scales: 4 of A, 8 of B
 constexpr int kTmemCols = 512;
@@ -88,30 +90,70 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t l
   }
 }
 
-// 32 columns of one row of C, from column n.
+// A warp's 32 rows of C, 64 bytes of each (U = 64 / sizeof(T) columns), of
+// which this thread holds row `lane`: staged in 2 KB of shared memory, so that
+// the warp then stores eight whole 64-byte pieces of rows at a time (one row
+// per thread would store 16 bytes of 32 rows).  16-byte piece c of row r is at
+// place c ^ (r / 2 & 3) of the row: neither side has bank conflicts.
 template <class T>
-__device__ __forceinline__ void store_cols(T* c, const float* acc, int ncol, bool wide,
-                                           bool accumulate) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, T* c, int64_t ldc, int rows, int cols,
+                                           const float* v, bool wide, bool accumulate) {
   constexpr int U = 16 / sizeof(T);
-  if (wide && ncol >= 32) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; i += U) {
-      float f[U];
+  for (int i = 0; i < 4; ++i) {
+    float f[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) f[k] = acc[i + k];
-      if (accumulate) {
-        float o[U];
-        load_run(c + i, o);
-#pragma unroll
-        for (int k = 0; k < U; ++k) f[k] += o[k];
-      }
-      store_run(c + i, f);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < ncol) c[i] = from_f32<T>(accumulate ? to_f32(c[i]) + acc[i] : acc[i]);
+    for (int k = 0; k < U; ++k) f[k] = v[i * U + k];
+    store_run(reinterpret_cast<T*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)), f);
   }
+  __syncwarp();
+  if (wide) {
+    const int i = lane & 3;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = 8 * q + (lane >> 2);
+      if (r >= rows || i * U >= cols) continue;
+      const T* p = reinterpret_cast<const T*>(stage + r * 64 + ((i ^ (r >> 1 & 3)) << 4));
+      T* o = c + r * ldc + i * U;
+      if (i * U + U <= cols) {
+        float f[U];
+        load_run(p, f);
+        if (accumulate) {
+          float old[U];
+          load_run(o, old);
+#pragma unroll
+          for (int k = 0; k < U; ++k) f[k] += old[k];
+        }
+        store_run(o, f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          if (i * U + k < cols) o[k] = accumulate ? from_f32<T>(to_f32(o[k]) + to_f32(p[k])) : p[k];
+      }
+    }
+  } else {  // rows that are not 16-byte aligned: a row's columns side by side
+#pragma unroll 1
+    for (int e = lane; e < 32 * 4 * U; e += 32) {
+      const int r = e / (4 * U), k = e % (4 * U);
+      if (r >= rows || k >= cols) continue;
+      const T x = *reinterpret_cast<const T*>(stage + r * 64 + (((k / U) ^ (r >> 1 & 3)) << 4) +
+                                              k % U * sizeof(T));
+      T* o = c + r * ldc + k;
+      *o = accumulate ? from_f32<T>(to_f32(*o) + to_f32(x)) : x;
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_tile(uint8_t* stage, T* c, int64_t ldc, int rows, int cols,
+                                           const float* sum, bool accumulate) {
+  constexpr int W = 64 / sizeof(T);
+  const bool wide = rows16(c, ldc, sizeof(T));
+#pragma unroll
+  for (int n = 0; n < kEpiCols; n += W)
+    if (n < cols) store_rows(stage, c + n, ldc, rows, cols - n, sum + n, wide, accumulate);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Mx g) {
@@ -119,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* scales = smem + kStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kStages * kScaleBytes);
+  uint8_t* staging = scales + kStages * kScaleBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStagingBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
@@ -184,10 +227,36 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issue
+    // Copies and MMAs run in the order of issue, and an MMA waits for its
+    // scales' copy: each block's copies are issued one block of MMAs ahead.
     const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    int64_t blocks = 0;  // K blocks of this CTA's units
+    for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {
+      const Unit t = unit_of(g, u);
+      blocks += t.k1 - t.k0;
+    }
+    int stage = 0, ahead = 0, acc = 0;
+    uint32_t ahead_phase = 0, acc_phase = 0;
     bool ok = true;
+    auto copy_scales = [&]() {  // of the next block to come
+      if (blocks == 0) return;
+      --blocks;
+      if (!ptx::mbar_wait(&full[ahead], ahead_phase, abort_flag, limit)) {
+        ok = false;
+        return;
+      }
+      ptx::tc_fence_after();
+      const uint32_t sc = ptx::smem_u32(scales + ahead * kScaleBytes);
+      const uint32_t sf = tmem + (uint32_t)(2 * BN + ahead * kScaleCols);
+      ptx::tmem_cp_32x128b_x4(sf, ptx::rows16_desc(sc));
+      ptx::tmem_cp_32x128b_x4(sf + 4, ptx::rows16_desc(sc + 512));
+      ptx::tmem_cp_32x128b_x4(sf + 8, ptx::rows16_desc(sc + 1024));
+      if (++ahead == kStages) {
+        ahead = 0;
+        ahead_phase ^= 1u;
+      }
+    };
+    copy_scales();
     for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
@@ -199,16 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         const int k1 = min(t.k1, kb + kStretch);
         for (int k = kb; k < k1; ++k) {
-          if (!ptx::mbar_wait(&full[stage], phase, abort_flag, limit)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t sc = ptx::smem_u32(scales + stage * kScaleBytes);
+          copy_scales();
+          if (!ok) break;
           const uint32_t sfa = tmem + (uint32_t)(2 * BN + stage * kScaleCols), sfb = sfa + 4;
-          ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
-          ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
-          ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
           const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
           const uint64_t da = ptx::sw128_kmajor_desc(st);
           const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
@@ -217,10 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), idesc, sfa, sfb,
                            (k > kb || i > 0) ? 1u : 0u);
           ptx::umma_commit(&empty[stage]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (++stage == kStages) stage = 0;
         }
         if (!ok) break;
         ptx::umma_commit(&tfull[acc]);
@@ -315,24 +374,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      const int row = t.m0 + quarter * 32 + lane, n0 = t.n0 + half * kEpiCols;
-      if (!ok || row >= p.M) continue;
-#pragma unroll
-      for (int c = 0; c < kEpiCols; c += 32) {
-        const int n = n0 + c, ncol = p.N - n;
-        if (ncol <= 0) break;
-        if (g.splits > 1) {
-          store_cols(p.part + ((int64_t)t.split * p.M + row) * g.ldp + n, sum + c, ncol, true, false);
-        } else {
-          const int64_t o = (int64_t)row * p.ldc + n;
-          if (p.ctype == ROT_TYPE_F32)
-            store_cols((float*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 4), p.accumulate);
-          else if (p.ctype == ROT_TYPE_F16)
-            store_cols((__half*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 2), false);
-          else
-            store_cols((__nv_bfloat16*)p.c + o, sum + c, ncol, rows16(p.c, p.ldc, 2), false);
-        }
-      }
+      const int row = t.m0 + quarter * 32, n0 = t.n0 + half * kEpiCols;
+      const int rows = p.M - row, cols = p.N - n0;
+      if (!ok || rows <= 0 || cols <= 0) continue;
+      uint8_t* stage = staging + (warp - 4) * kStagingBytes;
+      const int64_t o = (int64_t)row * p.ldc + n0;
+      if (g.splits > 1)
+        store_tile(stage, p.part + ((int64_t)t.split * p.M + row) * g.ldp + n0, g.ldp, rows, cols,
+                   sum, false);
+      else if (p.ctype == ROT_TYPE_F32)
+        store_tile(stage, (float*)p.c + o, p.ldc, rows, cols, sum, p.accumulate);
+      else if (p.ctype == ROT_TYPE_F16)
+        store_tile(stage, (__half*)p.c + o, p.ldc, rows, cols, sum, false);
+      else
+        store_tile(stage, (__nv_bfloat16*)p.c + o, p.ldc, rows, cols, sum, false);
     }
   }
 
