@@ -7,9 +7,10 @@
 // CTA per SM, walks the (tile, share of K) units of C.  Per CTA:
 //   warp 0      one thread issues TMA loads of A (128 x 128 bytes) and B
 //               (192 x 128 bytes) blocks into a five-deep ring
-//   warp 1      allocates TMEM; one thread copies a block's scales to TMEM
-//               and issues its four MMAs of 128 x 192 x 32
-//   warp 2      reads the blocks' scales and lays them out for that copy
+//   warp 1      allocates TMEM; one thread issues four MMAs of 128 x 192 x 32
+//               per block, and every four blocks the copies of their scales to
+//               TMEM (a cell holds four scales; the MMA names the one it takes)
+//   warp 2      reads the scales and lays them out for those copies
 //   warps 4-11  epilogue: each takes 32 rows x 96 columns
 // 128 x 192 is the widest tile whose accumulator fits TMEM twice next to the
 // scales, so that the epilogue overlaps the next tile's MMAs.
@@ -38,23 +39,25 @@ namespace {
 constexpr int BM = 128, BN = 192, BK = 128;
 constexpr int kStages = 5;
 constexpr int kABytes = BM * BK, kBBytes = BN * BK, kStageBytes = kABytes + kBBytes;
-constexpr int kScaleBytes = 512 + 1024;  // per stage: A's 128 rows, B's 192 (of 256)
+constexpr int kScaleBytes = 512 + 1024;  // a stretch's: A's 128 rows, B's 192 (of 256)
+constexpr int kSlots = 3;                // stretches of scales on their way
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8, kEpiCols = BN / 2;
 constexpr int kStagingBytes = 32 * 64;  // per epilogue warp
 constexpr int kSmem =
-    1024 + kStages * (kStageBytes + kScaleBytes) + kEpiWarps * kStagingBytes + 256;
+    1024 + kStages * kStageBytes + kSlots * kScaleBytes + kEpiWarps * kStagingBytes + 256;
 static_assert(kSmem <= 232448, "dynamic shared memory above 227 KB");
-constexpr int kStretch = 4;  // K blocks an accumulator takes
-constexpr int kScaleCols = 12;  // TMEM columns of a stage's scales: 4 of A, 8 of B
+constexpr int kStretch = 4;     // K blocks an accumulator takes, and a cell of scales holds
+constexpr int kScaleCols = 12;  // TMEM columns of a stretch's scales: 4 of A, 8 of B
 constexpr int kTmemCols = 512;
-static_assert(2 * BN + kStages * kScaleCols <= kTmemCols, "TMEM");
+static_assert(2 * BN + kSlots * kScaleCols <= kTmemCols, "TMEM");
 
 struct Mx {
   CUtensorMap a, b;
   Prod p;
   int tiles_m, tiles_n, kblocks, splits, per;  // per: K blocks of a unit
-  int64_t units, ldp;
+  int units;
+  int64_t ldp;
   int* status;
   unsigned long long limit_ns;
 };
@@ -67,18 +70,28 @@ constexpr int kGroupM = 8;
 struct Unit {
   int m0, n0, k0, k1, split;
 };
-__device__ __forceinline__ Unit unit_of(const Mx& g, int64_t u) {
-  const int64_t tile = u / g.splits;
+__device__ __forceinline__ Unit unit_of(const Mx& g, int u) {
+  const int tile = u / g.splits;
   const int per_group = kGroupM * g.tiles_n;
-  const int grp = (int)(tile / per_group), r = (int)(tile - (int64_t)grp * per_group);
+  const int grp = tile / per_group, r = tile - grp * per_group;
   const int h = min(kGroupM, g.tiles_m - grp * kGroupM);
   Unit t;
-  t.split = (int)(u - tile * g.splits);
+  t.split = u - tile * g.splits;
   t.m0 = (grp * kGroupM + r % h) * BM;
   t.n0 = r / h * BN;
   t.k0 = t.split * g.per;
   t.k1 = min(g.kblocks, t.k0 + g.per);
   return t;
+}
+
+// Bounded wait (ptx::mbar_wait) that looks at the clock only after a while:
+// the usual wait is short, and reading the timer is not.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                     uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return ptx::mbar_wait(bar, parity, abort, limit_ns);
 }
 
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -87,6 +100,26 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t l
   for (uint32_t it = 0;; ++it) {
     if (ptx::mbar_try_wait(bar, parity)) return;
     if ((it & 63u) == 0u && (ptx::globaltimer_ns() - t0 > limit_ns || it > (1u << 30))) return;
+  }
+}
+
+// The scales that a lane lays out for a stretch: rows lane, 32 + lane, .. of
+// A's four groups and B's six, in its four K blocks.  Rows past the last one
+// and blocks past k1 take the last one's: nothing of theirs is used, and no
+// load waits for another's condition.
+struct Scales {
+  uint32_t v[10][kStretch];
+};
+__device__ __forceinline__ void load_scales(const Prod& p, const Unit& t, int kb, int lane,
+                                            Scales& s) {
+#pragma unroll
+  for (int c = 0; c < 10; ++c) {
+    const bool a = c < 4;
+    const int r = min((a ? t.m0 + 32 * c : t.n0 + 32 * (c - 4)) + lane, (a ? p.M : p.N) - 1);
+    const uint8_t* q = a ? p.sa + (r >> p.ash) : p.sb + (r >> p.bsh);
+    const int64_t ld = a ? p.ldsa : p.ldsb;
+#pragma unroll
+    for (int j = 0; j < kStretch; ++j) s.v[c][j] = q[min(kb + j, t.k1 - 1) * ld];
   }
 }
 
@@ -161,12 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* scales = smem + kStages * kStageBytes;
-  uint8_t* staging = scales + kStages * kScaleBytes;
+  uint8_t* staging = scales + kSlots * kScaleBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStagingBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
+  uint64_t* sfull = tempty + 2;
+  uint64_t* sempty = sfull + kSlots;
+  uint64_t* done = sempty + kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -176,12 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 2);  // the loads, the scales
+      ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&tfull[a], 1);
       ptx::mbar_init(&tempty[a], kEpiWarps);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      ptx::mbar_init(&sfull[s], 1);
+      ptx::mbar_init(&sempty[s], 1);
     }
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
@@ -204,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; kb < t.k1; ++kb) {
-        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, limit)) {
+        if (!wait(&empty[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
@@ -227,119 +266,98 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issue
-    // Copies and MMAs run in the order of issue, and an MMA waits for its
-    // scales' copy: each block's copies are issued one block of MMAs ahead.
     const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
-    int64_t blocks = 0;  // K blocks of this CTA's units
-    for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {
-      const Unit t = unit_of(g, u);
-      blocks += t.k1 - t.k0;
-    }
-    int stage = 0, ahead = 0, acc = 0;
-    uint32_t ahead_phase = 0, acc_phase = 0;
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
-    auto copy_scales = [&]() {  // of the next block to come
-      if (blocks == 0) return;
-      --blocks;
-      if (!ptx::mbar_wait(&full[ahead], ahead_phase, abort_flag, limit)) {
-        ok = false;
-        return;
-      }
-      ptx::tc_fence_after();
-      const uint32_t sc = ptx::smem_u32(scales + ahead * kScaleBytes);
-      const uint32_t sf = tmem + (uint32_t)(2 * BN + ahead * kScaleCols);
-      ptx::tmem_cp_32x128b_x4(sf, ptx::rows16_desc(sc));
-      ptx::tmem_cp_32x128b_x4(sf + 4, ptx::rows16_desc(sc + 512));
-      ptx::tmem_cp_32x128b_x4(sf + 8, ptx::rows16_desc(sc + 1024));
-      if (++ahead == kStages) {
-        ahead = 0;
-        ahead_phase ^= 1u;
-      }
-    };
-    copy_scales();
-    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
-        if (!ptx::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit)) {
-          ok = false;
-          break;
-        }
+        ok = wait(&sfull[slot], slot_phase, abort_flag, limit) &&
+             wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit);
+        if (!ok) break;
         ptx::tc_fence_after();
+        // (copies and MMAs run in the order of issue)
+        const uint32_t sc = ptx::smem_u32(scales + slot * kScaleBytes);
+        const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * kScaleCols), sfb = sfa + 4;
+        ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
+        ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
+        ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        const int k1 = min(t.k1, kb + kStretch);
-        for (int k = kb; k < k1; ++k) {
-          copy_scales();
-          if (!ok) break;
-          const uint32_t sfa = tmem + (uint32_t)(2 * BN + stage * kScaleCols), sfb = sfa + 4;
+        const int n = min(t.k1 - kb, kStretch);
+        for (int j = 0; j < n; ++j) {
+          if (!wait(&full[stage], phase, abort_flag, limit)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
           const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
           const uint64_t da = ptx::sw128_kmajor_desc(st);
           const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
+          const uint32_t id = ptx::idesc_scales(idesc, j, j);
 #pragma unroll
           for (int i = 0; i < BK / 32; ++i)
-            ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), idesc, sfa, sfb,
-                           (k > kb || i > 0) ? 1u : 0u);
+            ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), id, sfa, sfb,
+                           (j > 0 || i > 0) ? 1u : 0u);
           ptx::umma_commit(&empty[stage]);
-          if (++stage == kStages) stage = 0;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
         if (!ok) break;
         ptx::umma_commit(&tfull[acc]);
+        ptx::umma_commit(&sempty[slot]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+        if (++slot == kSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
       }
     }
     ptx::umma_commit(done);
     drain(done, 0, limit);
   } else if (warp == 2) {
     // ------------------------------------------------------------ scales
-    // Lane l lays out rows l, 32 + l, 64 + l, .. : four bytes (one for each 32
-    // of the block's K, all the same) for each, which tcgen05.cp puts into
-    // lane l, columns 0, 1, 2, ..  The next stretch's bytes are on their way
-    // while this one's are written.
-    int stage = 0;
+    // A word per row, with the scales of the stretch's four K blocks, which
+    // tcgen05.cp puts into lane l, column c for row 32 c + l.  The next
+    // stretch's bytes are on their way while this one's are laid out.
+    int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
-      const Unit t = unit_of(g, u);
-      for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
-        const int n = min(kStretch, t.k1 - kb);
-        uint32_t va[kStretch][4], vb[kStretch][6];
+    int u = blockIdx.x, kb;
+    Unit t;
+    Scales s;
+    if (u < g.units) {
+      t = unit_of(g, u);
+      kb = t.k0;
+      load_scales(p, t, kb, lane, s);
+    }
+    while (u < g.units) {
+      uint32_t w[10];
 #pragma unroll
-        for (int j = 0; j < kStretch; ++j) {
-          if (j < n) {
-            const uint8_t* sa = p.sa + (kb + j) * p.ldsa;
-            const uint8_t* sb = p.sb + (kb + j) * p.ldsb;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int r = t.m0 + 32 * c + lane;
-              va[j][c] = r < p.M ? sa[r >> p.ash] : 127u;
-            }
-#pragma unroll
-            for (int c = 0; c < 6; ++c) {
-              const int r = t.n0 + 32 * c + lane;
-              vb[j][c] = r < p.N ? sb[r >> p.bsh] : 127u;
-            }
-          }
+      for (int c = 0; c < 10; ++c)
+        w[c] = s.v[c][0] | s.v[c][1] << 8 | s.v[c][2] << 16 | s.v[c][3] << 24;
+      kb += kStretch;
+      if (kb >= t.k1) {
+        u += gridDim.x;
+        if (u < g.units) {
+          t = unit_of(g, u);
+          kb = t.k0;
         }
-#pragma unroll
-        for (int j = 0; j < kStretch; ++j) {
-          if (j < n && ok) {
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, limit));
-            if (ok) {
-              uint4* s = reinterpret_cast<uint4*>(scales + stage * kScaleBytes);
-              constexpr uint32_t r = 0x01010101u;
-              s[lane] = make_uint4(va[j][0] * r, va[j][1] * r, va[j][2] * r, va[j][3] * r);
-              s[32 + lane] = make_uint4(vb[j][0] * r, vb[j][1] * r, vb[j][2] * r, vb[j][3] * r);
-              s[64 + lane] = make_uint4(vb[j][4] * r, vb[j][5] * r, 127u * r, 127u * r);
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(&full[stage]);
-              if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-              }
-            }
-          }
-        }
+      }
+      if (u < g.units) load_scales(p, t, kb, lane, s);
+      if (!__all_sync(0xffffffffu, wait(&sempty[slot], phase ^ 1u, abort_flag, limit))) break;
+      uint4* q = reinterpret_cast<uint4*>(scales + slot * kScaleBytes);
+      q[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+      q[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+      q[64 + lane] = make_uint4(w[8], w[9], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sfull[slot]);
+      if (++slot == kSlots) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
   } else if (warp >= 4) {
@@ -349,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       float sum[kEpiCols];
 #pragma unroll
       for (int c = 0; c < kEpiCols; ++c) sum[c] = 0.f;
       for (int kb = t.k0; kb < t.k1; kb += kStretch) {
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&tfull[acc], acc_phase, abort_flag, limit))) {
+        if (!__all_sync(0xffffffffu, wait(&tfull[acc], acc_phase, abort_flag, limit))) {
           ok = false;
           break;
         }
@@ -488,6 +506,7 @@ int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
       fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (attr != cudaSuccess || !encoder()) return ROT_ECUDA;
   const Shape s = shape_of(p.M, p.N, p.K);
+  if (s.tiles_m * s.tiles_n * s.splits > 0x7FFFFFFF) return ROT_EINVAL;  // (C beyond any memory)
   Mx g;
   int e = encode(&g.a, p.a, p.M, p.K, p.lda, BM);
   if (e == ROT_OK) e = encode(&g.b, p.b, p.N, p.K, p.ldb, BN);
@@ -495,12 +514,12 @@ int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
   g.p = p;
   g.tiles_m = (int)s.tiles_m, g.tiles_n = (int)s.tiles_n, g.kblocks = (int)s.kblocks;
   g.splits = (int)s.splits, g.per = (int)s.per, g.ldp = s.ldp;
-  g.units = s.tiles_m * s.tiles_n * s.splits;
+  g.units = (int)(s.tiles_m * s.tiles_n * s.splits);
   g.status = status;
   g.limit_ns = g_wait_limit_ns;
   {
     ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * p.M * (double)p.N * p.K, stream);
-    e = launch_behind(fp8_gemm_kernel, (unsigned)std::min<int64_t>(g.units, sm_count()), kThreads,
+    e = launch_behind(fp8_gemm_kernel, (unsigned)std::min(g.units, sm_count()), kThreads,
                       kSmem, stream, g);
   }
   if (e != ROT_OK || s.splits == 1) return e;

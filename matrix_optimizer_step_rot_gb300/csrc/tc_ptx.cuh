@@ -290,5 +290,11 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int a_e5m2, int 
          (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 7) << 27);
 }
 
+// The same with the scales taken from bytes a and b of their cells (bits 29-30
+// and 4-5).
+__host__ __device__ constexpr uint32_t idesc_scales(uint32_t idesc, int a, int b) {
+  return idesc | (static_cast<uint32_t>(b) << 4) | (static_cast<uint32_t>(a) << 29);
+}
+
 }  // namespace ptx
 }  // namespace rot
