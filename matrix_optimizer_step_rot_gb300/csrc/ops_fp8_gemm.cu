@@ -205,9 +205,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the same in every lane, and known to be)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t limit = g.limit_ns;
   const Prod& p = g.p;
+  auto ready = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity, abort_flag, limit)) != 0;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -233,29 +237,36 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   wait_for_prior();  // (the operands may come from the kernel before)
 
-  if (warp == 0 && lane == 0) {
+  // Warps 0 and 1 run their loops as a whole, with one lane's copies and MMAs
+  // in between: operands and addresses stay in uniform registers.  From a
+  // branch on the lane number the issue of a block's four MMAs took 570 cycles,
+  // half as long again as the MMAs.
+  if (warp == 0) {
     // ------------------------------------------------------------ loads
-    ptx::tma_prefetch_desc(&g.a);
-    ptx::tma_prefetch_desc(&g.b);
+    const bool one = ptx::elect_one();
+    if (one) {
+      ptx::tma_prefetch_desc(&g.a);
+      ptx::tma_prefetch_desc(&g.b);
+    }
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; kb < t.k1; ++kb) {
-        if (!wait(&empty[stage], phase ^ 1u, abort_flag, limit)) {
-          ok = false;
-          break;
-        }
+        ok = ready(&empty[stage], phase ^ 1u);
+        if (!ok) break;
         uint8_t* st = smem + stage * kStageBytes;
-        ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
+        if (one) {
+          ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
+          ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
+          ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
+        }
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
-        ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -264,50 +275,54 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
     for (int s = 0; s < kStages; ++s)
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
+    const bool one = ptx::elect_one();
     const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
     int stage = 0, acc = 0, slot = 0;
     uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
-      for (int kb = t.k0; ok && kb < t.k1; kb += kStretch) {
-        ok = wait(&sfull[slot], slot_phase, abort_flag, limit) &&
-             wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit);
+      for (int kb = t.k0; kb < t.k1; kb += kStretch) {
+        ok = ready(&sfull[slot], slot_phase) && ready(&tempty[acc], acc_phase ^ 1u);
         if (!ok) break;
         ptx::tc_fence_after();
         // (copies and MMAs run in the order of issue)
         const uint32_t sc = ptx::smem_u32(scales + slot * kScaleBytes);
         const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * kScaleCols), sfb = sfa + 4;
-        ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
-        ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
-        ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
+        if (one) {
+          ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
+          ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
+          ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
+        }
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         const int n = min(t.k1 - kb, kStretch);
         for (int j = 0; j < n; ++j) {
-          if (!wait(&full[stage], phase, abort_flag, limit)) {
-            ok = false;
-            break;
-          }
+          ok = ready(&full[stage], phase);
+          if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
           const uint64_t da = ptx::sw128_kmajor_desc(st);
           const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
           const uint32_t id = ptx::idesc_scales(idesc, j, j);
+          if (one) {
 #pragma unroll
-          for (int i = 0; i < BK / 32; ++i)
-            ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), id, sfa, sfb,
-                           (j > 0 || i > 0) ? 1u : 0u);
-          ptx::umma_commit(&empty[stage]);
+            for (int i = 0; i < BK / 32; ++i)
+              ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), id, sfa, sfb,
+                             (j > 0 || i > 0) ? 1u : 0u);
+            ptx::umma_commit(&empty[stage]);
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::umma_commit(&tfull[acc]);
-        ptx::umma_commit(&sempty[slot]);
+        if (one) {
+          ptx::umma_commit(&tfull[acc]);
+          ptx::umma_commit(&sempty[slot]);
+        }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
         if (++slot == kSlots) {
@@ -316,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
       }
     }
-    ptx::umma_commit(done);
+    if (one) ptx::umma_commit(done);
+    __syncwarp();
     drain(done, 0, limit);
   } else if (warp == 2) {
     // ------------------------------------------------------------ scales
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
       }
       if (u < g.units) load_scales(p, t, kb, lane, s);
-      if (!__all_sync(0xffffffffu, wait(&sempty[slot], phase ^ 1u, abort_flag, limit))) break;
+      if (!ready(&sempty[slot], phase ^ 1u)) break;
       uint4* q = reinterpret_cast<uint4*>(scales + slot * kScaleBytes);
       q[lane] = make_uint4(w[0], w[1], w[2], w[3]);
       q[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 #pragma unroll
       for (int c = 0; c < kEpiCols; ++c) sum[c] = 0.f;
       for (int kb = t.k0; kb < t.k1; kb += kStretch) {
-        if (!__all_sync(0xffffffffu, wait(&tfull[acc], acc_phase, abort_flag, limit))) {
+        if (!ready(&tfull[acc], acc_phase)) {
           ok = false;
           break;
         }

@@ -68,6 +68,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// One lane of a converged warp.  Code that a whole warp runs, with this lane's
+// instructions in between, keeps descriptors and addresses in uniform
+// registers; a branch on the lane number does not.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 // Bring the 128-byte line holding p into L2 (a hint: no fault, no effect on
 // the program's results).
