@@ -212,6 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   auto ready = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, abort_flag, limit)) != 0;
   };
+  // The waits of each block leave a timeout to `aborted`, once per stretch:
+  // once the flag is up, every wait returns after its first tries.
+  auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag) != 0; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -253,26 +256,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = blockIdx.x; u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
-      for (int kb = t.k0; kb < t.k1; ++kb) {
-        ok = ready(&empty[stage], phase ^ 1u);
-        if (!ok) break;
-        uint8_t* st = smem + stage * kStageBytes;
-        if (one) {
-          ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
-          ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
-          ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
-        }
-        armed |= 1u << stage;
-        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+      int kb = t.k0;
+      while (kb < t.k1 && !aborted()) {
+        const int k1 = min(t.k1, kb + kStretch);
+        for (; kb < k1; ++kb) {
+          wait(&empty[stage], phase ^ 1u, abort_flag, limit);
+          if (*abort_flag) break;  // (the stage may still be read)
+          uint8_t* st = smem + stage * kStageBytes;
+          if (one) {
+            ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
+            ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
+            ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
+          }
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
+      if (kb < t.k1) break;
     }
+    __syncwarp();
     for (int s = 0; s < kStages; ++s)
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
   } else if (warp == 1) {
@@ -285,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; kb < t.k1; kb += kStretch) {
-        ok = ready(&sfull[slot], slot_phase) && ready(&tempty[acc], acc_phase ^ 1u);
+        wait(&sfull[slot], slot_phase, abort_flag, limit);
+        wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit);
+        ok = !aborted();
         if (!ok) break;
         ptx::tc_fence_after();
         // (copies and MMAs run in the order of issue)
@@ -298,9 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         const int n = min(t.k1 - kb, kStretch);
-        for (int j = 0; j < n; ++j) {
-          ok = ready(&full[stage], phase);
-          if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < kStretch; ++j) {
+          if (j >= n) break;
+          wait(&full[stage], phase, abort_flag, limit);
           ptx::tc_fence_after();
           const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
           const uint64_t da = ptx::sw128_kmajor_desc(st);
@@ -318,7 +329,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             phase ^= 1u;
           }
         }
-        if (!ok) break;
         if (one) {
           ptx::umma_commit(&tfull[acc]);
           ptx::umma_commit(&sempty[slot]);
