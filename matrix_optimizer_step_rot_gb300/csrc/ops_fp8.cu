@@ -370,7 +370,7 @@ struct Carve {
   }
   Held matrix(int64_t rows, int64_t cols) {
     Held h;
-    h.ld = up(cols, 16) * 16;
+    h.ld = up(cols, kQ) * kQ;  // (rows of whole 128-byte lines, as the product's loads take them)
     h.lds = rows;
     h.q = reinterpret_cast<uint8_t*>(take((uint64_t)rows * h.ld));
     h.s = reinterpret_cast<uint8_t*>(take((uint64_t)rows * up(cols, kQ)));

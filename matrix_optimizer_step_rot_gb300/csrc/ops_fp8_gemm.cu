@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint64_t* sfull = tempty + 2;
   uint64_t* sempty = sfull + kSlots;
   uint64_t* done = sempty + kSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // (the same in every lane, and known to be)
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       ptx::mbar_init(&sfull[s], 1);
       ptx::mbar_init(&sempty[s], 1);
     }
-    ptx::mbar_init(done, 1);
+    ptx::mbar_init(&done[0], 1);
+    ptx::mbar_init(&done[1], 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -283,67 +284,78 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     __syncwarp();
     for (int s = 0; s < kStages; ++s)
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issue
+    // Warp 1 takes the even stretches, warp 3 the odd ones, each with its own
+    // accumulator: the issue of a block takes one warp longer than its MMAs.
+    const int odd = warp >> 1;
     const bool one = ptx::elect_one();
     const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
-    int stage = 0, acc = 0, slot = 0;
+    int stage = 0, turn = 0, slot = 0;
     uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
+    const uint32_t d = tmem + (uint32_t)(odd * BN);
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       for (int kb = t.k0; kb < t.k1; kb += kStretch) {
-        wait(&sfull[slot], slot_phase, abort_flag, limit);
-        wait(&tempty[acc], acc_phase ^ 1u, abort_flag, limit);
-        ok = !aborted();
-        if (!ok) break;
-        ptx::tc_fence_after();
-        // (copies and MMAs run in the order of issue)
-        const uint32_t sc = ptx::smem_u32(scales + slot * kScaleBytes);
-        const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * kScaleCols), sfb = sfa + 4;
-        if (one) {
-          ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
-          ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
-          ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
-        }
-        const uint32_t d = tmem + (uint32_t)(acc * BN);
         const int n = min(t.k1 - kb, kStretch);
-#pragma unroll
-        for (int j = 0; j < kStretch; ++j) {
-          if (j >= n) break;
-          wait(&full[stage], phase, abort_flag, limit);
+        if (turn == odd) {
+          wait(&sfull[slot], slot_phase, abort_flag, limit);
+          wait(&tempty[odd], acc_phase ^ 1u, abort_flag, limit);
+          ok = !aborted();
+          if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
-          const uint64_t da = ptx::sw128_kmajor_desc(st);
-          const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
-          const uint32_t id = ptx::idesc_scales(idesc, j, j);
+          // (copies and MMAs run in the order of issue)
+          const uint32_t sc = ptx::smem_u32(scales + slot * kScaleBytes);
+          const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * kScaleCols), sfb = sfa + 4;
           if (one) {
-#pragma unroll
-            for (int i = 0; i < BK / 32; ++i)
-              ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), id, sfa, sfb,
-                             (j > 0 || i > 0) ? 1u : 0u);
-            ptx::umma_commit(&empty[stage]);
+            ptx::tmem_cp_32x128b_x4(sfa, ptx::rows16_desc(sc));
+            ptx::tmem_cp_32x128b_x4(sfb, ptx::rows16_desc(sc + 512));
+            ptx::tmem_cp_32x128b_x4(sfb + 4, ptx::rows16_desc(sc + 1024));
           }
-          if (++stage == kStages) {
-            stage = 0;
+#pragma unroll
+          for (int j = 0; j < kStretch; ++j) {
+            if (j >= n) break;
+            wait(&full[stage], phase, abort_flag, limit);
+            ptx::tc_fence_after();
+            const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
+            const uint64_t da = ptx::sw128_kmajor_desc(st);
+            const uint64_t db = ptx::sw128_kmajor_desc(st + kABytes);
+            const uint32_t id = ptx::idesc_scales(idesc, j, j);
+            if (one) {
+#pragma unroll
+              for (int i = 0; i < BK / 32; ++i)
+                ptx::umma_mxf8(d, da + (uint64_t)(2 * i), db + (uint64_t)(2 * i), id, sfa, sfb,
+                               (j > 0 || i > 0) ? 1u : 0u);
+              ptx::umma_commit(&empty[stage]);
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (one) {
+            ptx::umma_commit(&tfull[odd]);
+            ptx::umma_commit(&sempty[slot]);
+          }
+          acc_phase ^= 1u;
+        } else {
+          stage += n;
+          if (stage >= kStages) {
+            stage -= kStages;
             phase ^= 1u;
           }
         }
-        if (one) {
-          ptx::umma_commit(&tfull[acc]);
-          ptx::umma_commit(&sempty[slot]);
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        turn ^= 1;
         if (++slot == kSlots) {
           slot = 0;
           slot_phase ^= 1u;
         }
       }
     }
-    if (one) ptx::umma_commit(done);
+    if (one) ptx::umma_commit(&done[odd]);
     __syncwarp();
-    drain(done, 0, limit);
+    drain(&done[odd], 0, limit);
   } else if (warp == 2) {
     // ------------------------------------------------------------ scales
     // A word per row, with the scales of the stretch's four K blocks, which
