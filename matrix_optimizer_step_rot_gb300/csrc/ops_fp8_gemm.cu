@@ -57,7 +57,9 @@ struct Mx {
   Prod p;
   int tiles_m, tiles_n, kblocks, splits, per;  // per: K blocks of a unit
   int units;
-  int64_t ldp;
+  void* c;
+  int64_t ldc;
+  int accumulate;
   int* status;
   unsigned long long limit_ns;
 };
@@ -123,14 +125,13 @@ __device__ __forceinline__ void load_scales(const Prod& p, const Unit& t, int kb
   }
 }
 
-// A warp's 32 rows of C, 64 bytes of each (U = 64 / sizeof(T) columns), of
-// which this thread holds row `lane`: staged in 2 KB of shared memory, so that
-// the warp then stores eight whole 64-byte pieces of rows at a time (one row
-// per thread would store 16 bytes of 32 rows).  16-byte piece c of row r is at
+// A warp's 32 rows of C, 64 bytes of each (64 / sizeof(T) columns), of which
+// this thread holds row `lane`: staged in 2 KB of shared memory, so that the
+// warp then stores eight whole 64-byte pieces of rows at a time (one row per
+// thread would store 16 bytes of 32 rows).  16-byte piece c of row r is at
 // place c ^ (r / 2 & 3) of the row: neither side has bank conflicts.
 template <class T>
-__device__ __forceinline__ void store_rows(uint8_t* stage, T* c, int64_t ldc, int rows, int cols,
-                                           const float* v, bool wide, bool accumulate) {
+__device__ __forceinline__ void stage_rows(uint8_t* stage, const float* v) {
   constexpr int U = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   __syncwarp();
@@ -142,53 +143,53 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, T* c, int64_t ldc, in
     store_run(reinterpret_cast<T*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)), f);
   }
   __syncwarp();
-  if (wide) {
-    const int i = lane & 3;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = 8 * q + (lane >> 2);
-      if (r >= rows || i * U >= cols) continue;
-      const T* p = reinterpret_cast<const T*>(stage + r * 64 + ((i ^ (r >> 1 & 3)) << 4));
-      T* o = c + r * ldc + i * U;
-      if (i * U + U <= cols) {
-        float f[U];
-        load_run(p, f);
-        if (accumulate) {
-          float old[U];
-          load_run(o, old);
-#pragma unroll
-          for (int k = 0; k < U; ++k) f[k] += old[k];
-        }
-        store_run(o, f);
-      } else {
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (i * U + k < cols) o[k] = accumulate ? from_f32<T>(to_f32(o[k]) + to_f32(p[k])) : p[k];
-      }
-    }
-  } else {  // rows that are not 16-byte aligned: a row's columns side by side
+}
+
+// Rows that are cut, not 16-byte aligned or added to: element by element, a
+// row's columns side by side.
+template <class T>
+__device__ __noinline__ void store_any(const uint8_t* stage, T* c, int64_t ldc, int rows, int cols,
+                                       bool accumulate) {
+  constexpr int W = 64 / sizeof(T), U = 16 / sizeof(T);
 #pragma unroll 1
-    for (int e = lane; e < 32 * 4 * U; e += 32) {
-      const int r = e / (4 * U), k = e % (4 * U);
-      if (r >= rows || k >= cols) continue;
-      const T x = *reinterpret_cast<const T*>(stage + r * 64 + (((k / U) ^ (r >> 1 & 3)) << 4) +
-                                              k % U * sizeof(T));
-      T* o = c + r * ldc + k;
-      *o = accumulate ? from_f32<T>(to_f32(*o) + to_f32(x)) : x;
-    }
+  for (int e = threadIdx.x & 31; e < 32 * W; e += 32) {
+    const int r = e / W, k = e % W;
+    if (r >= rows || k >= cols) continue;
+    const T x = *reinterpret_cast<const T*>(stage + r * 64 + (((k / U) ^ (r >> 1 & 3)) << 4) +
+                                            k % U * sizeof(T));
+    T* o = c + r * ldc + k;
+    *o = accumulate ? from_f32<T>(to_f32(*o) + to_f32(x)) : x;
   }
 }
 
+// A warp's 32 rows and kEpiCols columns from c on, cut to rows x cols.
 template <class T>
 __device__ __forceinline__ void store_tile(uint8_t* stage, T* c, int64_t ldc, int rows, int cols,
                                            const float* sum, bool accumulate) {
   constexpr int W = 64 / sizeof(T);
-  const bool wide = rows16(c, ldc, sizeof(T));
+  const int lane = threadIdx.x & 31, r = lane >> 2, i = lane & 3;
+  const bool whole = rows >= 32 && rows16(c, ldc, sizeof(T)) && !accumulate;
+  const uint4* from = reinterpret_cast<const uint4*>(stage + r * 64 + ((i ^ (r >> 1 & 3)) << 4));
+  uint8_t* to = reinterpret_cast<uint8_t*>(c + r * ldc) + 16 * i;
 #pragma unroll
-  for (int n = 0; n < kEpiCols; n += W)
-    if (n < cols) store_rows(stage, c + n, ldc, rows, cols - n, sum + n, wide, accumulate);
+  for (int n = 0; n < kEpiCols; n += W) {
+    if (n >= cols) break;
+    stage_rows<T>(stage, sum + n);
+    if (whole && n + W <= cols) {
+      uint4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = from[q * 32];  // rows 8 q + r
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(to + (8 * q * ldc + n) * (int64_t)sizeof(T)) = v[q];
+    } else {
+      store_any(stage, c + n, ldc, rows, cols - n, accumulate);
+    }
+  }
 }
 
+// C of type T; g.c and g.ldc: C, or with split K the parts (float32).
+template <class T>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Mx g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -434,16 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const int rows = p.M - row, cols = p.N - n0;
       if (!ok || rows <= 0 || cols <= 0) continue;
       uint8_t* stage = staging + (warp - 4) * kStagingBytes;
-      const int64_t o = (int64_t)row * p.ldc + n0;
-      if (g.splits > 1)
-        store_tile(stage, p.part + ((int64_t)t.split * p.M + row) * g.ldp + n0, g.ldp, rows, cols,
-                   sum, false);
-      else if (p.ctype == ROT_TYPE_F32)
-        store_tile(stage, (float*)p.c + o, p.ldc, rows, cols, sum, p.accumulate);
-      else if (p.ctype == ROT_TYPE_F16)
-        store_tile(stage, (__half*)p.c + o, p.ldc, rows, cols, sum, false);
-      else
-        store_tile(stage, (__nv_bfloat16*)p.c + o, p.ldc, rows, cols, sum, false);
+      store_tile(stage, static_cast<T*>(g.c) + ((int64_t)t.split * p.M + row) * g.ldc + n0, g.ldc,
+                 rows, cols, sum, g.accumulate);
     }
   }
 
@@ -531,6 +524,16 @@ int encode(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, int64
   return r == CUDA_SUCCESS ? ROT_OK : ROT_EINVAL;
 }
 
+template <class T>
+int launch_gemm(const Mx& g, cudaStream_t stream) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      fp8_gemm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr != cudaSuccess) return ROT_ECUDA;
+  ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * g.p.M * (double)g.p.N * g.p.K, stream);
+  return launch_behind(fp8_gemm_kernel<T>, (unsigned)std::min(g.units, sm_count()), kThreads, kSmem,
+                       stream, g);
+}
+
 }  // namespace
 
 uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K) {
@@ -540,9 +543,7 @@ uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess || !encoder()) return ROT_ECUDA;
+  if (!encoder()) return ROT_ECUDA;
   const Shape s = shape_of(p.M, p.N, p.K);
   if (s.tiles_m * s.tiles_n * s.splits > 0x7FFFFFFF) return ROT_EINVAL;  // (C beyond any memory)
   Mx g;
@@ -551,16 +552,19 @@ int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
   if (e != ROT_OK) return e;
   g.p = p;
   g.tiles_m = (int)s.tiles_m, g.tiles_n = (int)s.tiles_n, g.kblocks = (int)s.kblocks;
-  g.splits = (int)s.splits, g.per = (int)s.per, g.ldp = s.ldp;
+  g.splits = (int)s.splits, g.per = (int)s.per;
+  const bool parts = s.splits > 1;
+  g.c = parts ? p.part : p.c, g.ldc = parts ? s.ldp : p.ldc, g.accumulate = !parts && p.accumulate;
   g.units = (int)(s.tiles_m * s.tiles_n * s.splits);
   g.status = status;
   g.limit_ns = g_wait_limit_ns;
-  {
-    ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * p.M * (double)p.N * p.K, stream);
-    e = launch_behind(fp8_gemm_kernel, (unsigned)std::min(g.units, sm_count()), kThreads,
-                      kSmem, stream, g);
-  }
-  if (e != ROT_OK || s.splits == 1) return e;
+  if (parts || p.ctype == ROT_TYPE_F32)
+    e = launch_gemm<float>(g, stream);
+  else if (p.ctype == ROT_TYPE_F16)
+    e = launch_gemm<__half>(g, stream);
+  else
+    e = launch_gemm<__nv_bfloat16>(g, stream);
+  if (e != ROT_OK || !parts) return e;
   ProfScope prof(ROT_PROF_ELEMENTWISE, 4.0 * (s.splits + 1) * p.M * (double)p.N, stream);
   const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
   return launch_behind(fp8_join_kernel, (unsigned)std::min<int64_t>(blocks, 8ll * sm_count()), 256, 0,
