@@ -22,6 +22,7 @@ struct Quant {
   uint8_t *q, *s, *qt, *st;
   int64_t ldx, rows, cols, ldq, lds, ldqt, ldst;
   int e5m2, square;  // square: blocks of 128 x 128
+  int wide;          // q's rows are 16-byte aligned
 };
 
 // Two values as 8-bit floats, the first in the low byte.
@@ -29,24 +30,69 @@ __device__ __forceinline__ uint32_t pair_f8(float x, float y, bool e5m2) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
 }
 
-// A thread's 8 x 8 piece as loaded: 16-bit values two to a word (column 2 j in
-// the low half).
+// Element k of values as loaded: 16-bit ones two to a word (even k in the low
+// half).
 template <class T>
-struct Piece {
-  static constexpr int W = 8 * sizeof(T) / 4;  // words per row
-  uint32_t w[8][W];
-
-  __device__ __forceinline__ float at(int i, int k) const {
-    if constexpr (sizeof(T) == 4) {
-      return __uint_as_float(w[i][k]);
-    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-      return __uint_as_float(k & 1 ? w[i][k / 2] & 0xFFFF0000u : w[i][k / 2] << 16);
-    } else {
-      const uint32_t v = w[i][k / 2];
-      return __half2float(__ushort_as_half((unsigned short)(k & 1 ? v >> 16 : v & 0xFFFFu)));
-    }
+__device__ __forceinline__ float element(const uint32_t* w, int k) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(w[k]);
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    return __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+  } else {
+    const uint32_t v = w[k / 2];
+    return __half2float(__ushort_as_half((unsigned short)(k & 1 ? v >> 16 : v & 0xFFFFu)));
   }
-};
+}
+template <class T>
+__device__ __forceinline__ uint32_t magnitude_bits(const uint32_t* w, int k) {
+  return sizeof(T) == 4 ? w[k] & 0x7FFFFFFFu : w[k / 2] >> (16 * (k & 1)) & 0x7FFFu;
+}
+// the largest magnitudes of two words (of each half, for 16-bit values)
+template <class T>
+__device__ __forceinline__ uint32_t word_max(uint32_t m, uint32_t w) {
+  return sizeof(T) == 4 ? max(m, w & 0x7FFFFFFFu) : __vmaxu2(m, w & 0x7FFF7FFFu);
+}
+template <class T>
+__device__ __forceinline__ uint32_t halves_max(uint32_t m) {
+  return sizeof(T) == 4 ? m : max(m & 0xFFFFu, m >> 16);
+}
+// Run of N elements from p as words (N * sizeof(T) a multiple of 16), elements
+// from n on as 0.
+template <class T, int N, bool VEC>
+__device__ __forceinline__ void load_words(const T* p, int64_t n, uint32_t* w) {
+  constexpr int W = N * sizeof(T) / 4;
+  if (VEC && n >= N) {
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + k);
+      w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k) w[k] = 0u;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k < n) {
+      if constexpr (sizeof(T) == 4)
+        w[k] = __float_as_uint(p[k]);
+      else
+        w[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (16 * (k & 1));
+    }
+}
+// Four values under a scale as 8-bit floats.  The conversion saturates
+// infinities; where `odd` they become NaN by hand, as NaN stays.
+__device__ __forceinline__ uint32_t four_f8(float f0, float f1, float f2, float f3, float s,
+                                            bool odd, bool e5m2) {
+  float2 lo = mul2(make_float2(f0, f1), both(s)), hi = mul2(make_float2(f2, f3), both(s));
+  if (odd) {
+    if (!(fabsf(f0) < INFINITY)) lo.x = NAN;
+    if (!(fabsf(f1) < INFINITY)) lo.y = NAN;
+    if (!(fabsf(f2) < INFINITY)) hi.x = NAN;
+    if (!(fabsf(f3) < INFINITY)) hi.y = NAN;
+  }
+  return pair_f8(lo.x, lo.y, e5m2) | pair_f8(hi.x, hi.y, e5m2) << 16;
+}
 
 // |x| as an ordered whole number of the type's bits, and back as a float.
 template <class T>
@@ -63,6 +109,54 @@ constexpr uint32_t kInfBits = sizeof(T) == 4                             ? 0x7F8
 constexpr int kQ = 128;      // a block's edge
 constexpr int kPitch = 144;  // bytes between the staged rows of the transposed tile
 
+// Rows alone, one scale for each row and 128 columns: HBM bound, nothing to
+// exchange but the maxima of eight threads, which hold 16 elements of a block
+// each.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ Quant a) {
+  const uint32_t blocks = (uint32_t)((a.cols + 127) / 128), total = (uint32_t)a.rows * blocks;
+  const int v = threadIdx.x % 8;
+  for (uint32_t b = blockIdx.x * 32 + threadIdx.x / 8; b < (total + 3) / 4 * 4;
+       b += gridDim.x * 32) {  // (whole warps: four blocks each)
+    const uint32_t at = min(b, total - 1), r = at / blocks, j = at - r * blocks;
+    const int64_t row = r, c = (int64_t)j * 128 + 16 * v;
+    uint32_t x[4 * sizeof(T)];
+    load_words<T, 16, VEC>((const T*)a.x + row * a.ldx + c, a.cols - c, x);
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < (int)(4 * sizeof(T)); ++i) most = word_max<T>(most, x[i]);
+    most = halves_max<T>(most);
+    const bool odd = most >= kInfBits<T>;  // a NaN or an infinity among the 16
+    if (odd) {
+      most = 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t m = magnitude_bits<T>(x, i);
+        most = max(most, m >= kInfBits<T> ? 0u : m);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (b >= total) continue;
+    const int e = scale_byte(magnitude<T>(most), a.e5m2);
+    const float inv = inverse_scale(e);
+    if (v == 0) a.s[j * a.lds + row] = (uint8_t)e;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = four_f8(element<T>(x, 4 * i), element<T>(x, 4 * i + 1), element<T>(x, 4 * i + 2),
+                     element<T>(x, 4 * i + 3), inv, odd, a.e5m2);
+    uint8_t* o = a.q + row * a.ldq + c;
+    if (c + 16 <= a.cols && a.wide) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < a.cols) o[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+    }
+  }
+}
+
 // HBM bound (one read of x, one or two bytes written per element).  A 128 x
 // 128 tile per CTA, 256 threads: thread (g = t / 16, v = t % 16) holds rows
 // 8 g .. 8 g + 7 of columns 8 v .. 8 v + 7, so both orientations' runs of
@@ -71,41 +165,22 @@ constexpr int kPitch = 144;  // bytes between the staged rows of the transposed 
 // out as 8 bytes per thread (128 per row), the transposed tile through shared
 // memory as 16.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
+    quantize_kernel(const __grid_constant__ Quant a) {
   __shared__ __align__(16) uint32_t colmax[16][kQ];
   __shared__ __align__(16) uint8_t colscale[kQ];
   __shared__ uint32_t wide[8];
   __shared__ __align__(16) uint8_t tile[kQ * kPitch];
-  constexpr int W = Piece<T>::W;
+  constexpr int W = 8 * sizeof(T) / 4;
   const int64_t tiles_c = (a.cols + kQ - 1) / kQ;
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;  // tile row, column
   const int64_t r0 = tr * kQ, c0 = tc * kQ;
   const int g = threadIdx.x / 16, v = threadIdx.x % 16;
   const int64_t r = r0 + 8 * g, c = c0 + 8 * v;
-  Piece<T> x;
+  uint32_t x[8][W];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) x.w[i][k] = 0u;
-    if (r + i >= a.rows) continue;
-    const T* p = (const T*)a.x + (r + i) * a.ldx + c;
-    if (VEC && c + 8 <= a.cols) {
-#pragma unroll
-      for (int k = 0; k < W; k += 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + k);
-        x.w[i][k] = q.x, x.w[i][k + 1] = q.y, x.w[i][k + 2] = q.z, x.w[i][k + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < a.cols) {
-          if constexpr (sizeof(T) == 4)
-            x.w[i][k] = __float_as_uint(p[k]);
-          else
-            x.w[i][k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (16 * (k & 1));
-        }
-    }
-  }
+  for (int i = 0; i < 8; ++i)
+    load_words<T, 8, VEC>((const T*)a.x + (r + i) * a.ldx + c, r + i < a.rows ? a.cols - c : 0, x[i]);
   // largest |x| of each row and column of the piece
   uint32_t rm[8], cm[8];
   bool odd;  // a NaN or an infinity in the piece
@@ -118,17 +193,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
       uint32_t m = 0u;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        if constexpr (sizeof(T) == 4) {
-          const uint32_t b = x.w[i][k] & 0x7FFFFFFFu;
-          m = max(m, b);
-          cw[k] = max(cw[k], b);
-        } else {
-          const uint32_t b = x.w[i][k] & 0x7FFF7FFFu;
-          m = __vmaxu2(m, b);
-          cw[k] = __vmaxu2(cw[k], b);
-        }
+        m = word_max<T>(m, x[i][k]);
+        cw[k] = word_max<T>(cw[k], x[i][k]);
       }
-      rm[i] = sizeof(T) == 4 ? m : max(m & 0xFFFFu, m >> 16);
+      rm[i] = halves_max<T>(m);
       all = max(all, rm[i]);
     }
 #pragma unroll
@@ -142,14 +210,35 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          uint32_t b = sizeof(T) == 4 ? x.w[i][k % W] & 0x7FFFFFFFu
-                                      : x.w[i][k / 2 % W] >> (16 * (k & 1)) & 0x7FFFu;
+          uint32_t b = magnitude_bits<T>(x[i], k);
           if (b >= kInfBits<T>) b = 0u;
           rm[i] = max(rm[i], b);
           cm[k] = max(cm[k], b);
         }
     }
   }
+  auto put_rows = [&](const float (&ri)[8]) {
+    const bool run8 = (a.ldq % 8 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r + i >= a.rows) continue;
+      uint32_t o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 4 * h;
+        o[h] = four_f8(element<T>(x[i], k), element<T>(x[i], k + 1), element<T>(x[i], k + 2),
+                       element<T>(x[i], k + 3), ri[i], odd, a.e5m2);
+      }
+      uint8_t* p = a.q + (r + i) * a.ldq + c;
+      if (run8 && c + 8 <= a.cols) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k < a.cols) p[k] = (uint8_t)(o[k / 4] >> (8 * (k & 3)));
+      }
+    }
+    };
   float ri[8], ci[8];  // inverse scales of this thread's rows and columns
   if (a.square) {
     uint32_t m = 0u;
@@ -168,6 +257,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
       if (a.q) a.s[tc * a.lds + tr] = (uint8_t)b;
       if (a.qt) a.st[tr * a.ldst + tc] = (uint8_t)b;
     }
+    if (a.q) put_rows(ri);
   } else {
     if (a.qt) {
       uint4* p = reinterpret_cast<uint4*>(&colmax[g][8 * v]);
@@ -193,6 +283,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
         ri[i] = inverse_scale(b);
         if (v == i && r + i < a.rows) a.s[tc * a.lds + r + i] = (uint8_t)b;
       }
+      put_rows(ri);
     }
     if (a.qt) {
       __syncthreads();
@@ -202,31 +293,6 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
         ci[k] = inverse_scale((int)((k < 4 ? b.x : b.y) >> (8 * (k & 3)) & 0xFFu));
     }
   }
-  // (the conversion saturates infinities: they become NaN by hand)
-  auto value = [&](int i, int k) {
-    const float f = x.at(i, k);
-    return odd && !(fabsf(f) < INFINITY) ? NAN : f;
-  };
-  if (a.q) {
-    const bool run8 = (a.ldq % 8 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (r + i >= a.rows) continue;
-      uint32_t o[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o[h] = pair_f8(value(i, 4 * h) * ri[i], value(i, 4 * h + 1) * ri[i], a.e5m2) |
-               pair_f8(value(i, 4 * h + 2) * ri[i], value(i, 4 * h + 3) * ri[i], a.e5m2) << 16;
-      uint8_t* p = a.q + (r + i) * a.ldq + c;
-      if (run8 && c + 8 <= a.cols) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols) p[k] = (uint8_t)(o[k / 4] >> (8 * (k & 3)));
-      }
-    }
-  }
   if (a.qt) {
     // column 8 v + k is staged as row 16 k + v, so that a warp's writes spread
     // over the banks
@@ -234,9 +300,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Quant a) {
     for (int k = 0; k < 8; ++k) {
       uint32_t o[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o[h] = pair_f8(value(4 * h, k) * ci[k], value(4 * h + 1, k) * ci[k], a.e5m2) |
-               pair_f8(value(4 * h + 2, k) * ci[k], value(4 * h + 3, k) * ci[k], a.e5m2) << 16;
+      for (int h = 0; h < 2; ++h) {
+        const int i = 4 * h;
+        o[h] = four_f8(element<T>(x[i], k), element<T>(x[i + 1], k), element<T>(x[i + 2], k),
+                       element<T>(x[i + 3], k), ci[k], odd, a.e5m2);
+      }
       *reinterpret_cast<uint2*>(&tile[(16 * k + v) * kPitch + 8 * g]) = make_uint2(o[0], o[1]);
     }
     __syncthreads();
@@ -267,6 +335,14 @@ int launch_quantize(const Quant& a, cudaStream_t s) {
   const bool vec = rows16(a.x, a.ldx, sizeof(T));
   const double n = (double)a.rows * a.cols;
   ProfScope prof(ROT_PROF_ELEMENTWISE, n * (sizeof(T) + (a.q != nullptr) + (a.qt != nullptr)), s);
+  const int64_t row_blocks = a.rows * ((a.cols + 127) / 128);
+  if (!a.qt && !a.square && row_blocks < (1ll << 30)) {
+    const int64_t most = (row_blocks + 31) / 32;
+    const unsigned ctas = (unsigned)std::min<int64_t>(most, 16ll * sm_count());
+    auto k = vec ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>;
+    k<<<ctas, 256, 0, s>>>(a);
+    return launched();
+  }
   auto k = vec ? quantize_kernel<T, true> : quantize_kernel<T, false>;
   k<<<grid, 256, 0, s>>>(a);
   return launched();
@@ -307,7 +383,7 @@ int rot_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int
   const int dev = check_device();
   if (dev != ROT_OK) return dev;
   Quant a = {x, (uint8_t*)data, scale, (uint8_t*)data_t, scale_t, ldx, rows, cols, ldq, lds, ldqt,
-             ldst, format == ROT_TYPE_E5M2, block_rows == kQ};
+             ldst, format == ROT_TYPE_E5M2, block_rows == kQ, rows16(data, ldq, 1)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return guarded([&] {
     if (type == ROT_TYPE_F32) return launch_quantize<float>(a, s);

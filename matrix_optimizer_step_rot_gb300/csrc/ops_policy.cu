@@ -25,34 +25,77 @@ struct Policy {
   float lo, hi, kl, scale;
 };
 
-constexpr int kRow = 512;  // threads per CTA
 constexpr int kAhead = 4;  // 16-byte loads of a thread in flight
 
-// Running maximum and sum of exp(x - maximum).
-struct MaxSum {
-  float m, s;
+// Sum of exponentials on a running scale: the sum of 2^(x log2(e) - o) with a
+// whole number o near the largest x log2(e), so that o is exact, no rounding
+// of it enters the sum, and sums on different scales join by powers of two.
+// One fused multiply-add and one exponential per element.
+struct ScaledSum {
+  float o, s;  // o = -inf: nothing but -inf yet
 };
-// a reference point that keeps exp(-inf - m) at 0 while only -inf was seen
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
-  MaxSum r;
-  r.m = fmaxf(a.m, b.m);
-  const float o = base_of(r.m);
-  r.s = a.s * __expf(a.m - o) + b.s * __expf(b.m - o);
-  return r;
-}
-
-// exp of both halves: the difference first, so that values at the ends of
-// float32's range cannot overflow on the way.
-constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float2 exp_less(float2 x, float m) {
-  const float2 t = mul2(add2(x, both(-m)), both(kLog2e));
+// what is subtracted: 0 for o = -inf, so that 2^(-inf - o) stays 0
+__device__ __forceinline__ float base_of(float o) { return o == -INFINITY ? 0.f : o; }
+__device__ __forceinline__ ScaledSum join(ScaledSum a, ScaledSum b) {
+  ScaledSum r;
+  r.o = fmaxf(a.o, b.o);
+  const float o = base_of(r.o);
+  r.s = a.s * exp2_fast(a.o - o) + b.s * exp2_fast(b.o - o);
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// 2^((x - m) log2(e) - o) of both halves.
+__device__ __forceinline__ float2 exp_pair(float2 x, float m, float o) {
+  const float2 t = fma2(add2(x, both(-m)), both(kLog2e), both(-o));
   return make_float2(exp2_fast(t.x), exp2_fast(t.y));
+}
+
+// The largest of a run (NaN are passed over: their exponentials carry them on).
+template <int U>
+__device__ __forceinline__ float largest(const Run<float, U>& r) {
+  float m = r.v[0];
+#pragma unroll
+  for (int k = 1; k < U; ++k) m = fmaxf(m, r.v[k]);
+  return m;
+}
+__device__ __forceinline__ float largest(const Run<__half, 8>& r) {
+  __half2 m = __halves2half2(r.v[0], r.v[1]);
+#pragma unroll
+  for (int k = 2; k < 8; k += 2) m = __hmax2(m, __halves2half2(r.v[k], r.v[k + 1]));
+  return to_f32(__hmax(__low2half(m), __high2half(m)));
+}
+__device__ __forceinline__ float largest(const Run<__nv_bfloat16, 8>& r) {
+  __nv_bfloat162 m = __halves2bfloat162(r.v[0], r.v[1]);
+#pragma unroll
+  for (int k = 2; k < 8; k += 2) m = __hmax2(m, __halves2bfloat162(r.v[k], r.v[k + 1]));
+  return to_f32(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// n runs more.
+template <class T, int U, int N>
+__device__ __forceinline__ void add_runs(ScaledSum& t, const Run<T, U> (&r)[N]) {
+  float m = largest(r[0]);
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, largest(r[j]));
+  const float o1 = fmaxf(t.o, rintf(m * kLog2e)), o = base_of(o1);
+  float2 s[2] = {make_float2(t.s * exp2_fast(t.o - o), 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const Vec<U> f = unpack(r[j]);
+#pragma unroll
+    for (int k = 0; k < U / 2; ++k) {
+      const float2 e = fma2(f.p[k], both(kLog2e), both(-o));
+      s[k & 1] = add2(s[k & 1], make_float2(exp2_fast(e.x), exp2_fast(e.y)));
+    }
+  }
+  t.o = o1;
+  t.s = total(add2(s[0], s[1]));
 }
 
 // One CTA's share of a row: 16-byte runs v0 .. v1 - 1, run i starting at
@@ -103,16 +146,61 @@ __device__ __forceinline__ void term_of(const Policy& a, int64_t t, float w, flo
   slope = w * g;
 }
 
-// A row per cluster of `ranks` CTAs (1 where there are rows enough for the
-// SMs; more, and the row's parts joined through distributed shared memory,
-// where there are few).  A pass for maximum and sum, four 16-byte loads per
-// thread in flight; for the gradient a second pass, which finds the row in L2.
-template <class T>
-__global__ void __launch_bounds__(kRow, 2) policy_kernel(const __grid_constant__ Policy a,
-                                                         int ranks) {
+// The sums of a warp's lanes on one scale; the same in every lane.
+__device__ __forceinline__ ScaledSum join_warp(ScaledSum t) {
+  ScaledSum r;
+  r.o = warp_max(t.o);
+  r.s = warp_sum(t.s * exp2_fast(t.o - base_of(r.o)));
+  return r;
+}
+
+// A run that is not read again.
+template <class T, int U>
+__device__ __forceinline__ Run<T, U> last_read(const Run<T, U>* p) {
+  const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+  return *reinterpret_cast<const Run<T, U>*>(&v);
+}
+
+// The row's sum over the CTA's warps and the row's CTAs; the same in every
+// thread.
+template <int kRow>
+__device__ __forceinline__ ScaledSum join_row(ScaledSum t, ScaledSum* red, ScaledSum* mine,
+                                              int ranks) {
+  constexpr int W = kRow / 32;
+  const int lane = threadIdx.x & 31;
+  t = join_warp(t);
+  __syncthreads();  // (red may still be read from a call before)
+  if (lane == 0) red[threadIdx.x >> 5] = t;
+  __syncthreads();
+  const ScaledSum none = {-INFINITY, 0.f};
+  t = join_warp(lane < W ? red[lane] : none);
+  if (ranks > 1) {
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    if (threadIdx.x == 0) *mine = t;
+    cluster.sync();
+    t = *cluster.map_shared_rank(mine, 0);
+    for (int r = 1; r < ranks; ++r) t = join(t, *cluster.map_shared_rank(mine, r));
+    cluster.sync();  // (no CTA leaves, or writes again, while another reads)
+  }
+  return t;
+}
+
+// A row per cluster of `ranks` CTAs: a pass for the sum, four 16-byte loads per
+// thread in flight, and for the gradient a second one, which goes through the
+// row backwards, to meet what L2 and L1 still have.  What is not needed again
+// (the second pass's reads, the gradient) leaves the caches first.
+//
+// 4096 rows of 128 KB, a fifth of them masked: 171 us (5.7 TB/s) on 512
+// threads, two rows per SM; four rows of 256 threads each, 6 us more, since
+// L2 no longer keeps them all.  A share of the row held in shared memory by a
+// CTA of a cluster, read once: 191 to 259 us over shares and CTA counts; the
+// row's two cluster barriers leave too little in flight.
+template <class T, int kRow>
+__global__ void __launch_bounds__(kRow, 1024 / kRow)
+    policy_kernel(const __grid_constant__ Policy a, int ranks) {
   constexpr int U = 16 / sizeof(T);
-  __shared__ MaxSum red[kRow / 32];
-  __shared__ MaxSum mine;
+  __shared__ ScaledSum red[kRow / 32];
+  __shared__ ScaledSum mine;
   const int rank = ranks > 1 ? blockIdx.x % ranks : 0;
   const int64_t t = ranks > 1 ? blockIdx.x / ranks : blockIdx.x;
   const T* z = (const T*)a.logits + t * a.ldl;
@@ -125,7 +213,7 @@ __global__ void __launch_bounds__(kRow, 2) policy_kernel(const __grid_constant__
   auto put = [&](int i, const Run<T, U>& r) {
     T* q = d + sh.head + i * U;
     if (run16) {
-      *reinterpret_cast<Run<T, U>*>(q) = r;
+      __stcs(reinterpret_cast<uint4*>(q), *reinterpret_cast<const uint4*>(&r));
     } else {
 #pragma unroll
       for (int k = 0; k < U; ++k) q[k] = r.v[k];
@@ -146,57 +234,48 @@ __global__ void __launch_bounds__(kRow, 2) policy_kernel(const __grid_constant__
     return;
   }
   const Run<T, U>* runs = reinterpret_cast<const Run<T, U>*>(z + sh.head);
-  MaxSum ms = {-INFINITY, 0.f};
-  if (edge >= 0) {
-    ms.m = to_f32(z[edge]);
-    ms.s = __expf(ms.m - base_of(ms.m));
-  }
-  for (int i0 = sh.v0 + threadIdx.x; i0 < sh.v1; i0 += kRow * kAhead) {
-    Run<T, U> r[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (i0 + j * kRow < sh.v1) r[j] = runs[i0 + j * kRow];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j * kRow >= sh.v1) break;
-      const Vec<U> f = unpack(r[j]);
-      float m = ms.m;
-#pragma unroll
-      for (int k = 0; k < U / 2; ++k) m = fmaxf(fmaxf(m, f.p[k].x), f.p[k].y);
-      const float o = base_of(m);
-      float2 s = make_float2(ms.s * exp2_fast((ms.m - o) * kLog2e), 0.f);
-#pragma unroll
-      for (int k = 0; k < U / 2; ++k) s = add2(s, exp_less(f.p[k], o));
-      ms.m = m;
-      ms.s = s.x + s.y;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    MaxSum b;
-    b.m = __shfl_xor_sync(0xffffffffu, ms.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, ms.s, o);
-    ms = join(ms, b);
-  }
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ms;
-  __syncthreads();
-  ms = red[0];
-#pragma unroll
-  for (int i = 1; i < kRow / 32; ++i) ms = join(ms, red[i]);
-  if (ranks > 1) {
-    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    if (threadIdx.x == 0) mine = ms;
-    cluster.sync();
-    ms = *cluster.map_shared_rank(&mine, 0);
-    for (int r = 1; r < ranks; ++r) ms = join(ms, *cluster.map_shared_rank(&mine, r));
-    cluster.sync();  // (no CTA leaves while another reads its shared memory)
-  }
-  // every thread: the same numbers from the same inputs
-  const float sum = ms.m == -INFINITY ? NAN : ms.s;  // (-inf throughout: no distribution)
   const int64_t target = a.targets[t];
   const bool valid = target >= 0 && target < a.vocab;
+  // (read before anything is written: the gradient may take the logits' place)
   const float zt = valid ? to_f32(z[target]) : NAN;
-  const float logp = zt - ms.m - logf(sum);
+  ScaledSum sum = {-INFINITY, 0.f};
+  int i0 = sh.v0 + threadIdx.x;
+  for (; i0 + (kAhead - 1) * kRow < sh.v1; i0 += kAhead * kRow) {
+    Run<T, U> r[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) r[j] = runs[i0 + j * kRow];
+    add_runs(sum, r);
+  }
+  for (; i0 < sh.v1; i0 += kRow) {
+    const Run<T, U> r[1] = {runs[i0]};
+    add_runs(sum, r);
+  }
+  if (edge >= 0) {
+    const float x = to_f32(z[edge]) * kLog2e;
+    const ScaledSum one = {rintf(x), exp2_fast(x - base_of(rintf(x)))};
+    sum = join(sum, one);
+  }
+  sum = join_row<kRow>(sum, red, &mine, ranks);
+  // With x log2(e) beyond float32's range, or nothing but -inf, the scale says
+  // nothing: the row's largest element takes its part, 2^((x - m) log2(e)).
+  // (the same for every thread of the row)
+  float m = 0.f;
+  if (!(fabsf(sum.o) < INFINITY) || !(sum.s < INFINITY)) {
+    ScaledSum top = {-INFINITY, 0.f};  // o: the maximum
+    for (int i = sh.v0 + threadIdx.x; i < sh.v1; i += kRow) top.o = fmaxf(top.o, largest(runs[i]));
+    if (edge >= 0) top.o = fmaxf(top.o, to_f32(z[edge]));
+    m = join_row<kRow>(top, red, &mine, ranks).o;
+    sum.o = 0.f, sum.s = 0.f;
+    for (int i = sh.v0 + threadIdx.x; i < sh.v1; i += kRow) {
+      const Vec<U> f = unpack(runs[i]);
+#pragma unroll
+      for (int k = 0; k < U / 2; ++k) sum.s += total(exp_pair(f.p[k], m, 0.f));
+    }
+    if (edge >= 0) sum.s += exp_pair(both(to_f32(z[edge])), m, 0.f).x;
+    sum = join_row<kRow>(sum, red, &mine, ranks);
+  }
+  // every thread: the same numbers from the same inputs
+  const float logp = kLn2 * (fmaf(zt - m, kLog2e, -sum.o) - log2f(sum.s));
   float term = 0.f, slope = 0.f;
   if (a.loss) term_of(a, t, w, logp, term, slope);
   if (threadIdx.x == 0 && rank == 0) {
@@ -205,38 +284,33 @@ __global__ void __launch_bounds__(kRow, 2) policy_kernel(const __grid_constant__
   }
   if (!d) return;
   slope *= a.scale;
-  const float f = -slope / sum;
-  // (in place, the target's logit must be read by every thread before it is overwritten)
-  if (ranks > 1)
-    cooperative_groups::this_cluster().sync();
-  else
-    __syncthreads();
+  const float f = -slope / sum.s;
   if (edge >= 0) {
-    const float g = __expf(to_f32(z[edge]) - ms.m) * f;
+    const float g = exp_pair(both(to_f32(z[edge])), m, sum.o).x * f;
     d[edge] = from_f32<T>(edge == target ? g + slope : g);
   }
   const int64_t at = valid ? target - sh.head : -1;  // within the runs
-  for (int i0 = sh.v0 + threadIdx.x; i0 < sh.v1; i0 += kRow * kAhead) {
+  auto grad_run = [&](int i, const Run<T, U>& r) {
+    Vec<U> v = unpack(r);
+#pragma unroll
+    for (int k = 0; k < U / 2; ++k) v.p[k] = mul2(exp_pair(v.p[k], m, sum.o), both(f));
+    const int64_t k0 = at - (int64_t)i * U;
+    if (k0 >= 0 && k0 < U) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (k == k0) (k & 1 ? v.p[k / 2].y : v.p[k / 2].x) += slope;
+    }
+    put(i, pack<T>(v));
+  };
+  int i1 = sh.v1 - 1 - (int)threadIdx.x;
+  for (; i1 - (kAhead - 1) * kRow >= sh.v0; i1 -= kAhead * kRow) {
     Run<T, U> r[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (i0 + j * kRow < sh.v1) r[j] = runs[i0 + j * kRow];
+    for (int j = 0; j < kAhead; ++j) r[j] = last_read(runs + i1 - j * kRow);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kRow;
-      if (i >= sh.v1) break;
-      Vec<U> v = unpack(r[j]);
-#pragma unroll
-      for (int k = 0; k < U / 2; ++k) v.p[k] = mul2(exp_less(v.p[k], ms.m), both(f));
-      const int64_t k0 = at - (int64_t)i * U;
-      if (k0 >= 0 && k0 < U) {
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (k == k0) (k & 1 ? v.p[k / 2].y : v.p[k / 2].x) += slope;
-      }
-      put(i, pack<T>(v));
-    }
+    for (int j = 0; j < kAhead; ++j) grad_run(i1 - j * kRow, r[j]);
   }
+  for (; i1 >= sh.v0; i1 -= kRow) grad_run(i1, last_read(runs + i1));
 }
 
 // loss = sum of the terms, always in the same order.
@@ -257,19 +331,22 @@ __global__ void __launch_bounds__(1024) policy_sum_kernel(const float* terms, in
   }
 }
 
-// CTAs per row: while the rows leave SMs (two CTAs each) without work, shares
-// of a row down to 16 KB.
-inline int ranks_of(const Policy& a, int es) {
+// CTAs per row: while the rows leave SMs without work, shares of a row down to
+// 8 KB.  (With rows enough, two CTAs per row cost more in their barriers than
+// a fuller last round gains: 2049 rows of 200 KB in 120 us against 95.)
+inline int ranks_of(const Policy& a, int es, int per_sm) {
   int r = 1;
-  while (r < 8 && a.tokens * r * 2 <= 2 * sm_count() && (int64_t)a.vocab * es > r * 32768) r *= 2;
+  while (r < 8 && a.tokens * r * 2 <= per_sm * sm_count() &&
+         (int64_t)a.vocab * es > r * (16 << 10))
+    r *= 2;
   return r;
 }
 
-template <class T>
+template <class T, int kRow>
 int launch_rows(const Policy& a, cudaStream_t s) {
-  for (int64_t t0 = 0; t0 < a.tokens; t0 += 1 << 30) {
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += 1 << 27) {
     Policy b = a;
-    b.tokens = std::min<int64_t>(a.tokens - t0, 1 << 30);
+    b.tokens = std::min<int64_t>(a.tokens - t0, 1 << 27);
     b.logits = (const T*)a.logits + t0 * a.ldl;
     if (a.d) b.d = (T*)a.d + t0 * a.ldd;
     b.targets += t0, b.logp += t0;
@@ -278,7 +355,7 @@ int launch_rows(const Policy& a, cudaStream_t s) {
     if (a.ref) b.ref += t0;
     ProfScope prof(ROT_PROF_ELEMENTWISE,
                    (double)b.tokens * a.vocab * sizeof(T) * (a.d ? 2 : 1), s);
-    const int ranks = ranks_of(b, sizeof(T));
+    const int ranks = ranks_of(b, sizeof(T), 1024 / kRow);
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(b.tokens * ranks));
     c.blockDim = dim3(kRow);
@@ -288,7 +365,7 @@ int launch_rows(const Policy& a, cudaStream_t s) {
     at.val.clusterDim.x = ranks, at.val.clusterDim.y = at.val.clusterDim.z = 1;
     c.attrs = &at;
     c.numAttrs = ranks > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&c, policy_kernel<T>, b, ranks) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&c, policy_kernel<T, kRow>, b, ranks) != cudaSuccess) {
       cudaGetLastError();
       return ROT_ECUDA;
     }
@@ -296,10 +373,14 @@ int launch_rows(const Policy& a, cudaStream_t s) {
   return ROT_OK;
 }
 
+template <class T>
+int launch_type(const Policy& a, cudaStream_t s) {
+  return a.d ? launch_rows<T, 512>(a, s) : launch_rows<T, 256>(a, s);
+}
 int launch_policy(const Policy& a, int32_t type, cudaStream_t s) {
-  if (type == ROT_TYPE_F32) return launch_rows<float>(a, s);
-  if (type == ROT_TYPE_F16) return launch_rows<__half>(a, s);
-  return launch_rows<__nv_bfloat16>(a, s);
+  if (type == ROT_TYPE_F32) return launch_type<float>(a, s);
+  if (type == ROT_TYPE_F16) return launch_type<__half>(a, s);
+  return launch_type<__nv_bfloat16>(a, s);
 }
 
 bool bad_logits(const void* logits, int64_t ldl, const int64_t* targets, const float* logp,

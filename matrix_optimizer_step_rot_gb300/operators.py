@@ -350,7 +350,10 @@ def status(device="cuda") -> int:
 
 
 def _fp8_empty(rows: int, cols: int, block_rows: int, dtype, device) -> Fp8Matrix:
-    data = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=dtype,
+    # rows of whole 128-byte lines, as the product's loads take them (6144 x 2048 x 4099: 47 us,
+    # against 71 with rows 4112 bytes apart), where that is not several times the matrix
+    to = 128 if cols > 64 else 16
+    data = torch.empty_strided((rows, cols), ((cols + to - 1) // to * to, 1), dtype=dtype,
                                device=device)
     scale = torch.empty(((cols + 127) // 128, -(-rows // block_rows)), dtype=torch.uint8,
                         device=device)
@@ -358,6 +361,7 @@ def _fp8_empty(rows: int, cols: int, block_rows: int, dtype, device) -> Fp8Matri
 
 
 def _fp8_ld(t: torch.Tensor) -> int:
+    # (of a single row, torch leaves the stride arbitrary)
     return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else (t.shape[1] + 15) // 16 * 16
 
 
