@@ -25,6 +25,7 @@ struct Policy {
   float lo, hi, kl, scale;
 };
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kAhead = 4;  // 16-byte loads of a thread in flight
 
 // Sum of exponentials on a running scale: the sum of 2^(x log2(e) - o) with a
@@ -48,7 +49,6 @@ __device__ __forceinline__ ScaledSum join(ScaledSum a, ScaledSum b) {
   r.s = a.s * exp2_fast(a.o - o) + b.s * exp2_fast(b.o - o);
   return r;
 }
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // 2^((x - m) log2(e) - o) of both halves.
 __device__ __forceinline__ float2 exp_pair(float2 x, float m, float o) {
@@ -125,10 +125,32 @@ __device__ __forceinline__ int edge_of(const Share& s, int vocab, int rank, int 
   return -1;
 }
 
-// The token's term and the slope d(loss)/d(logp), from its log-probability.
+// The log-probability (x log2(e) - o - log2(s)) ln 2 as a float32 and what its
+// rounding leaves.  x log2(e) and the products with ln 2 carry their rounding
+// errors along, and s = 2^k f has its whole exponents taken off exactly: a
+// policy's ratios and their sum lose nothing to a logp of 10 being rounded to
+// 2^-21.
+__device__ __forceinline__ float log_prob(float x, float o, float s, float& rest) {
+  constexpr float kLog2eRest = 1.9259629911e-8f, kLn2Rest = -1.9046542999e-9f;
+  const float hi = x * kLog2e;
+  rest = 0.f;
+  if (!(fabsf(hi) < INFINITY) || !(s < INFINITY)) return kLn2 * (hi - o - log2f(s));
+  const float lo = fmaf(x, kLog2e, -hi) + x * kLog2eRest;
+  const int k = (__float_as_int(s) - 0x3F400000) >> 23;  // f in [0.75, 1.5)
+  const float f = __int_as_float(__float_as_int(s) - (k << 23));
+  const float d = (hi - o) - (float)k, r = lo - log2f(f);
+  const float t = d + r, e = r - (t - d);
+  const float p = kLn2 * t, q = fmaf(kLn2, t, -p) + (kLn2Rest * t + kLn2 * e);
+  const float logp = p + q;
+  rest = q - (logp - p);
+  return logp;
+}
+
+// The token's term and the slope d(loss)/d(logp), from its log-probability
+// logp + rest.
 __device__ __forceinline__ void term_of(const Policy& a, int64_t t, float w, float logp,
-                                        float& term, float& slope) {
-  const float adv = a.adv[t], ratio = expf(logp - a.old[t]);
+                                        float rest, float& term, float& slope) {
+  const float adv = a.adv[t], ratio = expf((logp - a.old[t]) + rest);
   // (comparisons, not fminf and fmaxf: NaN has to stay)
   const float lo = 1.f - a.lo, hi = 1.f + a.hi;
   const float clipped = ratio < lo ? lo : ratio > hi ? hi : ratio;
@@ -138,7 +160,7 @@ __device__ __forceinline__ void term_of(const Policy& a, int64_t t, float w, flo
   float v = -(plain != plain || through ? plain : bounded);
   float g = plain != plain || through ? -plain : 0.f;
   if (a.ref) {
-    const float r = a.ref[t] - logp, em = expm1f(r);
+    const float r = (a.ref[t] - logp) - rest, em = expm1f(r);
     v += a.kl * (em - r);
     g -= a.kl * em;
   }
@@ -275,9 +297,9 @@ __global__ void __launch_bounds__(kRow, 1024 / kRow)
     sum = join_row<kRow>(sum, red, &mine, ranks);
   }
   // every thread: the same numbers from the same inputs
-  const float logp = kLn2 * (fmaf(zt - m, kLog2e, -sum.o) - log2f(sum.s));
-  float term = 0.f, slope = 0.f;
-  if (a.loss) term_of(a, t, w, logp, term, slope);
+  float rest, term = 0.f, slope = 0.f;
+  const float logp = log_prob(zt - m, sum.o, sum.s, rest);
+  if (a.loss) term_of(a, t, w, logp, rest, term, slope);
   if (threadIdx.x == 0 && rank == 0) {
     a.logp[t] = logp;
     if (a.loss) a.terms[t] = term;
