@@ -1,4 +1,5 @@
-"""Compile librot.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Compile librot.so (the C-ABI library) in-tree for sm_103a with nvcc, and
+_rot_torch.so (the operators on torch tensors) with the host compiler.
 
 Each translation unit compiles in parallel into _build/, then one link step
 writes matrix_optimizer_step_rot_gb300/librot.so.  Rebuilds only what changed
@@ -23,6 +24,11 @@ LIB = os.path.join(PKG, "librot.so")
 BUILD_CHECK = os.path.join(PKG, "_build_check")
 LIB_CHECK = os.path.join(PKG, "librot_check.so")
 
+# the operators on torch tensors: an extension module that calls librot's entry
+# points by address (it does not link against the library)
+TORCH_SRC = os.path.join(CSRC, "torch", "torch_ops.cpp")
+TORCH_EXT = os.path.join(PKG, "_rot_torch.so")
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off",
               "-I", INCLUDE,
@@ -46,9 +52,34 @@ def _headers():
     return hs + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
 
 
+def _torch_command():
+    """Compile command of _rot_torch.so, or None if it is up to date (for the
+    torch at hand)."""
+    import sysconfig
+
+    import torch
+
+    stamp = os.path.join(BUILD, "torch_version")
+    if os.path.exists(TORCH_EXT) and os.path.exists(stamp) \
+            and open(stamp).read() == torch.__version__ \
+            and os.path.getmtime(TORCH_EXT) > max(map(os.path.getmtime, [TORCH_SRC, *_headers()])):
+        return None
+    root = os.path.dirname(torch.__file__)
+    nvcc = _nvcc()
+    cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-I", os.path.join(root, "include"),
+            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+            TORCH_SRC, "-o", TORCH_EXT + ".tmp", "-L", os.path.join(root, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False, extra_flags=None, check: bool = False) -> str:
-    """Build librot.so (check: the bounds-checked librot_check.so) if needed;
-    returns its path.  Raises on compiler errors."""
+    """Build librot.so (check: the bounds-checked librot_check.so) if needed, and
+    _rot_torch.so with the plain one; returns the library's path.  Raises on
+    compiler errors."""
     build_dir, lib = (BUILD_CHECK, LIB_CHECK) if check else (BUILD, LIB)
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -69,13 +100,21 @@ def build(verbose: bool = False, extra_flags=None, check: bool = False) -> str:
         return cmd, r
 
     stale_cmds = [c for s, c, _ in jobs if s]
-    if stale_cmds:
-        with ThreadPoolExecutor(max_workers=min(8, len(stale_cmds))) as ex:
-            for cmd, r in ex.map(run, stale_cmds):
+    torch_cmd = None if check else _torch_command()
+    if stale_cmds or torch_cmd:
+        cmds = stale_cmds + ([torch_cmd] if torch_cmd else [])
+        with ThreadPoolExecutor(max_workers=min(12, len(cmds))) as ex:
+            for cmd, r in ex.map(run, cmds):
                 if verbose and r.stderr:
                     sys.stderr.write(r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+                    raise RuntimeError(f"{cmd[0]} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if torch_cmd:
+        import torch
+
+        os.replace(TORCH_EXT + ".tmp", TORCH_EXT)
+        with open(os.path.join(BUILD, "torch_version"), "w") as f:
+            f.write(torch.__version__)
     objs = [o for _, _, o in jobs]
     if stale_cmds or not os.path.exists(lib):
         cmd = [nvcc, *ARCH, "-shared", "-o", lib + ".tmp", *objs]

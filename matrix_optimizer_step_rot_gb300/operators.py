@@ -5,31 +5,34 @@ dropout in front of it, the clipped policy loss with its gradient, and linear
 layers in 8-bit floating point with power-of-two block scales.  Between them
 they carry a training step from hidden states to the float32 gradients that
 `optimizer.RotatedAdam` reads.  include/rot_ops.h states the formulas, layouts
-and errors; every function here checks its tensors, allocates its outputs and
-workspace with torch and runs the library's kernels on the current stream, or
-on `stream` (a torch.cuda.Stream: outputs and workspaces then belong to it, and
-the inputs are marked as used on it; ordering it after their producers is the
-caller's).  There is no other path than the library's.
+and errors.  Every function checks its tensors (ValueError), allocates its
+outputs and workspace with torch and runs the library's kernels on the current
+stream (csrc/torch/torch_ops.cpp), or on `stream` (a torch.cuda.Stream: outputs
+and workspaces then belong to it, and the inputs are marked as used on it;
+ordering it after their producers is the caller's).  Tensors are on the current
+device; a tensor of more than two dimensions is rows of its last one.  There is
+no other path than the library's.  The first 8-bit product on a device
+allocates its status word: let it run before a stream capture.
 """
 
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 
 from . import binding as B
 
-_TYPES = {torch.float32: B.ROT_TYPE_F32, torch.float16: B.ROT_TYPE_F16,
-          torch.bfloat16: B.ROT_TYPE_BF16}
-_FORMATS = {torch.float8_e4m3fn: B.ROT_TYPE_E4M3, torch.float8_e5m2: B.ROT_TYPE_E5M2}
+_TYPES = (torch.float32, torch.float16, torch.bfloat16)
+_FORMATS = (torch.float8_e4m3fn, torch.float8_e5m2)
 
 
 class Fp8Matrix(NamedTuple):
     """An R x C matrix in 8 bits: `data` (float8_e4m3fn or float8_e5m2; rows a
-    multiple of 16 bytes apart) under one power-of-two scale for each block of
-    `block_rows` x 128 elements.  scale: uint8, [ceil(C / 128), ceil(R /
-    block_rows)], a byte e for 2^(e - 127), 255 for NaN."""
+    multiple of 16 bytes apart, best of 128) under one power-of-two scale for
+    each block of `block_rows` x 128 elements.  scale: uint8, [ceil(C / 128),
+    ceil(R / block_rows)], a byte e for 2^(e - 127), 255 for NaN."""
     data: torch.Tensor
     scale: torch.Tensor
     block_rows: int = 1
@@ -44,79 +47,41 @@ class Fp8Matrix(NamedTuple):
         return self.data.float() * s
 
 
-# ---------------------------------------------------------------------------
-# argument checks
-# ---------------------------------------------------------------------------
+_native = None
 
 
-def _fail(what: str):
-    raise ValueError(what)
-
-
-def _matrix(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """t as a 2-D view with unit column stride: leading dimensions fold into
-    the rows.  like: must have its shape, type and device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        _fail(f"{name}: expected a CUDA tensor")
-    if like is not None:
-        if t.dtype != like.dtype or t.shape != like.shape or t.get_device() != like.get_device():
-            _fail(f"{name}: expected shape {tuple(like.shape)}, {like.dtype} on {like.device}, got "
-                  f"{tuple(t.shape)}, {t.dtype} on {t.device}")
-    else:
-        if t.dtype not in _TYPES:
-            _fail(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
-        if t.get_device() != _current_device():
-            _fail(f"{name}: on {t.device}, but the current device is cuda:{_current_device()}")
-    if t.dim() != 2:
-        if t.dim() == 0:
-            _fail(f"{name}: expected at least one dimension")
-        try:
-            t = t.view(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
-        except RuntimeError:
-            _fail(f"{name}: its leading dimensions cannot be folded into rows without a copy")
-    if not t.is_contiguous():
-        rows, cols = t.shape
-        if cols > 1 and t.stride(1) != 1:
-            _fail(f"{name}: its last dimension is not contiguous")
-        if rows > 1 and t.stride(0) < cols:
-            _fail(f"{name}: its rows overlap")
-    return t
-
-
-def _ld(t: Optional[torch.Tensor]) -> int:
-    """Row pitch of a _matrix() view (torch leaves the stride of a single row,
-    or of no row, arbitrary)."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _vector(t: Optional[torch.Tensor], name: str, size: int, like: torch.Tensor,
-            dtypes) -> Optional[torch.Tensor]:
-    """t, `size` contiguous elements of one of `dtypes` on like's device (or None)."""
-    if t is not None and (not isinstance(t, torch.Tensor) or t.dtype not in dtypes
-                          or t.get_device() != like.get_device() or t.shape != (size,)
-                          or not t.is_contiguous()):
-        _fail(f"{name}: expected a contiguous tensor of {size} elements, "
-              f"{' or '.join(str(d) for d in dtypes)}, on {like.device}")
-    return t
-
-
-def _ptr(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
+def _load():
+    """The extension module, bound to the loaded library's entry points (raises
+    if either has not been built)."""
+    global _native
+    L = B.lib()
+    try:
+        from . import _rot_torch
+    except ImportError as e:
+        raise RuntimeError("_rot_torch.so is missing or does not load: build it with "
+                           "matrix_optimizer_step_rot_gb300.build.build()") from e
+    _rot_torch.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+                     for n in B.header_symbols()}, B.RotError)
+    _native = _rot_torch
+    return _native
 
 
 def _word(x: int, name: str) -> int:
     if not 0 <= x < 1 << 64:
-        _fail(f"{name}: expected a whole number from 0 to 2^64 - 1")
+        raise ValueError(f"{name}: expected a whole number from 0 to 2^64 - 1")
     return x
 
 
-_current_device = torch.cuda.current_device
+def _tensors(**given) -> None:
+    for name, t in given.items():
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
 
 
-def _stream() -> int:
-    return torch._C._cuda_getCurrentRawStream(_current_device())
+def _fp8(m, name: str) -> Fp8Matrix:
+    if not isinstance(m, Fp8Matrix):
+        raise ValueError(f"{name}: expected an Fp8Matrix, got {type(m).__name__}")
+    return m
 
 
 def _on(stream, call, *inputs):
@@ -146,19 +111,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
     if stream is not None:
         return _on(stream, lambda: dropout(x, p, seed, offset, residual=residual, out=out),
                    x, residual, out)
-    x2 = _matrix(x, "x")
-    rows, cols = x2.shape
-    r2 = None if residual is None else _matrix(residual, "residual", x)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        ldo, po = cols, out.data_ptr()
-    else:
-        o2 = _matrix(out, "out", x)
-        ldo, po = _ld(o2), o2.data_ptr()
-    B._check(B.lib().rot_dropout(x2.data_ptr(), _ld(x2), _ptr(r2), _ld(r2), po, ldo, rows, cols,
-                                 _TYPES[x.dtype], p, _word(seed, "seed"), _word(offset, "offset"),
-                                 _stream()), "rot_dropout")
-    return out
+    return (_native or _load()).dropout(x, p, _word(seed, "seed"), _word(offset, "offset"),
+                                        residual, out)
 
 
 def dropout_backward(dy: torch.Tensor, p: float, seed: int, offset: int = 0, *,
@@ -185,23 +139,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         return _on(stream, lambda: layer_norm(x, weight, bias, eps, residual=residual, p=p,
                                               seed=seed, offset=offset),
                    x, weight, bias, residual)
-    x2 = _matrix(x, "x")
-    rows, cols = x2.shape
-    r2 = None if residual is None else _matrix(residual, "residual", x)
-    if weight is None:
-        _fail("weight: expected a tensor")
-    _vector(weight, "weight", cols, x, (torch.float32, x.dtype))
-    _vector(bias, "bias", cols, x, (weight.dtype,))
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = x if residual is None and p == 0 else torch.empty_like(y)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    B._check(B.lib().rot_layer_norm_forward(
-        x2.data_ptr(), _ld(x2), _ptr(r2), _ld(r2), weight.data_ptr(), _ptr(bias),
-        _TYPES[weight.dtype], 0 if h is x else h.data_ptr(), cols, y.data_ptr(), cols,
-        mean.data_ptr(), rstd.data_ptr(), rows, cols, _TYPES[x.dtype], eps, p,
-        _word(seed, "seed"), _word(offset, "offset"), _stream()), "rot_layer_norm_forward")
-    return y, h, mean, rstd
+    _tensors(weight=weight)
+    return (_native or _load()).layer_norm(x, weight, bias, eps, residual, p, _word(seed, "seed"),
+                                           _word(offset, "offset"))
 
 
 def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -217,44 +157,15 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, r
         return _on(stream, lambda: layer_norm_backward(dy, h, mean, rstd, weight, dh=dh, p=p,
                                                        seed=seed, offset=offset, bias=bias),
                    dy, h, mean, rstd, weight, dh)
-    dy2, h2 = _matrix(dy, "dy"), _matrix(h, "h", dy)
-    rows, cols = dy2.shape
-    d2 = None if dh is None else _matrix(dh, "dh", dy)
-    if weight is None:
-        _fail("weight: expected a tensor")
-    _vector(weight, "weight", cols, dy, (torch.float32, dy.dtype))
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if not isinstance(t, torch.Tensor) or not t.is_contiguous():
-            _fail(f"{name}: expected a contiguous tensor")
-        _vector(t if t.dim() == 1 else t.view(-1), name, rows, dy, (torch.float32,))
-    L = B.lib()
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    dres = torch.empty_like(dx) if p > 0 else dx
-    dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
-    dbias = torch.empty_like(dweight) if bias else None
-    need = L.rot_layer_norm_work_bytes(rows, cols)
-    work = torch.empty(need, dtype=torch.uint8, device=dy.device)
-    B._check(L.rot_layer_norm_backward(
-        dy2.data_ptr(), _ld(dy2), h2.data_ptr(), _ld(h2), mean.data_ptr(), rstd.data_ptr(),
-        weight.data_ptr(), _TYPES[weight.dtype], _ptr(d2), _ld(d2),
-        dres.data_ptr() if p > 0 else 0, cols, dx.data_ptr(), cols, dweight.data_ptr(),
-        _ptr(dbias), rows, cols, _TYPES[dy.dtype], p, _word(seed, "seed"),
-        _word(offset, "offset"), work.data_ptr(), need, _stream()), "rot_layer_norm_backward")
-    return dx, dres, dweight, dbias
+    _tensors(h=h, mean=mean, rstd=rstd, weight=weight)
+    return (_native or _load()).layer_norm_backward(dy, h, mean, rstd, weight, dh, p,
+                                                    _word(seed, "seed"), _word(offset, "offset"),
+                                                    bias)
 
 
 # ---------------------------------------------------------------------------
 # policy loss
 # ---------------------------------------------------------------------------
-
-
-def _per_token(t: torch.Tensor, name: str, logits: torch.Tensor, dtype=torch.float32) -> int:
-    """Address of a contiguous tensor with an element for each row of logits."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != logits.shape[:-1] \
-            or not t.is_contiguous() or t.get_device() != logits.get_device():
-        _fail(f"{name}: expected a contiguous {dtype} tensor of shape "
-              f"{tuple(logits.shape[:-1])} on {logits.device}")
-    return t.data_ptr()
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *,
@@ -265,14 +176,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *,
     if stream is not None:
         return _on(stream, lambda: token_logprobs(logits, targets, weights=weights),
                    logits, targets, weights)
-    z = _matrix(logits, "logits")
-    pt = _per_token(targets, "targets", logits, torch.int64)
-    pw = 0 if weights is None else _per_token(weights, "weights", logits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    B._check(B.lib().rot_token_logprobs(z.data_ptr(), _ld(z), pt, pw, logp.data_ptr(), z.shape[0],
-                                        z.shape[1], _TYPES[logits.dtype], _stream()),
-             "rot_token_logprobs")
-    return logp
+    _tensors(targets=targets)
+    return (_native or _load()).token_logprobs(logits, targets, weights)
 
 
 def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor,
@@ -292,47 +197,30 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
             logits, targets, old_logp, advantages, weights, ref_logp=ref_logp, clip_low=clip_low,
             clip_high=clip_high, kl_coef=kl_coef, grad=grad, grad_scale=grad_scale, out=out),
             logits, targets, old_logp, advantages, weights, ref_logp, out)
-    z = _matrix(logits, "logits")
-    tokens, vocab = z.shape
-    pt = _per_token(targets, "targets", logits, torch.int64)
-    po = _per_token(old_logp, "old_logp", logits)
-    pa = _per_token(advantages, "advantages", logits)
-    pw = _per_token(weights, "weights", logits)
-    pr = 0 if ref_logp is None else _per_token(ref_logp, "ref_logp", logits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    loss = torch.empty((), dtype=torch.float32, device=logits.device)
-    terms = torch.empty_like(logp)
-    if not grad:
-        out, pd, ldd = None, 0, 0
-    elif out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        pd, ldd = out.data_ptr(), vocab
-    else:
-        o2 = _matrix(out, "out", logits)
-        pd, ldd = o2.data_ptr(), _ld(o2)
-    B._check(B.lib().rot_policy_loss(
-        z.data_ptr(), _ld(z), pt, po, pr, pa, pw, loss.data_ptr(), logp.data_ptr(),
-        terms.data_ptr(), pd, ldd, tokens,
-        vocab, _TYPES[logits.dtype], clip_low, clip_high, kl_coef, grad_scale, _stream()),
-        "rot_policy_loss")
-    return loss, logp, out
+    _tensors(targets=targets, old_logp=old_logp, advantages=advantages, weights=weights)
+    return (_native or _load()).policy_loss(logits, targets, old_logp, advantages, weights,
+                                            ref_logp, clip_low, clip_high, kl_coef, grad,
+                                            grad_scale, out)
 
 
 # ---------------------------------------------------------------------------
 # 8-bit matrices and linear layers
 # ---------------------------------------------------------------------------
 
-_status = {}  # device index -> the products' status word
+_status = {}  # device index -> (the products' status word, its address)
 
 
 def _status_word(like: torch.Tensor) -> int:
-    """Address of the status word of like's device."""
+    """Address of the status word of like's device (0 for a tensor that the
+    call will refuse)."""
     i = like.get_device()
-    word = _status.get(i)
-    if word is None:
-        word = _status[i] = torch.zeros(1, dtype=torch.int32, device=like.device)
+    if i < 0:
+        return 0
+    if i not in _status:
+        word = torch.zeros(1, dtype=torch.int32, device=like.device)
         torch.cuda.synchronize(word.device)  # (later calls may be on any stream)
-    return word.data_ptr()
+        _status[i] = word, word.data_ptr()
+    return _status[i][1]
 
 
 def status(device="cuda") -> int:
@@ -340,29 +228,14 @@ def status(device="cuda") -> int:
     ROT_OK, or ROT_ETIMEOUT if a device-side wait gave up since the last
     call."""
     device = torch.device(device)
-    word = _status.get(_current_device() if device.index is None else device.index)
+    i = torch.cuda.current_device() if device.index is None else device.index
     torch.cuda.synchronize(device)
-    if word is None:
+    if i not in _status:
         return B.ROT_OK
+    word = _status[i][0]
     code = int(word.item())
     word.zero_()
     return code
-
-
-def _fp8_empty(rows: int, cols: int, block_rows: int, dtype, device) -> Fp8Matrix:
-    # rows of whole 128-byte lines, as the product's loads take them (6144 x 2048 x 4099: 47 us,
-    # against 71 with rows 4112 bytes apart), where that is not several times the matrix
-    to = 128 if cols > 64 else 16
-    data = torch.empty_strided((rows, cols), ((cols + to - 1) // to * to, 1), dtype=dtype,
-                               device=device)
-    scale = torch.empty(((cols + 127) // 128, -(-rows // block_rows)), dtype=torch.uint8,
-                        device=device)
-    return Fp8Matrix(data, scale, block_rows)
-
-
-def _fp8_ld(t: torch.Tensor) -> int:
-    # (of a single row, torch leaves the stride arbitrary)
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else (t.shape[1] + 15) // 16 * 16
 
 
 def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, rows: bool = True,
@@ -374,49 +247,12 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, rows: bool = True,
     if stream is not None:
         return _on(stream, lambda: fp8_quantize(x, block_rows=block_rows, rows=rows,
                                                 transposed=transposed, dtype=dtype), x)
-    x2 = _matrix(x, "x")
-    if block_rows not in (1, 128):
-        _fail("block_rows: expected 1 or 128")
     if dtype not in _FORMATS:
-        _fail("dtype: expected float8_e4m3fn or float8_e5m2")
-    if not rows and not transposed:
-        _fail("nothing to write: rows and transposed are both false")
-    R, C = x2.shape
-    q = _fp8_empty(R, C, block_rows, dtype, x.device) if rows else None
-    t = _fp8_empty(C, R, block_rows, dtype, x.device) if transposed else None
-    qa = (q.data.data_ptr(), _fp8_ld(q.data), q.scale.data_ptr(), q.scale.shape[1]) if rows \
-        else (0, 0, 0, 0)
-    ta = (t.data.data_ptr(), _fp8_ld(t.data), t.scale.data_ptr(), t.scale.shape[1]) \
-        if transposed else (0, 0, 0, 0)
-    B._check(B.lib().rot_fp8_quantize(x2.data_ptr(), _ld(x2), R, C, _TYPES[x.dtype],
-                                      _FORMATS[dtype], block_rows, *qa, *ta, _stream()),
-             "rot_fp8_quantize")
-    return q, t
-
-
-def _operand(m: Fp8Matrix, name: str, device: int = -1):
-    """The entry points' arguments for m, on `device` (any: the current one)."""
-    if not isinstance(m, Fp8Matrix):
-        _fail(f"{name}: expected an Fp8Matrix")
-    d, sc, block_rows = m
-    if not isinstance(d, torch.Tensor) or not d.is_cuda or d.dtype not in _FORMATS \
-            or d.dim() != 2 or (d.shape[1] > 1 and d.stride(1) != 1):
-        _fail(f"{name}: expected a 2-D float8_e4m3fn or float8_e5m2 CUDA tensor of unit column "
-              "stride")
-    if d.get_device() != (_current_device() if device < 0 else device):
-        _fail(f"{name}: on {d.device}, expected cuda:{_current_device() if device < 0 else device}")
-    (rows, cols), ld, p = d.shape, _fp8_ld(d), d.data_ptr()
-    if p % 16 or ld % 16 or ld < cols:
-        _fail(f"{name}: its rows must start on multiples of 16 bytes")
-    if block_rows not in (1, 128):
-        _fail(f"{name}: block_rows must be 1 or 128")
-    blocks = -(-rows // block_rows)
-    if not isinstance(sc, torch.Tensor) or sc.dtype != torch.uint8 \
-            or sc.get_device() != d.get_device() or sc.shape != (-(-cols // 128), blocks) \
-            or not sc.is_contiguous():
-        _fail(f"{name}: expected a contiguous uint8 scale of shape {(-(-cols // 128), blocks)} "
-              f"on {d.device}")
-    return p, ld, _FORMATS[d.dtype], sc.data_ptr(), blocks, block_rows
+        raise ValueError("dtype: expected float8_e4m3fn or float8_e5m2")
+    q, t = (_native or _load()).fp8_quantize(x, block_rows, rows, transposed,
+                                             dtype == torch.float8_e5m2)
+    return (None if q is None else Fp8Matrix(q[0], q[1], block_rows),
+            None if t is None else Fp8Matrix(t[0], t[1], block_rows))
 
 
 def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, dtype=torch.float32,
@@ -427,33 +263,10 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, dtype=torch.float32,
     if stream is not None:
         return _on(stream, lambda: fp8_matmul(a, b, dtype=dtype, out=out, accumulate=accumulate),
                    a, b, out)
-    pa = _operand(a, "a")
-    pb = _operand(b, "b", a.data.get_device())
-    (M, K), N = a.data.shape, b.data.shape[0]
-    if b.data.shape[1] != K:
-        _fail(f"b: expected {K} columns, got {b.data.shape[1]}")
-    out, ldo = _product_out(out, M, N, dtype, accumulate, a.data)
-    L = B.lib()
-    need = L.rot_fp8_gemm_work_bytes(M, N, K)
-    work = torch.empty(need, dtype=torch.uint8, device=out.device) if need else None
-    B._check(L.rot_fp8_gemm(M, N, K, *pa, *pb, out.data_ptr(), ldo, _TYPES[out.dtype],
-                            int(accumulate), _ptr(work), need, _status_word(out), _stream()),
-             "rot_fp8_gemm")
-    return out
-
-
-def _product_out(out, M: int, N: int, dtype, accumulate: bool, like: torch.Tensor):
-    """(out, its row pitch): the tensor given, checked, or a new one."""
-    if accumulate and (out is None or out.dtype != torch.float32):
-        _fail("accumulate: expected a float32 out")
-    if out is None:
-        if dtype not in _TYPES:
-            _fail("dtype: expected float32, float16 or bfloat16")
-        return torch.empty((M, N), dtype=dtype, device=like.device), N
-    if out.shape != (M, N):
-        _fail(f"out: expected shape {(M, N)}")
-    _matrix(out, "out")
-    return out, max(_ld(out), N)
+    if dtype not in _TYPES:
+        raise ValueError("dtype: expected float32, float16 or bfloat16")
+    return (_native or _load()).fp8_matmul(*_fp8(a, "a"), *_fp8(b, "b"), dtype, out, accumulate,
+                                           _status_word(a.data))
 
 
 def fp8_linear(x: torch.Tensor, weight: Fp8Matrix, *, stream=None) -> torch.Tensor:
@@ -461,19 +274,7 @@ def fp8_linear(x: torch.Tensor, weight: Fp8Matrix, *, stream=None) -> torch.Tens
     is kept in 8 bits by the caller (fp8_quantize(w, block_rows=128))."""
     if stream is not None:
         return _on(stream, lambda: fp8_linear(x, weight), x, weight)
-    x2 = _matrix(x, "x")
-    pw = _operand(weight, "weight")
-    (tokens, inner), outer = x2.shape, weight.data.shape[0]
-    if weight.data.shape[1] != inner:
-        _fail(f"weight: expected {inner} columns, got {weight.data.shape[1]}")
-    L = B.lib()
-    y = torch.empty((*x.shape[:-1], outer), dtype=x.dtype, device=x.device)
-    need = L.rot_fp8_linear_work_bytes(tokens, inner, outer)
-    work = torch.empty(need, dtype=torch.uint8, device=x.device)
-    B._check(L.rot_fp8_linear(tokens, inner, outer, x2.data_ptr(), _ld(x2), _TYPES[x.dtype], *pw,
-                              y.data_ptr(), outer, work.data_ptr(), need, _status_word(x),
-                              _stream()), "rot_fp8_linear")
-    return y
+    return (_native or _load()).fp8_linear(x, *_fp8(weight, "weight"), _status_word(x))
 
 
 def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight_t: Fp8Matrix, *,
@@ -488,22 +289,6 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight_t: Fp8Matrix, 
         return _on(stream, lambda: fp8_linear_backward(dy, x, weight_t, dw=dw,
                                                        accumulate=accumulate),
                    dy, x, weight_t, dw)
-    dy2, x2 = _matrix(dy, "dy"), _matrix(x, "x")
-    if x.dtype != dy.dtype or x2.shape[0] != dy2.shape[0]:
-        _fail(f"x: expected {dy2.shape[0]} rows of {dy.dtype}, got {x2.shape[0]} of {x.dtype}")
-    pw = _operand(weight_t, "weight_t")
-    (tokens, outer), inner = dy2.shape, x2.shape[1]
-    if weight_t.data.shape != (inner, outer):
-        _fail(f"weight_t: expected shape {(inner, outer)}, got {tuple(weight_t.data.shape)}")
-    if dw is not None and dw.dtype != torch.float32:
-        _fail("dw: expected float32")
-    dw, ldw = _product_out(dw, outer, inner, torch.float32, accumulate, x)
-    L = B.lib()
-    dx = torch.empty((*dy.shape[:-1], inner), dtype=dy.dtype, device=dy.device)
-    need = L.rot_fp8_linear_backward_work_bytes(tokens, inner, outer)
-    work = torch.empty(need, dtype=torch.uint8, device=x.device)
-    B._check(L.rot_fp8_linear_backward(
-        tokens, inner, outer, dy2.data_ptr(), _ld(dy2), x2.data_ptr(), _ld(x2), _TYPES[x.dtype],
-        *pw, dx.data_ptr(), inner, dw.data_ptr(), ldw, int(accumulate), work.data_ptr(), need,
-        _status_word(x), _stream()), "rot_fp8_linear_backward")
-    return dx, dw
+    _tensors(x=x)
+    return (_native or _load()).fp8_linear_backward(dy, x, *_fp8(weight_t, "weight_t"), dw,
+                                                    accumulate, _status_word(x))
