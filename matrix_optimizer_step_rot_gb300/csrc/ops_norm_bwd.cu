@@ -1,0 +1,348 @@
+// Layer norm backward (include/rot_ops.h): the rows' gradients, and the weight
+// gradient as partial sums and their join.  Bound by HBM, with dropout nearly
+// as long in the generator's arithmetic.
+#include <algorithm>
+
+#include "ops_norm.cuh"
+#include "profile.h"
+
+namespace rot {
+namespace ops {
+namespace {
+
+// The gradient of one run, g, written out; dropped into dx.  d: the run of
+// dh, already loaded.
+template <class T, int U>
+__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, Vec<U>& g,
+                                           const Run<T, U>& d) {
+  if (a.dh) {
+    const Vec<U> v = unpack(d);
+#pragma unroll
+    for (int k = 0; k < Vec<U>::P; ++k) g.p[k] = add2(g.p[k], v.p[k]);
+  }
+  if (a.dres) put_run(a.dres, row * a.lddres + c, pack<T>(g));
+  drop_run(a.d, (uint64_t)row * a.cols + c, g);
+  put_run(a.dx, row * a.lddx + c, pack<T>(g));
+}
+
+template <int U>
+__device__ __forceinline__ float at(const Vec<U>& v, int k) {
+  if constexpr (U == 1)
+    return v.p[0];
+  else
+    return k & 1 ? v.p[k / 2].y : v.p[k / 2].x;
+}
+
+// A block walks the rows with a stride and sums its columns' weight gradients,
+// in registers or (SMEM: rows of 1024 threads, which leave no registers) in
+// shared memory at places of the thread's own; each block writes one part at
+// its end.
+//
+// 16-byte runs (U > 1) come through shared memory by asynchronous copies of
+// kDepth rows ahead; a thread copies and reads its own runs alone, so that no
+// thread waits for another's, and the registers are left to the sums.
+template <int U, bool SMEM>
+constexpr int kDepth = U > 1 && !SMEM ? 2 : 0;
+
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(smem)),
+               "l"(global)
+               : "memory");
+}
+
+template <class T, int U, int TPR, int N, bool SMEM>
+__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_of(TPR))
+    norm_bwd_kernel(const __grid_constant__ NormBwd a) {
+  constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR, D = kDepth<U, SMEM>;
+  extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums; else the rows ahead
+  __shared__ __align__(16) float2 red[2][kBlock / 32];
+  __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const float inv = 1.f / (float)a.cols;
+  using E = typename Vec<U>::E;
+  constexpr int P = Vec<U>::P;
+  Vec<U> dw[SMEM ? 1 : N], db[SMEM ? 1 : N];
+  // (SMEM: run n of thread t at element (n * TPR + t) * U of each half)
+  E* sums = reinterpret_cast<E*>(dyn);
+  constexpr int kHalf = N * TPR * P;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if constexpr (SMEM)
+        sums[(n * TPR + t) * P + k] = sums[kHalf + (n * TPR + t) * P + k] = all_of<E>(0.f);
+      else
+        dw[n].p[k] = db[n].p[k] = all_of<E>(0.f);
+    }
+  // rows ahead: [slot][array][run][thread]
+  Run<T, U>* ahead = reinterpret_cast<Run<T, U>*>(dyn) + threadIdx.x;
+  auto slot_of = [&](int slot, int array, int n) {
+    return ahead + ((slot * 3 + array) * N + n) * kBlock;
+  };
+  auto fetch = [&](int slot, int64_t row) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * TPR + t) * U;
+        if (c < a.cols) {
+          copy16(slot_of(slot, 0, n), (const T*)a.dy + row * a.lddy + c);
+          copy16(slot_of(slot, 1, n), (const T*)a.h + row * a.ldh + c);
+          if (a.dh) copy16(slot_of(slot, 2, n), (const T*)a.dh + row * a.lddh + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  const int64_t first = (int64_t)blockIdx.x * RPB + group;
+  if constexpr (D > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, first + d * step);
+  }
+  int turn = 0, slot = 0;
+  float mean = first < a.rows ? a.mean[first] : 0.f, rstd = first < a.rows ? a.rstd[first] : 0.f;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
+    const int64_t row = base + group;
+    const bool live = row < a.rows;
+    if constexpr (D > 0) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    Run<T, U> dy[N], h[N], dh[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        if constexpr (D > 0) {
+          dy[n] = *slot_of(slot, 0, n);
+          h[n] = *slot_of(slot, 1, n);
+        } else {
+          dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c);
+          h[n] = raw_run<T, U>(a.h, row * a.ldh + c);
+          if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c);
+        }
+      }
+    }
+    E s1 = all_of<E>(0.f), s2 = all_of<E>(0.f);
+    Vec<U> hat[N], wdy[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy[n]), x = unpack(h[n]);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          hat[n].p[k] = mul2(add2(x.p[k], all_of<E>(-mean)), all_of<E>(rstd));
+          wdy[n].p[k] = mul2(y.p[k], w.p[k]);
+          s1 = add2(s1, wdy[n].p[k]);
+          s2 = fma2(wdy[n].p[k], hat[n].p[k], s2);
+          if constexpr (SMEM) {
+            E* q = sums + (n * TPR + t) * P + k;
+            q[0] = fma2(y.p[k], hat[n].p[k], q[0]);
+            q[kHalf] = add2(q[kHalf], y.p[k]);
+          } else {
+            dw[n].p[k] = fma2(y.p[k], hat[n].p[k], dw[n].p[k]);
+            db[n].p[k] = add2(db[n].p[k], y.p[k]);
+          }
+        }
+      }
+    }
+    const float rstd0 = rstd;
+    if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
+    const float2 s = row_sum2<TPR, kBlock>(total(s1), total(s2), red[turn]);
+    const float m1 = s.x * inv, m2 = s.y * inv;
+    turn ^= 1;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * TPR + t) * U;
+      if (live && c < a.cols) {
+        if constexpr (D > 0) {
+          if (a.dh) dh[n] = *slot_of(slot, 2, n);
+        }
+        Vec<U> g;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          g.p[k] = add2(wdy[n].p[k], all_of<E>(-m1));
+          g.p[k] = mul2(fma2(hat[n].p[k], all_of<E>(-m2), g.p[k]), all_of<E>(rstd0));
+        }
+        write_grad(a, row, c, g, dh[n]);
+      }
+    }
+    if constexpr (D > 0) {
+      fetch(slot, row + D * step);
+      slot = slot + 1 == D ? 0 : slot + 1;
+    }
+  }
+  // this block's part of the weight gradient: the groups' sums in order
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          join[group][(n * TPR + t) * U + k] = at<U>(which ? db[n] : dw[n], k);
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += kBlock) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < RPB; ++g) sum += join[g][c];
+        part[which * a.cols + c] = sum;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * TPR + t) * U;
+        if (c < a.cols) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            if constexpr (SMEM)
+              part[which * a.cols + c + k] = dyn[which * N * TPR * U + c + k];
+            else
+              part[which * a.cols + c + k] = at<U>(which ? db[n] : dw[n], k);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Rows too wide for the registers: the rows' gradients (two passes over a
+// row) and the columns' partial sums in kernels of their own.
+template <class T>
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_constant__ NormBwd a) {
+  __shared__ __align__(16) float2 red[2][32];
+  const float inv = 1.f / (float)a.cols;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* h = (const T*)a.h + row * a.ldh;
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      const float wdy = to_f32(dy[c]) * load_weight<T, 1>(a.w, a.w32, c).p[0];
+      s1 += wdy;
+      s2 += wdy * ((to_f32(h[c]) - mean) * rstd);
+    }
+    const float2 s = row_sum2<1024, 1024>(s1, s2, red[turn]);
+    s1 = s.x * inv, s2 = s.y * inv;
+    turn ^= 1;
+    for (int c = threadIdx.x; c < a.cols; c += 1024) {
+      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
+      const float hat = (to_f32(h[c]) - mean) * rstd;
+      Vec<1> g = {{rstd * (to_f32(dy[c]) * w - s1 - hat * s2)}};
+      Run<T, 1> d;
+      if (a.dh) d = raw_run<T, 1>(a.dh, row * a.lddh + c);
+      write_grad(a, row, c, g, d);
+    }
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const __grid_constant__ NormBwd a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  float dw = 0.f, db = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float dy = to_f32(((const T*)a.dy)[row * a.lddy + c]);
+    dw += dy * ((to_f32(((const T*)a.h)[row * a.ldh + c]) - a.mean[row]) * a.rstd[row]);
+    db += dy;
+  }
+  float* part = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+  part[c] = dw;
+  part[a.cols + c] = db;
+}
+
+// dweight and dbias: the parts' sums.  32 columns by 32 strided shares of the
+// parts per block, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int parts, int cols,
+                                                         float* dweight, float* dbias) {
+  __shared__ float share[32][33];
+  wait_for_prior();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane, width = 2ll * cols;
+  float sum = 0.f;
+  if (i < width)
+    for (int p = warp; p < parts; p += 32) sum += part[(int64_t)p * width + i];
+  share[warp][lane] = sum;
+  __syncthreads();
+  sum = warp_sum(share[lane][warp]);  // column `warp` of this block
+  const int64_t j = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && j < width) {
+    if (j < cols)
+      dweight[j] = sum;
+    else if (dbias)
+      dbias[j - cols] = sum;
+  }
+}
+
+// A thread's share of a row: two 16-byte runs (it keeps two sums for each
+// element), or 8 elements one by one where the rows are not 16-byte aligned.
+template <int U>
+constexpr int kRuns = U > 1 ? 2 : 8;
+
+template <class T, int U, int TPR, bool SMEM>
+int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
+  constexpr int N = kRuns<U>, block = block_of(TPR), rpb = block / TPR;
+  constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : kDepth<U, SMEM> * 3 * N * block * 16;
+  auto k = norm_bwd_kernel<T, U, TPR, N, SMEM>;
+  if constexpr (smem > 0) {
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (attr != cudaSuccess) return ROT_ECUDA;
+  }
+  const int per_sm = TPR == 1024 ? 1 : 512 / block;
+  *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
+                                  std::min(kMaxParts, per_sm * sm_count()));
+  k<<<*parts, block, smem, s>>>(a);
+  return launched();
+}
+
+template <class T, int U>
+int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
+  switch (row_threads(a.cols, U * kRuns<U>)) {
+    case 32: return launch_bwd_rows<T, U, 32, false>(a, parts, s);
+    case 128: return launch_bwd_rows<T, U, 128, false>(a, parts, s);
+    case 256: return launch_bwd_rows<T, U, 256, false>(a, parts, s);
+    case 512: return launch_bwd_rows<T, U, 512, false>(a, parts, s);
+    case 1024: return launch_bwd_rows<T, U, 1024, true>(a, parts, s);
+  }
+  norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
+  const int e = launched();
+  if (e != ROT_OK) return e;
+  *parts = (int)std::min<int64_t>(a.rows, 64);
+  ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
+  norm_bwd_cols_kernel<T><<<dim3((a.cols + 255) / 256, *parts), 256, 0, s>>>(a);
+  return launched();
+}
+
+template <class T>
+int run(const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
+  constexpr int U = 16 / sizeof(T);
+  int parts = 0, e = ROT_OK;
+  {
+    ProfScope prof(ROT_PROF_ELEMENTWISE,
+                   (double)a.rows * a.cols * sizeof(T) *
+                       (3 + (a.dh != nullptr) + (a.dres != nullptr)), s);
+    const bool vec = a.cols % U == 0 && rows16(a.dy, a.lddy, sizeof(T)) &&
+                     rows16(a.h, a.ldh, sizeof(T)) && rows16(a.dh, a.lddh, sizeof(T)) &&
+                     rows16(a.dres, a.lddres, sizeof(T)) && rows16(a.dx, a.lddx, sizeof(T)) &&
+                     aligned16(a.w);
+    e = vec ? launch_bwd<T, U>(a, &parts, s) : launch_bwd<T, 1>(a, &parts, s);
+  }
+  if (e != ROT_OK) return e;
+  ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
+  return launch_behind(norm_join_kernel, (2 * a.cols + 31) / 32, 1024, 0, s, a.part, parts, a.cols,
+                       dweight, dbias);
+}
+
+}  // namespace
+
+int norm_backward(int32_t type, const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
+  if (type == ROT_TYPE_F32) return run<float>(a, dweight, dbias, s);
+  if (type == ROT_TYPE_F16) return run<__half>(a, dweight, dbias, s);
+  return run<__nv_bfloat16>(a, dweight, dbias, s);
+}
+
+}  // namespace ops
+}  // namespace rot
