@@ -21,7 +21,7 @@ __device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c,
     for (int k = 0; k < Vec<U>::P; ++k) g.p[k] = add2(g.p[k], v.p[k]);
   }
   if (a.dres) put_run(a.dres, row * a.lddres + c, pack<T>(g));
-  drop_run(a.d, (uint64_t)row * a.cols + c, g);
+  if (a.d.on) drop_run(a.d, (uint64_t)row * a.cols + c, g);
   put_run(a.dx, row * a.lddx + c, pack<T>(g));
 }
 
@@ -51,7 +51,7 @@ __device__ __forceinline__ void copy16(void* smem, const void* global) {
                : "memory");
 }
 
-template <class T, int U, int TPR, int N, bool SMEM>
+template <class T, int U, int TPR, int N, bool SMEM, bool DROP>
 __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_of(TPR))
     norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR, D = kDepth<U, SMEM>;
@@ -75,6 +75,16 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
       else
         dw[n].p[k] = db[n].p[k] = all_of<E>(0.f);
     }
+  // (past the row's end a thread takes its first element again, with a
+  // gradient of 0, and stores nothing)
+  int c[N];
+  bool in[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    c[n] = (n * TPR + t) * U;
+    in[n] = c[n] < a.cols;
+    if (!in[n]) c[n] = 0;
+  }
   // rows ahead: [slot][array][run][thread]
   Run<T, U>* ahead = reinterpret_cast<Run<T, U>*>(dyn) + threadIdx.x;
   auto slot_of = [&](int slot, int array, int n) {
@@ -84,12 +94,9 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
     if (row < a.rows) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int c = (n * TPR + t) * U;
-        if (c < a.cols) {
-          copy16(slot_of(slot, 0, n), (const T*)a.dy + row * a.lddy + c);
-          copy16(slot_of(slot, 1, n), (const T*)a.h + row * a.ldh + c);
-          if (a.dh) copy16(slot_of(slot, 2, n), (const T*)a.dh + row * a.lddh + c);
-        }
+        copy16(slot_of(slot, 0, n), (const T*)a.dy + row * a.lddy + c[n]);
+        copy16(slot_of(slot, 1, n), (const T*)a.h + row * a.ldh + c[n]);
+        if (a.dh) copy16(slot_of(slot, 2, n), (const T*)a.dh + row * a.lddh + c[n]);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -106,30 +113,29 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
     const int64_t row = base + group;
     const bool live = row < a.rows;
     if constexpr (D > 0) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    Run<T, U> dy[N], h[N], dh[N];
+    Run<T, U> dh[N];
+    Vec<U> hat[N], wdy[N];
+    E s1 = all_of<E>(0.f), s2 = all_of<E>(0.f);
+    if (live) {  // (the same for the row's threads)
+      Run<T, U> dy[N], h[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (live && c < a.cols) {
+      for (int n = 0; n < N; ++n) {
         if constexpr (D > 0) {
           dy[n] = *slot_of(slot, 0, n);
           h[n] = *slot_of(slot, 1, n);
         } else {
-          dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c);
-          h[n] = raw_run<T, U>(a.h, row * a.ldh + c);
-          if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c);
+          dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c[n]);
+          h[n] = raw_run<T, U>(a.h, row * a.ldh + c[n]);
+          if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c[n]);
         }
       }
-    }
-    E s1 = all_of<E>(0.f), s2 = all_of<E>(0.f);
-    Vec<U> hat[N], wdy[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (live && c < a.cols) {
-        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c), y = unpack(dy[n]), x = unpack(h[n]);
+      for (int n = 0; n < N; ++n) {
+        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c[n]), x = unpack(h[n]);
+        Vec<U> y = unpack(dy[n]);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
+          if (!in[n]) y.p[k] = all_of<E>(0.f);
           hat[n].p[k] = mul2(add2(x.p[k], all_of<E>(-mean)), all_of<E>(rstd));
           wdy[n].p[k] = mul2(y.p[k], w.p[k]);
           s1 = add2(s1, wdy[n].p[k]);
@@ -150,21 +156,36 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
     const float2 s = row_sum2<TPR, kBlock>(total(s1), total(s2), red[turn]);
     const float m1 = s.x * inv, m2 = s.y * inv;
     turn ^= 1;
+    if (live) {
+      Vec<U> g[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * TPR + t) * U;
-      if (live && c < a.cols) {
-        if constexpr (D > 0) {
-          if (a.dh) dh[n] = *slot_of(slot, 2, n);
-        }
-        Vec<U> g;
+      for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          g.p[k] = add2(wdy[n].p[k], all_of<E>(-m1));
-          g.p[k] = mul2(fma2(hat[n].p[k], all_of<E>(-m2), g.p[k]), all_of<E>(rstd0));
+          g[n].p[k] = add2(wdy[n].p[k], all_of<E>(-m1));
+          g[n].p[k] = mul2(fma2(hat[n].p[k], all_of<E>(-m2), g[n].p[k]), all_of<E>(rstd0));
         }
-        write_grad(a, row, c, g, dh[n]);
+      if (a.dh) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          if constexpr (D > 0) dh[n] = *slot_of(slot, 2, n);
+          const Vec<U> v = unpack(dh[n]);
+#pragma unroll
+          for (int k = 0; k < P; ++k) g[n].p[k] = add2(g[n].p[k], v.p[k]);
+        }
       }
+      if (a.dres) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (in[n]) put_run(a.dres, row * a.lddres + c[n], pack<T>(g[n]));
+      }
+      if (DROP) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) drop_run(a.d, (uint64_t)row * a.cols + c[n], g[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (in[n]) put_run(a.dx, row * a.lddx + c[n], pack<T>(g[n]));
     }
     if constexpr (D > 0) {
       fetch(slot, row + D * step);
@@ -281,11 +302,11 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int 
 template <int U>
 constexpr int kRuns = U > 1 ? 2 : 8;
 
-template <class T, int U, int TPR, bool SMEM>
+template <class T, int U, int TPR, bool SMEM, bool DROP>
 int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
   constexpr int N = kRuns<U>, block = block_of(TPR), rpb = block / TPR;
   constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : kDepth<U, SMEM> * 3 * N * block * 16;
-  auto k = norm_bwd_kernel<T, U, TPR, N, SMEM>;
+  auto k = norm_bwd_kernel<T, U, TPR, N, SMEM, DROP>;
   if constexpr (smem > 0) {
     static const cudaError_t attr =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -298,14 +319,14 @@ int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
   return launched();
 }
 
-template <class T, int U>
+template <class T, int U, bool DROP>
 int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
   switch (row_threads(a.cols, U * kRuns<U>)) {
-    case 32: return launch_bwd_rows<T, U, 32, false>(a, parts, s);
-    case 128: return launch_bwd_rows<T, U, 128, false>(a, parts, s);
-    case 256: return launch_bwd_rows<T, U, 256, false>(a, parts, s);
-    case 512: return launch_bwd_rows<T, U, 512, false>(a, parts, s);
-    case 1024: return launch_bwd_rows<T, U, 1024, true>(a, parts, s);
+    case 32: return launch_bwd_rows<T, U, 32, false, DROP>(a, parts, s);
+    case 128: return launch_bwd_rows<T, U, 128, false, DROP>(a, parts, s);
+    case 256: return launch_bwd_rows<T, U, 256, false, DROP>(a, parts, s);
+    case 512: return launch_bwd_rows<T, U, 512, false, DROP>(a, parts, s);
+    case 1024: return launch_bwd_rows<T, U, 1024, true, DROP>(a, parts, s);
   }
   norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
   const int e = launched();
@@ -328,7 +349,10 @@ int run(const NormBwd& a, float* dweight, float* dbias, cudaStream_t s) {
                      rows16(a.h, a.ldh, sizeof(T)) && rows16(a.dh, a.lddh, sizeof(T)) &&
                      rows16(a.dres, a.lddres, sizeof(T)) && rows16(a.dx, a.lddx, sizeof(T)) &&
                      aligned16(a.w);
-    e = vec ? launch_bwd<T, U>(a, &parts, s) : launch_bwd<T, 1>(a, &parts, s);
+    if (vec)
+      e = a.d.on ? launch_bwd<T, U, true>(a, &parts, s) : launch_bwd<T, U, false>(a, &parts, s);
+    else
+      e = a.d.on ? launch_bwd<T, 1, true>(a, &parts, s) : launch_bwd<T, 1, false>(a, &parts, s);
   }
   if (e != ROT_OK) return e;
   ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
