@@ -158,7 +158,17 @@ NORM = [  # rows, cols, type, pad, residual, p, weight type, bias
     (40, 12288, BF16, 0, True, 0.1, F32, True),
     (2, 16384, F32, 0, True, 0.1, F32, True),
     (2, 16385, BF16, 3, True, 0.1, F32, True),
-    (1, 65536, F32, 0, False, 0.0, F32, True)]
+    (1, 65536, F32, 0, False, 0.0, F32, True),
+    # either side of the widths where the threads or the runs per row change
+    (9, 256, BF16, 0, True, 0.1, F32, True), (9, 264, F16, 0, False, 0.1, F32, True),
+    (6, 776, BF16, 0, True, 0.0, F32, True), (6, 1024, F16, 8, True, 0.1, F16, True),
+    (6, 1032, BF16, 0, False, 0.0, F32, False), (5, 2056, BF16, 0, True, 0.1, F32, True),
+    (3, 4104, F16, 0, True, 0.1, F32, True), (3, 5000, BF16, 0, False, 0.0, BF16, True),
+    (3, 8193, BF16, 0, True, 0.1, F32, True), (2, 16392, F16, 0, True, 0.1, F32, True),
+    (2, 20480, BF16, 0, True, 0.0, F32, True), (2, 32776, BF16, 0, True, 0.1, F32, True),
+    (5, 128, F32, 0, True, 0.1, F32, True), (5, 516, F32, 4, True, 0.1, F32, True),
+    (5, 1028, F32, 0, False, 0.1, F32, True), (3, 2052, F32, 0, True, 0.0, F32, False),
+    (3, 6000, F32, 0, True, 0.1, F32, True), (2, 12000, F32, 0, True, 0.1, F32, True)]
 
 
 def norm_inputs(rows, cols, dtype, pad, residual, wtype, bias, seed):
@@ -508,7 +518,8 @@ def test_quantize_special_values(fmt, block_rows):
 
 
 PRODUCT = [(1, 1, 1), (1, 6144, 2048), (3, 130, 16), (128, 128, 128), (127, 129, 131), (200, 300, 4096), (64, 2048, 500),
-           (513, 40, 1030), (16, 16, 20000), (1, 128, 70000), (300, 520, 129), (40, 1000, 640)]
+           (513, 40, 1030), (16, 16, 20000), (1, 128, 70000), (300, 520, 129), (40, 1000, 640), (129, 193, 513),
+           (256, 384, 1024), (9, 192, 512), (1000, 385, 4100), (3000, 2000, 130)]
 
 
 def product_bound(a, b, K):
@@ -660,6 +671,101 @@ def test_linear(tokens, inner, outer, dtype):
     twice = dw.clone()
     ops.fp8_linear_backward(dy, x, t, dw=twice, accumulate=True)
     near(twice, 2 * want, 2 * bound + 4 * E * want.abs(), "dw accumulated")
+
+
+# ---------------------------------------------------------------------------
+# large operands, streams, graphs, all together
+# ---------------------------------------------------------------------------
+
+
+def test_layer_norm_past_2_31_elements():
+    """524296 x 4096 in bfloat16: the last rows as by themselves."""
+    rows = (1 << 19) + 8
+    x = torch.zeros(rows, 4096, dtype=BF16, device="cuda")
+    x[-5:] = torch.randn(5, 4096, generator=gen(1), device="cuda").to(BF16)
+    w = torch.randn(4096, generator=gen(2), device="cuda")
+    y, _, mean, rstd = ops.layer_norm(x, w, w)
+    tail = ops.layer_norm(x[-5:], w, w)
+    assert torch.equal(y[-5:], tail[0]) and torch.equal(mean[-5:], tail[2])
+    dx, _, dw, db = ops.layer_norm_backward(x, x, mean, rstd, w)
+    assert torch.equal(dx[-5:], ops.layer_norm_backward(x[-5:], x[-5:], tail[2], tail[3], w)[0])
+    del x, y, dx
+    torch.cuda.empty_cache()
+
+
+def test_quantize_and_product_past_2_31_elements():
+    """70000 x 32768 to 8 bits in both orientations, and a product of 2.4e9 results."""
+    x = torch.zeros(70000, 32768, dtype=BF16, device="cuda")
+    x[-300:] = torch.randn(300, 32768, generator=gen(1), device="cuda").to(BF16)
+    q, t = ops.fp8_quantize(x, transposed=True)
+    first = 70000 // 128 * 128 - 128  # whole blocks of rows
+    qa, ta = ops.fp8_quantize(x[first:], transposed=True)
+    assert torch.equal(q.data[first:].view(torch.uint8), qa.data.view(torch.uint8))
+    assert torch.equal(q.scale[:, first:], qa.scale) and torch.equal(t.scale[first // 128:], ta.scale)
+    assert torch.equal(t.data[:, first:].contiguous().view(torch.uint8), ta.data.contiguous().view(torch.uint8))
+    del x, q, t
+    a = ops.fp8_quantize(torch.randn(40000, 40, generator=gen(2), device="cuda"))[0]
+    b = ops.fp8_quantize(torch.randn(60001, 40, generator=gen(3), device="cuda"))[0]
+    c = ops.fp8_matmul(a, b, dtype=BF16)
+    part = ops.Fp8Matrix(a.data[-130:], a.scale[:, -130:].contiguous(), 1)
+    assert torch.equal(c[-130:], ops.fp8_matmul(part, b, dtype=BF16))
+    del c
+    torch.cuda.empty_cache()
+
+
+def step_of(x, w, q, qt, targets, ones):
+    """A forward and backward pass through one of everything."""
+    y, h, mean, rstd = ops.layer_norm(x, w, w, residual=x, p=0.1, seed=3, offset=4)
+    logits = ops.fp8_linear(y, q)
+    loss, logp, d = ops.policy_loss(logits, targets, -6.0 * ones, ones, ones)
+    dy, dw = ops.fp8_linear_backward(d, y, qt)
+    return (loss, logp, dw, *ops.layer_norm_backward(dy, h, mean, rstd, w, p=0.1, seed=3, offset=4),
+            ops.dropout(x, 0.3, 5, residual=h))
+
+
+@pytest.mark.parametrize("tokens", [1, 6, 300])
+def test_on_another_stream_and_in_a_graph(tokens):
+    """The same bits on the current stream, on another one and replayed from a
+    graph with new inputs in the captured ones' place."""
+    g = gen(tokens)
+    x = torch.randn(tokens, 512, generator=g, device="cuda").to(BF16)
+    w = torch.ones(512, device="cuda")
+    q, qt = ops.fp8_quantize(torch.randn(700, 512, generator=g, device="cuda") * 0.05, block_rows=128, transposed=True)
+    targets = torch.randint(700, (tokens,), generator=g, device="cuda")
+    args = (x, w, q, qt, targets, torch.ones(tokens, device="cuda"))
+    want = step_of(*args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        other = step_of(*args)
+    on = ops.fp8_linear(x, q, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(want, other)) and torch.equal(on, ops.fp8_linear(x, q))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step_of(*args)
+    keep = x.clone()
+    x.copy_(torch.randn(tokens, 512, generator=g, device="cuda").to(BF16))
+    fresh = step_of(*args)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(fresh, captured))
+    x.copy_(keep)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, captured))
+
+
+def test_example_learns():
+    """40 steps of the example's bandit, 32 actions: from chance (1 / 32) to
+    most rewards."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "policy_step.py")
+    spec = importlib.util.spec_from_file_location("policy_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rewards = example.train(steps=40, say=None)
+    assert rewards[0] < 0.1 and sum(rewards[-10:]) / 10 > 0.8
 
 
 # ---------------------------------------------------------------------------
