@@ -1,6 +1,10 @@
 // Layer norm backward (include/rot_ops.h): the rows' gradients, and the weight
 // gradient as partial sums and their join.  Bound by HBM, with dropout nearly
 // as long in the generator's arithmetic.
+//
+// 16383 x 2048 in bfloat16 with the stream's gradient and dropout: 75 us and 4
+// for the join, 4.2 TB/s.  Five blocks per SM instead of four leave too few
+// registers (80 us), as do the generator's keys in shared memory (79 us).
 #include <algorithm>
 
 #include "ops_norm.cuh"

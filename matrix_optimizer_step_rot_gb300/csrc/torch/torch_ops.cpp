@@ -2,9 +2,9 @@
 // outputs and workspaces from torch's allocator, and the call into librot on
 // the current stream.  No arithmetic.
 //
-// A call of a small operator is host time alone: through ctypes and Python
-// checks a layer norm of one token took 21 us, four allocations and a launch
-// among them.
+// A call of a small operator is host time alone: a layer norm of one token
+// takes 11 us here, four allocations and a launch among them, and took 21 with
+// the same checks in Python and the call through ctypes.
 //
 // The library's entry points come as addresses (bind), so that the one library
 // the process has loaded is the one that runs.

@@ -307,6 +307,23 @@ def test_layer_norm_in_three_dimensions_and_twice_the_same():
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+def test_rows_of_more_dimensions_fold_where_they_can():
+    """A slice of the last dimension of a 3-D tensor folds into rows; one of the
+    middle dimension cannot."""
+    full = torch.randn(4, 50, 96, device="cuda")
+    w = torch.randn(64, device="cuda")
+    part = full[:, :, :64]
+    y = ops.layer_norm(part, w)[0]
+    assert y.shape == (4, 50, 64) and torch.equal(y, ops.layer_norm(part.contiguous(), w)[0])
+    assert torch.equal(ops.dropout(part, 0.4, 1), ops.dropout(part.contiguous(), 0.4, 1))
+    one = full[:1, :1, :64].squeeze()  # a single row of one dimension
+    assert torch.equal(ops.layer_norm(one, w)[0], y[0, 0]) and ops.layer_norm(one, w)[2].shape == ()
+    with pytest.raises(ValueError):
+        ops.dropout(full[:, :40], 0.4, 1)
+    with pytest.raises(ValueError):
+        ops.layer_norm(full.transpose(0, 2), torch.ones(4, device="cuda"))
+
+
 # ---------------------------------------------------------------------------
 # policy loss
 # ---------------------------------------------------------------------------
