@@ -26,8 +26,9 @@ struct Quant {
 };
 
 // Two values as 8-bit floats, the first in the low byte.
-__device__ __forceinline__ uint32_t pair_f8(float x, float y, bool e5m2) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+template <bool E5>
+__device__ __forceinline__ uint32_t pair_f8(float x, float y) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, E5 ? __NV_E5M2 : __NV_E4M3);
 }
 
 // Element k of values as loaded: 16-bit ones two to a word (even k in the low
@@ -81,17 +82,17 @@ __device__ __forceinline__ void load_words(const T* p, int64_t n, uint32_t* w) {
     }
 }
 // Four values under a scale as 8-bit floats.  The conversion saturates
-// infinities; where `odd` they become NaN by hand, as NaN stays.
-__device__ __forceinline__ uint32_t four_f8(float f0, float f1, float f2, float f3, float s,
-                                            bool odd, bool e5m2) {
+// infinities; with FIX they become NaN by hand, as NaN stays.
+template <bool E5, bool FIX>
+__device__ __forceinline__ uint32_t four_f8(float f0, float f1, float f2, float f3, float s) {
   float2 lo = mul2(make_float2(f0, f1), both(s)), hi = mul2(make_float2(f2, f3), both(s));
-  if (odd) {
+  if (FIX) {
     if (!(fabsf(f0) < INFINITY)) lo.x = NAN;
     if (!(fabsf(f1) < INFINITY)) lo.y = NAN;
     if (!(fabsf(f2) < INFINITY)) hi.x = NAN;
     if (!(fabsf(f3) < INFINITY)) hi.y = NAN;
   }
-  return pair_f8(lo.x, lo.y, e5m2) | pair_f8(hi.x, hi.y, e5m2) << 16;
+  return pair_f8<E5>(lo.x, lo.y) | pair_f8<E5>(hi.x, hi.y) << 16;
 }
 
 // |x| as an ordered whole number of the type's bits, and back as a float.
@@ -111,8 +112,8 @@ constexpr int kPitch = 144;  // bytes between the staged rows of the transposed 
 
 // Rows alone, one scale for each row and 128 columns: HBM bound, nothing to
 // exchange but the maxima of eight threads, which hold 16 elements of a block
-// each.  8192 x 4096 in bfloat16: 20 us, 5.0 TB/s.
-template <class T, bool VEC>
+// each.  8192 x 4096 in bfloat16: 19 us, 5.2 TB/s.
+template <class T, bool VEC, bool E5>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ Quant a) {
   const uint32_t blocks = (uint32_t)((a.cols + 127) / 128), total = (uint32_t)a.rows * blocks;
   const int v = threadIdx.x % 8;
@@ -138,14 +139,21 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (b >= total) continue;
-    const int e = scale_byte(magnitude<T>(most), a.e5m2);
+    const int e = scale_byte(magnitude<T>(most), E5);
     const float inv = inverse_scale(e);
     if (v == 0) a.s[j * a.lds + row] = (uint8_t)e;
     uint32_t w[4];
+    auto convert = [&](auto fix) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = four_f8(element<T>(x, 4 * i), element<T>(x, 4 * i + 1), element<T>(x, 4 * i + 2),
-                     element<T>(x, 4 * i + 3), inv, odd, a.e5m2);
+      for (int i = 0; i < 4; ++i)
+        w[i] = four_f8<E5, decltype(fix)::value>(element<T>(x, 4 * i), element<T>(x, 4 * i + 1),
+                                                 element<T>(x, 4 * i + 2), element<T>(x, 4 * i + 3),
+                                                 inv);
+    };
+    if (odd)
+      convert(std::true_type());
+    else
+      convert(std::false_type());
     uint8_t* o = a.q + row * a.ldq + c;
     if (c + 16 <= a.cols && a.wide) {
       *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -158,14 +166,14 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
 }
 
 // HBM bound (one read of x, one or two bytes written per element); 4099 x 6144
-// in both orientations: 28 us, 3.6 TB/s, half of it instructions.  A 128 x
+// in both orientations: 21 us, 4.8 TB/s.  A 128 x
 // 128 tile per CTA, 256 threads: thread (g = t / 16, v = t % 16) holds rows
 // 8 g .. 8 g + 7 of columns 8 v .. 8 v + 7, so both orientations' runs of
 // eight are in one thread.  Maxima are taken on the bits of |x|; a row's 16
 // threads join by shuffles, a column's through shared memory.  The rows go
 // out as 8 bytes per thread (128 per row), the transposed tile through shared
 // memory as 16.
-template <class T, bool VEC>
+template <class T, bool VEC, bool E5>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
     quantize_kernel(const __grid_constant__ Quant a) {
   __shared__ __align__(16) uint32_t colmax[16][kQ];
@@ -218,28 +226,42 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
         }
     }
   }
+  // a whole tile, every access wide
+  const bool whole = a.wide && r0 + kQ <= a.rows && c0 + kQ <= a.cols;
   auto put_rows = [&](const float (&ri)[8]) {
-    const bool run8 = (a.ldq % 8 == 0) && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (r + i >= a.rows) continue;
-      uint32_t o[2];
+    auto convert = [&](int i, uint32_t (&o)[2], auto fix) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = 4 * h;
-        o[h] = four_f8(element<T>(x[i], k), element<T>(x[i], k + 1), element<T>(x[i], k + 2),
-                       element<T>(x[i], k + 3), ri[i], odd, a.e5m2);
+        o[h] = four_f8<E5, decltype(fix)::value>(element<T>(x[i], k), element<T>(x[i], k + 1),
+                                                 element<T>(x[i], k + 2), element<T>(x[i], k + 3),
+                                                 ri[i]);
       }
-      uint8_t* p = a.q + (r + i) * a.ldq + c;
-      if (run8 && c + 8 <= a.cols) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols) p[k] = (uint8_t)(o[k / 4] >> (8 * (k & 3)));
-      }
-    }
     };
+    uint8_t* p = a.q + r * a.ldq + c;
+    if (whole && !odd) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i, p += a.ldq) {
+        uint32_t o[2];
+        convert(i, o, std::false_type());
+        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i, p += a.ldq) {
+      if (r + i >= a.rows) continue;
+      uint32_t o[2];
+      convert(i, o, std::true_type());
+      if (a.wide && c + 8 <= a.cols) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+        continue;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < a.cols) p[k] = (uint8_t)(o[k / 4] >> (8 * (k & 3)));
+    }
+  };
   float ri[8], ci[8];  // inverse scales of this thread's rows and columns
   if (a.square) {
     uint32_t m = 0u;
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
     m = wide[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = max(m, wide[i]);
-    const int b = scale_byte(magnitude<T>(m), a.e5m2);
+    const int b = scale_byte(magnitude<T>(m), E5);
 #pragma unroll
     for (int i = 0; i < 8; ++i) ri[i] = ci[i] = inverse_scale(b);
     if (threadIdx.x == 0) {
@@ -269,21 +291,37 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
         uint32_t m = colmax[0][threadIdx.x];
 #pragma unroll
         for (int i = 1; i < 16; ++i) m = max(m, colmax[i][threadIdx.x]);
-        const int b = scale_byte(magnitude<T>(m), a.e5m2);
+        const int b = scale_byte(magnitude<T>(m), E5);
         colscale[threadIdx.x] = (uint8_t)b;
         if (c0 + threadIdx.x < a.cols) a.st[tr * a.ldst + c0 + threadIdx.x] = (uint8_t)b;
       }
     }
     if (a.q) {
+      // the largest of each row over its 16 threads, two rows to a word where
+      // they fit; thread v works out row v's scale for all of them
+      uint32_t mine = 0u;
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t m = rm[i];
+        for (int i = 0; i < 8; ++i) {
+          uint32_t m = rm[i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int b = scale_byte(magnitude<T>(m), a.e5m2);
-        ri[i] = inverse_scale(b);
-        if (v == i && r + i < a.rows) a.s[tc * a.lds + r + i] = (uint8_t)b;
+          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (v == i) mine = m;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t m = rm[2 * i] | rm[2 * i + 1] << 16;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (v / 2 == i) mine = v & 1 ? m >> 16 : m & 0xFFFFu;
+        }
       }
+      const int b = scale_byte(magnitude<T>(mine), E5);
+      if (v < 8 && r + v < a.rows) a.s[tc * a.lds + r + v] = (uint8_t)b;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        ri[i] = inverse_scale(__shfl_sync(0xffffffffu, b, (threadIdx.x & 16) + i));
       put_rows(ri);
     }
     if (a.qt) {
@@ -297,17 +335,24 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
   if (a.qt) {
     // column 8 v + k is staged as row 16 k + v, so that a warp's writes spread
     // over the banks
+    auto stage = [&](auto fix) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t o[2];
+      for (int k = 0; k < 8; ++k) {
+        uint32_t o[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = 4 * h;
-        o[h] = four_f8(element<T>(x[i], k), element<T>(x[i + 1], k), element<T>(x[i + 2], k),
-                       element<T>(x[i + 3], k), ci[k], odd, a.e5m2);
+        for (int h = 0; h < 2; ++h) {
+          const int i = 4 * h;
+          o[h] = four_f8<E5, decltype(fix)::value>(element<T>(x[i], k), element<T>(x[i + 1], k),
+                                                   element<T>(x[i + 2], k),
+                                                   element<T>(x[i + 3], k), ci[k]);
+        }
+        *reinterpret_cast<uint2*>(&tile[(16 * k + v) * kPitch + 8 * g]) = make_uint2(o[0], o[1]);
       }
-      *reinterpret_cast<uint2*>(&tile[(16 * k + v) * kPitch + 8 * g]) = make_uint2(o[0], o[1]);
-    }
+    };
+    if (odd)
+      stage(std::true_type());
+    else
+      stage(std::false_type());
     __syncthreads();
     const bool run16 = rows16(a.qt, a.ldqt, 1);
     const int64_t rr = r0 + 16 * (threadIdx.x % 8);
@@ -340,11 +385,13 @@ int launch_quantize(const Quant& a, cudaStream_t s) {
   if (!a.qt && !a.square && row_blocks < (1ll << 30)) {
     const int64_t most = (row_blocks + 31) / 32;
     const unsigned ctas = (unsigned)std::min<int64_t>(most, 16ll * sm_count());
-    auto k = vec ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>;
+    auto k = a.e5m2 ? (vec ? quantize_rows_kernel<T, true, true> : quantize_rows_kernel<T, false, true>)
+                    : (vec ? quantize_rows_kernel<T, true, false> : quantize_rows_kernel<T, false, false>);
     k<<<ctas, 256, 0, s>>>(a);
     return launched();
   }
-  auto k = vec ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+  auto k = a.e5m2 ? (vec ? quantize_kernel<T, true, true> : quantize_kernel<T, false, true>)
+                  : (vec ? quantize_kernel<T, true, false> : quantize_kernel<T, false, false>);
   k<<<grid, 256, 0, s>>>(a);
   return launched();
 }
