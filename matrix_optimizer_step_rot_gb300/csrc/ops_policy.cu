@@ -122,7 +122,7 @@ __device__ __forceinline__ int edge_of(const Share& s, int vocab, int rank, int 
   const int t = threadIdx.x;
   if (rank == 0 && t < s.head) return t;
   const int tail = s.head + s.runs * U;
-  if (rank == ranks - 1 && t >= 32 && t - 32 < vocab - tail) return tail + t - 32;
+  if (rank == ranks - 1 && t >= 16 && t - 16 < vocab - tail) return tail + t - 16;
   return -1;
 }
 
@@ -149,9 +149,9 @@ __device__ __forceinline__ float log_prob(float x, float o, float s, float& rest
 
 // The token's term and the slope d(loss)/d(logp), from its log-probability
 // logp + rest.
-__device__ __forceinline__ void term_of(const Policy& a, int64_t t, float w, float logp,
-                                        float rest, float& term, float& slope) {
-  const float adv = a.adv[t], ratio = expf((logp - a.old[t]) + rest);
+__device__ __forceinline__ void term_of(const Policy& a, float w, float adv, float old, float ref,
+                                        float logp, float rest, float& term, float& slope) {
+  const float ratio = expf((logp - old) + rest);
   // (comparisons, not fminf and fmaxf: NaN has to stay)
   const float lo = 1.f - a.lo, hi = 1.f + a.hi;
   const float clipped = ratio < lo ? lo : ratio > hi ? hi : ratio;
@@ -161,7 +161,7 @@ __device__ __forceinline__ void term_of(const Policy& a, int64_t t, float w, flo
   float v = -(plain != plain || through ? plain : bounded);
   float g = plain != plain || through ? -plain : 0.f;
   if (a.ref) {
-    const float r = (a.ref[t] - logp) - rest, em = expm1f(r);
+    const float r = (ref - logp) - rest, em = expm1f(r);
     v += a.kl * (em - r);
     g -= a.kl * em;
   }
@@ -192,11 +192,13 @@ __device__ __forceinline__ ScaledSum join_row(ScaledSum t, ScaledSum* red, Scale
   constexpr int W = kRow / 32;
   const int lane = threadIdx.x & 31;
   t = join_warp(t);
-  __syncthreads();  // (red may still be read from a call before)
-  if (lane == 0) red[threadIdx.x >> 5] = t;
-  __syncthreads();
-  const ScaledSum none = {-INFINITY, 0.f};
-  t = join_warp(lane < W ? red[lane] : none);
+  if constexpr (W > 1) {
+    __syncthreads();  // (red may still be read from a call before)
+    if (lane == 0) red[threadIdx.x >> 5] = t;
+    __syncthreads();
+    const ScaledSum none = {-INFINITY, 0.f};
+    t = join_warp(lane < W ? red[lane] : none);
+  }
   if (ranks > 1) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     if (threadIdx.x == 0) *mine = t;
@@ -261,6 +263,8 @@ __global__ void __launch_bounds__(kRow, 1024 / kRow)
   const bool valid = target >= 0 && target < a.vocab;
   // (read before anything is written: the gradient may take the logits' place)
   const float zt = valid ? to_f32(z[target]) : NAN;
+  const float adv = a.loss ? a.adv[t] : 0.f, old = a.loss ? a.old[t] : 0.f;
+  const float ref = a.ref ? a.ref[t] : 0.f;
   ScaledSum sum = {-INFINITY, 0.f};
   int i0 = sh.v0 + threadIdx.x;
   for (; i0 + (kAhead - 1) * kRow < sh.v1; i0 += kAhead * kRow) {
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kRow, 1024 / kRow)
   // every thread: the same numbers from the same inputs
   float rest, term = 0.f, slope = 0.f;
   const float logp = log_prob(zt - m, sum.o, sum.s, rest);
-  if (a.loss) term_of(a, t, w, logp, rest, term, slope);
+  if (a.loss) term_of(a, w, adv, old, ref, logp, rest, term, slope);
   if (threadIdx.x == 0 && rank == 0) {
     a.logp[t] = logp;
     if (a.loss) a.terms[t] = term;
@@ -336,13 +340,34 @@ __global__ void __launch_bounds__(kRow, 1024 / kRow)
   for (; i1 >= sh.v0; i1 -= kRow) grad_run(i1, last_read(runs + i1));
 }
 
-// loss = sum of the terms, always in the same order.
+// loss = sum of the terms, always in the same order.  A thread adds 16 terms
+// at a time as a float32 and the rounding errors of its sums (Knuth's exact
+// sum of two), and only such results in double: 16384 terms in 6 us, and in
+// 13 with each addition in double, of which an SM makes few.
 __global__ void __launch_bounds__(1024) policy_sum_kernel(const float* terms, int64_t tokens,
                                                           float* loss) {
   __shared__ double red[32];
   wait_for_prior();
   double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < tokens; i += 1024) sum += terms[i];
+  for (int64_t i0 = threadIdx.x; i0 < tokens; i0 += 16 * 1024) {
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = i0 + k * 1024 < tokens ? terms[i0 + k * 1024] : 0.f;
+    float s = v[0], rest = 0.f;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) {
+      const float t = __fadd_rn(s, v[k]), b = __fsub_rn(t, s);
+      rest += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(v[k], b));
+      s = t;
+    }
+    // (a sum beyond float32's range has no errors to speak of: term by term)
+    if (fabsf(s) < INFINITY) {
+      sum += (double)s + (double)rest;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum += v[k];
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
@@ -396,8 +421,18 @@ int launch_rows(const Policy& a, cudaStream_t s) {
   return ROT_OK;
 }
 
+// Threads of a row: 512 (log-probabilities alone 256), so that few rows share
+// the caches at once; but with rows for more than one round of those, fewer
+// for short rows, whose time is that of a few dependent steps and the more of
+// which an SM then holds.  With the gradient, in us on 32, 128 and 512 threads:
+// 16384 rows of 2 KB 20, 52 and 190, of 8 KB 49, 69 and 212; 8192 of 16 KB 52,
+// 55 and 135; 4096 of 64 KB 106 on 128 and 123 on 512; but 600 of 8 KB 8.4,
+// 6.2 and 10.1.
 template <class T>
 int launch_type(const Policy& a, cudaStream_t s) {
+  const int64_t bytes = (int64_t)a.vocab * sizeof(T);
+  if (bytes <= (8 << 10) && a.tokens > 8 * sm_count()) return launch_rows<T, 32>(a, s);
+  if (bytes <= (64 << 10) && a.tokens > 2 * sm_count()) return launch_rows<T, 128>(a, s);
   return a.d ? launch_rows<T, 512>(a, s) : launch_rows<T, 256>(a, s);
 }
 int launch_policy(const Policy& a, int32_t type, cudaStream_t s) {
