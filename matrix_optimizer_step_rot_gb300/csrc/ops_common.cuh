@@ -285,6 +285,38 @@ __device__ __forceinline__ void drop_run(const Drop& d, uint64_t i0, Vec<U>& f) 
   }
 }
 
+// Dropout of a warp's 32 N consecutive elements from i0, whatever i0 mod 4 is:
+// element n * 32 + lane of this lane is kept where bit n is set.  Each lane
+// takes every 32nd of the N * 8 generator calls (one more where i0 lies within
+// a call) and the others fetch its four answers: N / 4 calls per N elements
+// instead of one each.  The whole warp calls it; only the first `count`
+// answers (or all) are asked for.
+template <int N>
+__device__ __forceinline__ uint32_t keep_bits(const Drop& d, uint64_t i0, int count = 32 * N) {
+  static_assert(N % 4 == 0 && N <= 16, "whole generator calls, at most five answers");
+  const int lane = threadIdx.x & 31;
+  const uint32_t phase = (uint32_t)i0 & 3u;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int r = 0; r < N / 4 + 1; ++r) {
+    if (r == N / 4 && (int)phase + count <= 32 * N) break;
+    const Words w = philox(d, (i0 >> 2) + r * 32 + lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine |= (w.w[k] > d.bar ? 1u : 0u) << (4 * r + k);
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint32_t e = phase + n * 32 + lane;
+    const uint32_t v = __shfl_sync(0xffffffffu, mine, (e >> 2) & 31);
+    bits |= (v >> ((e >> 7) * 4 + (e & 3)) & 1u) << n;
+  }
+  return bits;
+}
+__device__ __forceinline__ float kept(const Drop& d, bool keep, float x) {
+  return keep ? __fmul_rn(x, d.scale) : 0.f;
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);

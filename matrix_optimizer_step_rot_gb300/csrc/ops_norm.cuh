@@ -98,6 +98,7 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
     const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = x;
     row_barrier<TPR, BLOCK>();
+    if constexpr (W == 2) return red[warp & ~1] + red[warp | 1];
     const float4* p = reinterpret_cast<const float4*>(red + warp / W * W);
     float2 sum = both(0.f);
 #pragma unroll
@@ -118,6 +119,83 @@ inline int row_threads(int cols, int share) {
   for (int t : {32, 128, 256, 512, 1024})
     if (cols <= t * share) return t;
   return 0;
+}
+
+// Rows that are not 16-byte aligned go element by element (runs of U = 1): a
+// warp takes 32 N consecutive ones, lane by lane, so that accesses stay
+// together and the warp shares the dropout's generator calls (keep_bits).
+// Shares of a warp are then large: 64 threads per row as well, and for short
+// rows shares of 4.
+constexpr int kSingles = 8, kFewSingles = 4;
+inline int row_threads_single(int cols) {
+  return cols > 32 * kSingles && cols <= 64 * kSingles ? 64 : row_threads(cols, kSingles);
+}
+// First element of run n of a row's thread t.
+template <int U, int TPR, int N>
+__device__ __forceinline__ int column_of(int n, int t) {
+  return U > 1 ? (n * TPR + t) * U : (t / 32 * N + n) * 32 + t % 32;
+}
+// Whether the warp of thread t has elements of the row at all.
+template <int U, int N>
+__device__ __forceinline__ bool has_columns(int t, int cols) {
+  return U > 1 || t / 32 * N * 32 < cols;
+}
+// A thread's runs of the row at element o of p.  Single elements are 32 apart,
+// so that one address serves them all; those past the row's end read as 0.
+template <class T, int U, int N>
+__device__ __forceinline__ void get_runs(Run<T, U> (&r)[N], const void* p, int64_t o,
+                                         const int (&c)[N], const bool (&in)[N]) {
+  if constexpr (U > 1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) r[n] = raw_run<T, U>(p, o + c[n]);
+  } else {
+    const T* q = (const T*)p + o + c[0];
+#pragma unroll
+    for (int n = 0; n < N; ++n) r[n].v[0] = in[n] ? q[32 * n] : from_f32<T>(0.f);
+  }
+}
+template <class T, int U, int N>
+__device__ __forceinline__ void put_runs(void* p, int64_t o, const int (&c)[N],
+                                         const bool (&in)[N], const Vec<U> (&f)[N]) {
+  T* q = (T*)p + o + c[0];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (!in[n]) continue;
+    if constexpr (U > 1)
+      put_run(p, o + c[n], pack<T>(f[n]));
+    else
+      q[32 * n] = from_f32<T>(f[n].p[0]);
+  }
+}
+template <class T, int U, int N>
+__device__ __forceinline__ void get_weights(Vec<U> (&f)[N], const void* w, bool w32,
+                                            const int (&c)[N], const bool (&in)[N]) {
+  if constexpr (U > 1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[n] = load_weight<T, U>(w, w32, c[n]);
+  } else if (w32) {
+    const float* q = (const float*)w + c[0];
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[n].p[0] = in[n] ? q[32 * n] : 0.f;
+  } else {
+    const T* q = (const T*)w + c[0];
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[n].p[0] = in[n] ? to_f32(q[32 * n]) : 0.f;
+  }
+}
+// Dropout of the N runs of a thread of a row.
+template <int U, int N>
+__device__ __forceinline__ void drop_runs(const Drop& d, uint64_t row0, const int (&c)[N],
+                                          int t, int cols, Vec<U> (&f)[N]) {
+  if constexpr (U > 1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) drop_run(d, row0 + c[n], f[n]);
+  } else {
+    const int c0 = t / 32 * N * 32;
+    const uint32_t bits = keep_bits<N>(d, row0 + c0, cols - c0);
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[n].p[0] = kept(d, bits >> n & 1, f[n].p[0]);
+  }
 }
 
 // Partial sums of the weight gradient kept at most (the workspace's size does

@@ -14,21 +14,6 @@ namespace rot {
 namespace ops {
 namespace {
 
-// The gradient of one run, g, written out; dropped into dx.  d: the run of
-// dh, already loaded.
-template <class T, int U>
-__device__ __forceinline__ void write_grad(const NormBwd& a, int64_t row, int c, Vec<U>& g,
-                                           const Run<T, U>& d) {
-  if (a.dh) {
-    const Vec<U> v = unpack(d);
-#pragma unroll
-    for (int k = 0; k < Vec<U>::P; ++k) g.p[k] = add2(g.p[k], v.p[k]);
-  }
-  if (a.dres) put_run(a.dres, row * a.lddres + c, pack<T>(g));
-  if (a.d.on) drop_run(a.d, (uint64_t)row * a.cols + c, g);
-  put_run(a.dx, row * a.lddx + c, pack<T>(g));
-}
-
 template <int U>
 __device__ __forceinline__ float at(const Vec<U>& v, int k) {
   if constexpr (U == 1)
@@ -45,6 +30,10 @@ __device__ __forceinline__ float at(const Vec<U>& v, int k) {
 // 16-byte runs (U > 1) come through shared memory by asynchronous copies of
 // kDepth rows ahead; a thread copies and reads its own runs alone, so that no
 // thread waits for another's, and the registers are left to the sums.
+//
+// Single elements (U = 1) have the next row's and the weights in registers
+// instead: 32768 x 1325 in 249 us; loaded where they are used, 282 us, and 319
+// and 326 us on twice and 1.5 times the threads per SM, which spill.
 template <int U, bool SMEM>
 constexpr int kDepth = U > 1 && !SMEM ? 2 : 0;
 
@@ -55,14 +44,20 @@ __device__ __forceinline__ void copy16(void* smem, const void* global) {
                : "memory");
 }
 
+// Blocks per SM.
+constexpr int per_sm_of(int tpr) { return tpr == 1024 ? 1 : 512 / block_of(tpr); }
+
 template <class T, int U, int TPR, int N, bool SMEM, bool DROP>
-__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_of(TPR))
+__global__ void __launch_bounds__(block_of(TPR), per_sm_of(TPR))
     norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR, D = kDepth<U, SMEM>;
+  // single elements: the next row's, and the weights, in registers
+  constexpr bool kNext = U == 1 && !SMEM;
   extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums; else the rows ahead
   __shared__ __align__(16) float2 red[2][kBlock / 32];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const bool busy = has_columns<U, N>(t, a.cols);  // (the same for a warp)
   const float inv = 1.f / (float)a.cols;
   using E = typename Vec<U>::E;
   constexpr int P = Vec<U>::P;
@@ -85,10 +80,12 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
   bool in[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    c[n] = (n * TPR + t) * U;
+    c[n] = column_of<U, TPR, N>(n, t);
     in[n] = c[n] < a.cols;
-    if (!in[n]) c[n] = 0;
+    if (U > 1 && !in[n]) c[n] = 0;
   }
+  Vec<U> weight[N];
+  if constexpr (kNext) get_weights<T>(weight, a.w, a.w32, c, in);
   // rows ahead: [slot][array][run][thread]
   Run<T, U>* ahead = reinterpret_cast<Run<T, U>*>(dyn) + threadIdx.x;
   auto slot_of = [&](int slot, int array, int n) {
@@ -111,31 +108,41 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch(d, first + d * step);
   }
+  Run<T, U> dy[N], h[N], dh[N];
+  auto load = [&](int64_t row) {
+    if (row >= a.rows || !busy) return;
+    get_runs(dy, a.dy, row * a.lddy, c, in);
+    get_runs(h, a.h, row * a.ldh, c, in);
+    if (a.dh) get_runs(dh, a.dh, row * a.lddh, c, in);
+  };
+  if constexpr (kNext) load(first);
   int turn = 0, slot = 0;
   float mean = first < a.rows ? a.mean[first] : 0.f, rstd = first < a.rows ? a.rstd[first] : 0.f;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
     const int64_t row = base + group;
-    const bool live = row < a.rows;
+    const bool live = row < a.rows && busy;
     if constexpr (D > 0) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    Run<T, U> dh[N];
     Vec<U> hat[N], wdy[N];
     E s1 = all_of<E>(0.f), s2 = all_of<E>(0.f);
-    if (live) {  // (the same for the row's threads)
-      Run<T, U> dy[N], h[N];
+    if (live) {  // (the same for a warp)
+      if constexpr (D > 0) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if constexpr (D > 0) {
+        for (int n = 0; n < N; ++n) {
           dy[n] = *slot_of(slot, 0, n);
           h[n] = *slot_of(slot, 1, n);
-        } else {
-          dy[n] = raw_run<T, U>(a.dy, row * a.lddy + c[n]);
-          h[n] = raw_run<T, U>(a.h, row * a.ldh + c[n]);
-          if (a.dh) dh[n] = raw_run<T, U>(a.dh, row * a.lddh + c[n]);
         }
+      } else if constexpr (!kNext) {
+        load(row);
+        if constexpr (U == 1) get_weights<T>(weight, a.w, a.w32, c, in);
       }
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const Vec<U> w = load_weight<T, U>(a.w, a.w32, c[n]), x = unpack(h[n]);
+        Vec<U> w;
+        if constexpr (U > 1)
+          w = load_weight<T, U>(a.w, a.w32, c[n]);
+        else
+          w = weight[n];
+        const Vec<U> x = unpack(h[n]);
         Vec<U> y = unpack(dy[n]);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
@@ -155,6 +162,12 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
         }
       }
     }
+    Run<T, U> dh0[N];
+    if constexpr (kNext) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) dh0[n] = dh[n];
+      load(row + step);
+    }
     const float rstd0 = rstd;
     if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
     const float2 s = row_sum2<TPR, kBlock>(total(s1), total(s2), red[turn]);
@@ -173,23 +186,14 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           if constexpr (D > 0) dh[n] = *slot_of(slot, 2, n);
-          const Vec<U> v = unpack(dh[n]);
+          const Vec<U> v = unpack(kNext ? dh0[n] : dh[n]);
 #pragma unroll
           for (int k = 0; k < P; ++k) g[n].p[k] = add2(g[n].p[k], v.p[k]);
         }
       }
-      if (a.dres) {
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (in[n]) put_run(a.dres, row * a.lddres + c[n], pack<T>(g[n]));
-      }
-      if (DROP) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) drop_run(a.d, (uint64_t)row * a.cols + c[n], g[n]);
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (in[n]) put_run(a.dx, row * a.lddx + c[n], pack<T>(g[n]));
+      if (a.dres) put_runs<T>(a.dres, row * a.lddres, c, in, g);
+      if (DROP) drop_runs<U, N>(a.d, (uint64_t)row * a.cols, c, t, a.cols, g);
+      put_runs<T>(a.dx, row * a.lddx, c, in, g);
     }
     if constexpr (D > 0) {
       fetch(slot, row + D * step);
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
       for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          join[group][(n * TPR + t) * U + k] = at<U>(which ? db[n] : dw[n], k);
+          join[group][column_of<U, TPR, N>(n, t) + k] = at<U>(which ? db[n] : dw[n], k);
       __syncthreads();
       for (int c = threadIdx.x; c < a.cols; c += kBlock) {
         float sum = 0.f;
@@ -217,12 +221,12 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 512 / block_o
     } else {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int c = (n * TPR + t) * U;
+        const int c = column_of<U, TPR, N>(n, t);
         if (c < a.cols) {
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             if constexpr (SMEM)
-              part[which * a.cols + c + k] = dyn[which * N * TPR * U + c + k];
+              part[which * a.cols + c + k] = dyn[(which * N * TPR + n * TPR + t) * U + k];
             else
               part[which * a.cols + c + k] = at<U>(which ? db[n] : dw[n], k);
           }
@@ -252,13 +256,25 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_consta
     const float2 s = row_sum2<1024, 1024>(s1, s2, red[turn]);
     s1 = s.x * inv, s2 = s.y * inv;
     turn ^= 1;
-    for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
-      const float hat = (to_f32(h[c]) - mean) * rstd;
-      Vec<1> g = {{rstd * (to_f32(dy[c]) * w - s1 - hat * s2)}};
-      Run<T, 1> d;
-      if (a.dh) d = raw_run<T, 1>(a.dh, row * a.lddh + c);
-      write_grad(a, row, c, g, d);
+    // (128 consecutive elements per warp)
+    for (int c0 = threadIdx.x / 32 * 128; c0 < a.cols; c0 += 32 * 128) {
+      const uint32_t bits = a.d.on ? keep_bits<4>(a.d, (uint64_t)row * a.cols + c0) : 0;
+      float g[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = min(c0 + (int)threadIdx.x % 32 + 32 * k, a.cols - 1);
+        const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
+        const float hat = (to_f32(h[c]) - mean) * rstd;
+        g[k] = rstd * (to_f32(dy[c]) * w - s1 - hat * s2);
+        if (a.dh) g[k] = __fadd_rn(g[k], to_f32(((const T*)a.dh)[row * a.lddh + c]));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + threadIdx.x % 32 + 32 * k;
+        if (c >= a.cols) continue;
+        if (a.dres) ((T*)a.dres)[row * a.lddres + c] = from_f32<T>(g[k]);
+        ((T*)a.dx)[row * a.lddx + c] = from_f32<T>(a.d.on ? kept(a.d, bits >> k & 1, g[k]) : g[k]);
+      }
     }
   }
 }
@@ -302,13 +318,13 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int 
 }
 
 // A thread's share of a row: two 16-byte runs (it keeps two sums for each
-// element), or 8 elements one by one where the rows are not 16-byte aligned.
+// element), or single elements where the rows are not 16-byte aligned.
 template <int U>
-constexpr int kRuns = U > 1 ? 2 : 8;
+constexpr int kRuns = U > 1 ? 2 : kSingles;
 
-template <class T, int U, int TPR, bool SMEM, bool DROP>
+template <class T, int U, int TPR, bool SMEM, bool DROP, int N = kRuns<U>>
 int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
-  constexpr int N = kRuns<U>, block = block_of(TPR), rpb = block / TPR;
+  constexpr int block = block_of(TPR), rpb = block / TPR;
   constexpr int smem = SMEM ? 2 * N * U * TPR * 4 : kDepth<U, SMEM> * 3 * N * block * 16;
   auto k = norm_bwd_kernel<T, U, TPR, N, SMEM, DROP>;
   if constexpr (smem > 0) {
@@ -316,7 +332,7 @@ int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return ROT_ECUDA;
   }
-  const int per_sm = TPR == 1024 ? 1 : 512 / block;
+  constexpr int per_sm = per_sm_of(TPR);
   *parts = (int)std::min<int64_t>((a.rows + rpb - 1) / rpb,
                                   std::min(kMaxParts, per_sm * sm_count()));
   k<<<*parts, block, smem, s>>>(a);
@@ -325,8 +341,16 @@ int launch_bwd_rows(const NormBwd& a, int* parts, cudaStream_t s) {
 
 template <class T, int U, bool DROP>
 int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
-  switch (row_threads(a.cols, U * kRuns<U>)) {
-    case 32: return launch_bwd_rows<T, U, 32, false, DROP>(a, parts, s);
+  switch (U > 1 ? row_threads(a.cols, U * kRuns<U>) : row_threads_single(a.cols)) {
+    case 32:
+      if constexpr (U == 1) {
+        if (a.cols <= 32 * kFewSingles)
+          return launch_bwd_rows<T, U, 32, false, DROP, kFewSingles>(a, parts, s);
+      }
+      return launch_bwd_rows<T, U, 32, false, DROP>(a, parts, s);
+    case 64:
+      if constexpr (U == 1) return launch_bwd_rows<T, U, 64, false, DROP>(a, parts, s);
+      break;
     case 128: return launch_bwd_rows<T, U, 128, false, DROP>(a, parts, s);
     case 256: return launch_bwd_rows<T, U, 256, false, DROP>(a, parts, s);
     case 512: return launch_bwd_rows<T, U, 512, false, DROP>(a, parts, s);

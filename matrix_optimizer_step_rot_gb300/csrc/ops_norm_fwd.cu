@@ -20,13 +20,14 @@ namespace {
 // that the runs' arithmetic overlaps: past the row's end a thread takes its
 // first element again, counts it as 0 and stores nothing.
 template <class T, int U, int TPR, int N, bool DROP>
-__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 640 / block_of(TPR))
+__global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : (U > 1 ? 640 : 1024) / block_of(TPR))
     norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR;
   using E = typename Vec<U>::E;
   constexpr int P = Vec<U>::P;
   __shared__ __align__(16) float red[2][kBlock / 32];
   const int t = threadIdx.x % TPR;
+  const bool busy = has_columns<U, N>(t, a.cols);  // (the same for a warp)
   const float inv = 1.f / (float)a.cols;
   const int64_t wanted = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = wanted < a.rows;
@@ -35,82 +36,77 @@ __global__ void __launch_bounds__(block_of(TPR), TPR == 1024 ? 1 : 640 / block_o
   bool in[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    c[n] = (n * TPR + t) * U;
+    c[n] = column_of<U, TPR, N>(n, t);
     in[n] = (U > 1 && n < N - 1) || c[n] < a.cols;
-    if (!in[n]) c[n] = 0;
-  }
-  Run<T, U> x[N], r[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) x[n] = raw_run<T, U>(a.x, row * a.ldx + c[n]);
-  if (a.res) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) r[n] = raw_run<T, U>(a.res, row * a.ldr + c[n]);
+    if (U > 1 && !in[n]) c[n] = 0;
   }
   Vec<U> h[N];
+  E sum = all_of<E>(0.f);
+  if (busy) {
+    Run<T, U> x[N], r[N];
+    get_runs(x, a.x, row * a.ldx, c, in);
+    if (a.res) get_runs(r, a.res, row * a.ldr, c, in);
 #pragma unroll
-  for (int n = 0; n < N; ++n) h[n] = unpack(x[n]);
-  if (DROP) {
+    for (int n = 0; n < N; ++n) h[n] = unpack(x[n]);
+    if (DROP) drop_runs<U, N>(a.d, (uint64_t)row * a.cols, c, t, a.cols, h);
+    if (a.h) {
+      if (a.res) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) drop_run(a.d, (uint64_t)row * a.cols + c[n], h[n]);
-  }
-  if (a.h) {
-    if (a.res) {
+        for (int n = 0; n < N; ++n) {
+          const Vec<U> v = unpack(r[n]);
+#pragma unroll
+          for (int k = 0; k < P; ++k) h[n].p[k] = add2(v.p[k], h[n].p[k]);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const Vec<U> v = unpack(r[n]);
-#pragma unroll
-        for (int k = 0; k < P; ++k) h[n].p[k] = add2(v.p[k], h[n].p[k]);
+        const Run<T, U> stored = pack<T>(h[n]);
+        if (live && in[n])
+          put_run(a.h, row * a.ldh + (U > 1 ? c[n] : c[0] + 32 * n), stored);
+        h[n] = unpack(stored);  // the norm reads what is stored
       }
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const Run<T, U> stored = pack<T>(h[n]);
-      if (live && in[n]) put_run(a.h, row * a.ldh + c[n], stored);
-      h[n] = unpack(stored);  // the norm reads what is stored
-    }
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        if (!in[n]) h[n].p[k] = all_of<E>(0.f);
+        sum = add2(sum, h[n].p[k]);
+      }
   }
-  E sum = all_of<E>(0.f);
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      if (!in[n]) h[n].p[k] = all_of<E>(0.f);
-      sum = add2(sum, h[n].p[k]);
-    }
   const float mean = row_sum<TPR, kBlock>(total(sum), red[0]) * inv;
   E sq = all_of<E>(0.f);
+  if (busy) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const float less = in[n] ? -mean : 0.f;
+    for (int n = 0; n < N; ++n) {
+      const float less = in[n] ? -mean : 0.f;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      h[n].p[k] = add2(h[n].p[k], all_of<E>(less));
-      sq = fma2(h[n].p[k], h[n].p[k], sq);
+      for (int k = 0; k < P; ++k) {
+        h[n].p[k] = add2(h[n].p[k], all_of<E>(less));
+        sq = fma2(h[n].p[k], h[n].p[k], sq);
+      }
     }
   }
   const float rstd = inverse_root(row_sum<TPR, kBlock>(total(sq), red[1]) * inv + a.eps);
-  if (!live) return;
+  if (!live || !busy) return;
   if (t == 0) {
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const Vec<U> w = load_weight<T, U>(a.w, a.w32, c[n]);
-#pragma unroll
-    for (int k = 0; k < P; ++k) h[n].p[k] = mul2(mul2(h[n].p[k], all_of<E>(rstd)), w.p[k]);
-  }
-  if (a.b) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const Vec<U> b = load_weight<T, U>(a.b, a.w32, c[n]);
-#pragma unroll
-      for (int k = 0; k < P; ++k) h[n].p[k] = add2(h[n].p[k], b.p[k]);
-    }
-  }
+  Vec<U> w[N];
+  get_weights<T>(w, a.w, a.w32, c, in);
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    if (in[n]) put_run(a.y, row * a.ldy + c[n], pack<T>(h[n]));
+#pragma unroll
+    for (int k = 0; k < P; ++k) h[n].p[k] = mul2(mul2(h[n].p[k], all_of<E>(rstd)), w[n].p[k]);
+  if (a.b) {
+    get_weights<T>(w, a.b, a.w32, c, in);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int k = 0; k < P; ++k) h[n].p[k] = add2(h[n].p[k], w[n].p[k]);
+  }
+  put_runs<T>(a.y, row * a.ldy, c, in, h);
 }
 
 // Rows too wide for the registers: a block per row, three passes over it (the
@@ -122,67 +118,112 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_consta
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* src = a.h ? (const T*)a.h + row * a.ldh : (const T*)a.x + row * a.ldx;
     float sum = 0.f;
-    for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      Vec<1> f = {{to_f32(((const T*)a.x)[row * a.ldx + c])}};
-      if (a.h) {
-        const float r = a.res ? to_f32(((const T*)a.res)[row * a.ldr + c]) : 0.f;
-        drop_run(a.d, (uint64_t)row * a.cols + c, f);
-        const T v = from_f32<T>(a.res ? __fadd_rn(r, f.p[0]) : f.p[0]);
-        ((T*)a.h)[row * a.ldh + c] = v;
-        f.p[0] = to_f32(v);
+    // (128 consecutive elements per warp; a thread meets its own again below)
+    for (int c0 = threadIdx.x / 32 * 128; c0 < a.cols; c0 += 32 * 128) {
+      const int c = c0 + threadIdx.x % 32;
+      T x[4], r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = c + 32 * k < a.cols;
+        x[k] = in ? ((const T*)a.x)[row * a.ldx + c + 32 * k] : from_f32<T>(0.f);
+        r[k] = in && a.res ? ((const T*)a.res)[row * a.ldr + c + 32 * k] : from_f32<T>(0.f);
       }
-      sum += f.p[0];
+      const uint32_t bits = a.d.on ? keep_bits<4>(a.d, (uint64_t)row * a.cols + c0) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f = to_f32(x[k]);
+        if (a.h) {
+          if (a.d.on) f = kept(a.d, bits >> k & 1, f);
+          const T v = from_f32<T>(a.res ? __fadd_rn(to_f32(r[k]), f) : f);
+          if (c + 32 * k < a.cols) ((T*)a.h)[row * a.ldh + c + 32 * k] = v;
+          f = c + 32 * k < a.cols ? to_f32(v) : 0.f;
+        }
+        sum += f;
+      }
     }
     const float mean = row_sum<1024, 1024>(sum, red[0]) * inv;
     float sq = 0.f;
-    for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float f = to_f32(src[c]) - mean;
-      sq += f * f;
-    }
+    for (int c0 = threadIdx.x / 32 * 128; c0 < a.cols; c0 += 32 * 128)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + threadIdx.x % 32 + 32 * k;
+        const float f = c < a.cols ? to_f32(src[c]) - mean : 0.f;
+        sq += f * f;
+      }
     const float rstd = inverse_root(row_sum<1024, 1024>(sq, red[1]) * inv + a.eps);
     if (threadIdx.x == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
-    for (int c = threadIdx.x; c < a.cols; c += 1024) {
-      const float w = load_weight<T, 1>(a.w, a.w32, c).p[0];
-      const float b = a.b ? load_weight<T, 1>(a.b, a.w32, c).p[0] : 0.f;
-      ((T*)a.y)[row * a.ldy + c] = from_f32<T>((to_f32(src[c]) - mean) * rstd * w + b);
+    for (int c0 = threadIdx.x / 32 * 128; c0 < a.cols; c0 += 32 * 128) {
+      float f[4], w[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = min(c0 + (int)threadIdx.x % 32 + 32 * k, a.cols - 1);
+        // (the last element for those past the end, which store nothing)
+        f[k] = to_f32(src[c]);
+        w[k] = load_weight<T, 1>(a.w, a.w32, c).p[0];
+        b[k] = a.b ? load_weight<T, 1>(a.b, a.w32, c).p[0] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + threadIdx.x % 32 + 32 * k;
+        if (c < a.cols)
+          ((T*)a.y)[row * a.ldy + c] = from_f32<T>((f[k] - mean) * rstd * w[k] + b[k]);
+      }
     }
   }
 }
 
 // A thread's share of a row: up to four 16-byte runs (so that what a thread
-// does once per row weighs little), or 8 elements one by one where the rows
-// are not 16-byte aligned.
-template <int U>
-constexpr int kMostRuns = U > 1 ? 4 : 8;
+// does once per row weighs little), or single elements where the rows are not
+// 16-byte aligned.
+constexpr int kMostRuns = 4;
 
 template <class T, int U, int TPR, int N, bool DROP>
 int launch_runs(const NormFwd& a, unsigned grid, cudaStream_t s) {
   // (at or below a quarter of TPR * 4 runs the next smaller TPR takes the row:
   // those counts need no kernel)
-  constexpr int least = U == 1 ? N : TPR == 32 ? 1 : TPR == 128 ? 2 : 3;
+  constexpr int least = TPR == 32 ? 1 : TPR == 128 ? 2 : 3;
   if constexpr (N > least) {
     if (a.cols <= (N - 1) * TPR * U) return launch_runs<T, U, TPR, N - 1, DROP>(a, grid, s);
   }
   norm_fwd_kernel<T, U, TPR, N, DROP><<<grid, block_of(TPR), 0, s>>>(a);
   return launched();
 }
+template <class T, int TPR, int N, bool DROP>
+int launch_single(const NormFwd& a, unsigned grid, cudaStream_t s) {
+  norm_fwd_kernel<T, 1, TPR, N, DROP><<<grid, block_of(TPR), 0, s>>>(a);
+  return launched();
+}
 
 template <class T, int U, bool DROP>
 int launch_rows(const NormFwd& a, cudaStream_t s) {
-  constexpr int N = kMostRuns<U>;
-  const int tpr = row_threads(a.cols, U * N);
-  const int64_t per = tpr == 32 ? 4 : 1, blocks = (a.rows + per - 1) / per;
+  const int tpr = U > 1 ? row_threads(a.cols, U * kMostRuns) : row_threads_single(a.cols);
+  const int64_t per = tpr == 0 ? 1 : block_of(tpr) / tpr, blocks = (a.rows + per - 1) / per;
   if (blocks > 0x7FFFFFFF) return ROT_EINVAL;
   const unsigned grid = (unsigned)blocks;
-  switch (tpr) {
-    case 32: return launch_runs<T, U, 32, N, DROP>(a, grid, s);
-    case 128: return launch_runs<T, U, 128, N, DROP>(a, grid, s);
-    case 256: return launch_runs<T, U, 256, N, DROP>(a, grid, s);
-    case 512: return launch_runs<T, U, 512, N, DROP>(a, grid, s);
-    case 1024: return launch_runs<T, U, 1024, N, DROP>(a, grid, s);
+  if constexpr (U == 1) {
+    constexpr int N = kSingles;
+    switch (tpr) {
+      case 32:
+        if (a.cols <= 32 * kFewSingles) return launch_single<T, 32, kFewSingles, DROP>(a, grid, s);
+        return launch_single<T, 32, N, DROP>(a, grid, s);
+      case 64: return launch_single<T, 64, N, DROP>(a, grid, s);
+      case 128: return launch_single<T, 128, N, DROP>(a, grid, s);
+      case 256: return launch_single<T, 256, N, DROP>(a, grid, s);
+      case 512: return launch_single<T, 512, N, DROP>(a, grid, s);
+      case 1024: return launch_single<T, 1024, N, DROP>(a, grid, s);
+    }
+  } else {
+    constexpr int N = kMostRuns;
+    switch (tpr) {
+      case 32: return launch_runs<T, U, 32, N, DROP>(a, grid, s);
+      case 128: return launch_runs<T, U, 128, N, DROP>(a, grid, s);
+      case 256: return launch_runs<T, U, 256, N, DROP>(a, grid, s);
+      case 512: return launch_runs<T, U, 512, N, DROP>(a, grid, s);
+      case 1024: return launch_runs<T, U, 1024, N, DROP>(a, grid, s);
+    }
   }
   norm_fwd_wide_kernel<T><<<grid, 1024, 0, s>>>(a);
   return launched();
