@@ -591,6 +591,24 @@ def test_product_of_few_rows(M, N, K):
     near(c, 1 + want, bound + 2 * E * (want.abs() + 1), "accumulated")
 
 
+@pytest.mark.parametrize("N", [300, 301, 571])
+def test_product_whose_cut_columns_come_again(N):
+    """Several tiles to an SM, of which every other one is cut within the
+    columns that a warp stores at once."""
+    g = gen(N)
+    M, K = 128 * 308 + 5, 130
+    a = ops.fp8_quantize(torch.randn(M, K, generator=g, device="cuda"))[0]
+    b = ops.fp8_quantize(torch.randn(N, K, generator=g, device="cuda"), block_rows=128)[0]
+    va, vb = ref.values(a), ref.values(b)
+    want, bound = va @ vb.t(), product_bound(va, vb, K)
+    near(ops.fp8_matmul(a, b), want, bound, "float32")
+    near(ops.fp8_matmul(a, b, dtype=BF16), want, bound + (want.abs() + bound) * U[BF16] * 1.01 + TINY[BF16], "bfloat16")
+    c = torch.ones(M, N, device="cuda")
+    ops.fp8_matmul(a, b, out=c, accumulate=True)
+    near(c, 1 + want, bound + 2 * E * (want.abs() + 1), "accumulated")
+    assert ops.status() == B.ROT_OK
+
+
 def test_layer_reads_a_weight_written_just_before():
     """Back to back on one stream, each call's operands from the call before."""
     g = gen(9)
