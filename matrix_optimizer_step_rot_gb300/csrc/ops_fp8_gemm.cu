@@ -262,7 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  wait_for_prior();  // (the operands may come from the kernel before)
+  // The operands may come from the kernel before; not those of a product's
+  // second, whose first has waited for them before it let this one start.
+  if (p.chain != kSecond) wait_for_prior();
+  if (p.chain == kFirst) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Warps 0 and 1 run their loops as a whole, with one lane's copies and MMAs
   // in between: operands and addresses stay in uniform registers.  From a
@@ -466,6 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
   if (threadIdx.x == 0 && *abort_flag && g.status) atomicExch(g.status, ROT_ETIMEOUT);
+  // (what comes after this kernel takes the first product for done, too)
+  if (p.chain == kSecond) wait_for_prior();
 }
 
 // C from the parts, added in order of K.
@@ -560,6 +565,10 @@ uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   const Shape s = shape_of(M, N, K);
   return s.splits > 1 ? align256(4ull * s.splits * M * s.ldp) : 0;
+}
+
+bool fp8_one_launch(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && N > 0 && K > 0 && !fp8_few(M, N, K) && shape_of(M, N, K).splits == 1;
 }
 
 int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
