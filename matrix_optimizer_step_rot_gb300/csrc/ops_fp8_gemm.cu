@@ -45,6 +45,14 @@ constexpr int kStages = 5;
 constexpr int kABytes = BM * BK, kBBytes = BN * BK, kStageBytes = kABytes + kBBytes;
 constexpr int kScaleBytes = 512 + 1024;  // a stretch's: A's 128 rows, B's 192 (of 256)
 constexpr int kSlots = 3;                // stretches of scales on their way
+// Two barriers of arrival per stage, taken in turn: an issuing warp passes over
+// the other's stretches without waiting, and a barrier tells only the last
+// phase from the one before.  With one per stage a warp could reach a stage
+// whose last load, the other warp's, had not arrived yet, and take it for its
+// own.  When it waits for block x, its last own block is x - 5 or later, whose
+// load was issued after block x - 10, the barrier's last use, was consumed.
+constexpr int kFulls = 2 * kStages;
+static_assert(kStages >= 5, "a warp's blocks are at most a stretch and one apart");
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8, kEpiCols = BN / 2;
 constexpr int kStagingBytes = 32 * 64;  // per epilogue warp
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint8_t* scales = smem + kStages * kStageBytes;
   uint8_t* staging = scales + kSlots * kScaleBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStagingBytes);
-  uint64_t* empty = full + kStages;
+  uint64_t* empty = full + kFulls;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* sfull = tempty + 2;
@@ -237,10 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag) != 0; };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < kFulls; ++s) ptx::mbar_init(&full[s], 1);
+    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&empty[s], 1);
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&tfull[a], 1);
       ptx::mbar_init(&tempty[a], kEpiWarps);
@@ -278,26 +284,28 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       ptx::tma_prefetch_desc(&g.a);
       ptx::tma_prefetch_desc(&g.b);
     }
-    int stage = 0;
-    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    int turn = 0;  // block mod kFulls
+    uint32_t phase = 0, armed = 0, armed_parity = 0;  // phase: of full[turn]
     for (int u = blockIdx.x; u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
       int kb = t.k0;
       while (kb < t.k1 && !aborted()) {
         const int k1 = min(t.k1, kb + kStretch);
         for (; kb < k1; ++kb) {
-          wait(&empty[stage], phase ^ 1u, abort_flag, limit);
+          // (a stage's uses alternate with the two halves of the turns)
+          const int stage = turn < kStages ? turn : turn - kStages;
+          wait(&empty[stage], turn < kStages ? 1u : 0u, abort_flag, limit);
           if (*abort_flag) break;  // (the stage may still be read)
           uint8_t* st = smem + stage * kStageBytes;
           if (one) {
-            ptx::mbar_arrive_expect_tx(&full[stage], kStageBytes);
-            ptx::tma_load_2d(st, &g.a, &full[stage], kb * BK, t.m0);
-            ptx::tma_load_2d(st + kABytes, &g.b, &full[stage], kb * BK, t.n0);
+            ptx::mbar_arrive_expect_tx(&full[turn], kStageBytes);
+            ptx::tma_load_2d(st, &g.a, &full[turn], kb * BK, t.m0);
+            ptx::tma_load_2d(st + kABytes, &g.b, &full[turn], kb * BK, t.n0);
           }
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
+          armed |= 1u << turn;
+          armed_parity = (armed_parity & ~(1u << turn)) | (phase << turn);
+          if (++turn == kFulls) {
+            turn = 0;
             phase ^= 1u;
           }
         }
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (kb < t.k1) break;
     }
     __syncwarp();
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < kFulls; ++s)
       if (armed & (1u << s)) drain(&full[s], (armed_parity >> s) & 1u, limit);
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issue
@@ -314,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int odd = warp >> 1;
     const bool one = ptx::elect_one();
     const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
-    int stage = 0, turn = 0, slot = 0;
+    int block = 0, turn = 0, slot = 0;  // block: mod kFulls; phase: of full[block]
     uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
     const uint32_t d = tmem + (uint32_t)(odd * BN);
@@ -339,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < kStretch; ++j) {
             if (j >= n) break;
-            wait(&full[stage], phase, abort_flag, limit);
+            const int stage = block < kStages ? block : block - kStages;
+            wait(&full[block], phase, abort_flag, limit);
             ptx::tc_fence_after();
             const uint32_t st = ptx::smem_u32(smem + stage * kStageBytes);
             const uint64_t da = ptx::sw128_kmajor_desc(st);
@@ -352,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                                (j > 0 || i > 0) ? 1u : 0u);
               ptx::umma_commit(&empty[stage]);
             }
-            if (++stage == kStages) {
-              stage = 0;
+            if (++block == kFulls) {
+              block = 0;
               phase ^= 1u;
             }
           }
@@ -363,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           }
           acc_phase ^= 1u;
         } else {
-          stage += n;
-          if (stage >= kStages) {
-            stage -= kStages;
+          block += n;
+          if (block >= kFulls) {
+            block -= kFulls;
             phase ^= 1u;
           }
         }

@@ -1,6 +1,8 @@
 """The training operators without a GPU: the generator against its published
 vectors, what the entry points refuse, and sizes with nothing to do."""
 
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -157,3 +159,54 @@ def test_dequantize():
     assert torch.equal(m.dequantize(), torch.tensor([[1.5, -448.0], [0.0, 8.0]]))
     m = ops.Fp8Matrix(q, torch.tensor([[255]], dtype=torch.uint8), 128)
     assert torch.isnan(m.dequantize()).all()
+
+
+def _ring(r, bars, lengths, stages=5, most=4):
+    """A model of the 8-bit product's ring: one warp loads blocks of K into
+    `stages` places in order, loads arrive and products end in any order, and
+    two warps take stretches of up to `most` blocks in turns, each waiting for
+    its own blocks alone on barrier (block mod `bars`), which tells the parity
+    of its last finished phase.  What goes wrong, or None."""
+    blocks, own, turn = 0, ([], []), 0
+    for k in lengths:
+        while k > 0:
+            n = min(most, k)
+            own[turn].extend(range(blocks, blocks + n))
+            blocks, k, turn = blocks + n, k - n, turn ^ 1
+    full, empty, armed = [0] * bars, [0] * stages, set()
+    loading, arrived, products, at, issued = [], set(), [], [0, 0], 0
+    while True:
+        todo = ["load"] * (issued < blocks and empty[issued % stages] == issued // stages)
+        todo += ["arrive"] * bool(loading) + ["end"] * bool(products)
+        # a parity wait returns where the phase under way has the other parity
+        todo += [w for w in (0, 1) if at[w] < len(own[w]) and
+                 full[own[w][at[w]] % bars] % 2 != own[w][at[w]] // bars % 2]
+        if not todo:
+            return None if issued == blocks and at == [len(own[0]), len(own[1])] else "stuck"
+        what = r.choice(todo)
+        if what == "load":
+            if issued % bars in armed:
+                return "armed twice"
+            armed.add(issued % bars)
+            loading.append(issued)
+            issued += 1
+        elif what == "arrive":
+            b = loading.pop(r.randrange(len(loading)))
+            arrived.add(b)
+            armed.discard(b % bars)
+            full[b % bars] += 1
+        elif what == "end":
+            empty[products.pop(r.randrange(len(products))) % stages] += 1
+        else:
+            b = own[what][at[what]]
+            if b not in arrived:
+                return "taken before it arrived"
+            products.append(b)
+            at[what] += 1
+
+
+def test_ring_needs_two_barriers_per_stage():
+    r = random.Random(5)
+    cases = [[r.randint(1, 13) for _ in range(r.randint(1, 8))] for _ in range(1500)]
+    assert all(_ring(r, 10, c) is None for c in cases)
+    assert any(_ring(r, 5, c) == "taken before it arrived" for c in cases)
