@@ -24,6 +24,12 @@ struct Quant {
   int e5m2, square;  // square: blocks of 128 x 128
   int wide;          // q's rows are 16-byte aligned
 };
+// Two matrices in one launch: CTAs up to `first` take the one, the others the
+// other.
+struct QuantPair {
+  Quant m[2];
+  unsigned first;
+};
 
 // Two values as 8-bit floats, the first in the low byte.
 template <bool E5>
@@ -175,14 +181,16 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
 // memory as 16.
 template <class T, bool VEC, bool E5>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
-    quantize_kernel(const __grid_constant__ Quant a) {
+    quantize_kernel(const __grid_constant__ QuantPair pair) {
+  const Quant& a = pair.m[blockIdx.x >= pair.first];
+  const unsigned block = blockIdx.x - (blockIdx.x >= pair.first ? pair.first : 0u);
   __shared__ __align__(16) uint32_t colmax[16][kQ];
   __shared__ __align__(16) uint8_t colscale[kQ];
   __shared__ uint32_t wide[8];
   __shared__ __align__(16) uint8_t tile[kQ * kPitch];
   constexpr int W = 8 * sizeof(T) / 4;
   const int64_t tiles_c = (a.cols + kQ - 1) / kQ;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;  // tile row, column
+  const int64_t tr = block / tiles_c, tc = block % tiles_c;  // tile row, column
   const int64_t r0 = tr * kQ, c0 = tc * kQ;
   const int g = threadIdx.x / 16, v = threadIdx.x % 16;
   const int64_t r = r0 + 8 * g, c = c0 + 8 * v;
@@ -375,12 +383,33 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
   }
 }
 
+inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m; }
+constexpr int64_t kMost = (int64_t(1) << 31) - 256;
+
+inline int64_t tiles_of(const Quant& a) { return up(a.rows, kQ) * up(a.cols, kQ); }
+template <class T>
+bool vec_of(const Quant& a) {
+  return rows16(a.x, a.ldx, sizeof(T));
+}
+template <class T>
+double bytes_of(const Quant& a) {
+  return (double)a.rows * a.cols * (sizeof(T) + (a.q != nullptr) + (a.qt != nullptr));
+}
+
+template <class T>
+int launch_tiles(const QuantPair& p, unsigned grid, cudaStream_t s) {
+  const bool vec = vec_of<T>(p.m[0]);
+  auto k = p.m[0].e5m2 ? (vec ? quantize_kernel<T, true, true> : quantize_kernel<T, false, true>)
+                       : (vec ? quantize_kernel<T, true, false> : quantize_kernel<T, false, false>);
+  k<<<grid, 256, 0, s>>>(p);
+  return launched();
+}
+
 template <class T>
 int launch_quantize(const Quant& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)(((a.cols + kQ - 1) / kQ) * ((a.rows + kQ - 1) / kQ));
-  const bool vec = rows16(a.x, a.ldx, sizeof(T));
-  const double n = (double)a.rows * a.cols;
-  ProfScope prof(ROT_PROF_ELEMENTWISE, n * (sizeof(T) + (a.q != nullptr) + (a.qt != nullptr)), s);
+  const unsigned grid = (unsigned)tiles_of(a);
+  const bool vec = vec_of<T>(a);
+  ProfScope prof(ROT_PROF_ELEMENTWISE, bytes_of<T>(a), s);
   const int64_t row_blocks = a.rows * ((a.cols + 127) / 128);
   if (!a.qt && !a.square && row_blocks < (1ll << 30)) {
     const int64_t most = (row_blocks + 31) / 32;
@@ -390,14 +419,22 @@ int launch_quantize(const Quant& a, cudaStream_t s) {
     k<<<ctas, 256, 0, s>>>(a);
     return launched();
   }
-  auto k = a.e5m2 ? (vec ? quantize_kernel<T, true, true> : quantize_kernel<T, false, true>)
-                  : (vec ? quantize_kernel<T, true, false> : quantize_kernel<T, false, false>);
-  k<<<grid, 256, 0, s>>>(a);
-  return launched();
+  return launch_tiles<T>({{a, a}, grid}, grid, s);
 }
 
-inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m; }
-constexpr int64_t kMost = (int64_t(1) << 31) - 256;
+// Both orientations' tiles of a (and of b) in one launch where they load
+// alike: small matrices' launches are most of their time (436 x 2714 and 436 x
+// 203: 6 us, 18 in two).
+template <class T>
+int launch_both(const Quant& a, const Quant& b, cudaStream_t s) {
+  const int64_t grid = tiles_of(a) + tiles_of(b);
+  if (vec_of<T>(a) != vec_of<T>(b) || grid > 0x7FFFFFFF) {
+    const int e = launch_quantize<T>(a, s);
+    return e != ROT_OK ? e : launch_quantize<T>(b, s);
+  }
+  ProfScope prof(ROT_PROF_ELEMENTWISE, bytes_of<T>(a) + bytes_of<T>(b), s);
+  return launch_tiles<T>({{a, b}, (unsigned)tiles_of(a)}, (unsigned)grid, s);
+}
 
 bool bad_operand(const void* d, int64_t ld, int32_t fmt, const uint8_t* s, int64_t lds,
                  int32_t block_rows, int64_t rows, int64_t K) {
@@ -591,11 +628,22 @@ int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const 
   const uint64_t more =
       std::max(rot_fp8_gemm_work_bytes(tokens, inner, outer), rot_fp8_gemm_work_bytes(outer, inner, tokens));
   char* part = c.take(more);
-  int e = rot_fp8_quantize(dy, lddy, tokens, outer, type, ROT_TYPE_E4M3, 1, d.q, d.ld, d.s, d.lds,
-                           dt.q, dt.ld, dt.s, dt.lds, stream);
-  if (e == ROT_OK)
-    e = rot_fp8_quantize(x, ldx, tokens, inner, type, ROT_TYPE_E4M3, 1, nullptr, 0, nullptr, 0,
-                         xt.q, xt.ld, xt.s, xt.lds, stream);
+  int e = ROT_OK;
+  if (tokens > 0 && inner > 0 && outer > 0) {
+    if (up(tokens, kQ) * up(std::max(inner, outer), kQ) > 0x7FFFFFFF) return ROT_EINVAL;
+    e = check_device();
+    if (e != ROT_OK) return e;
+    const Quant qd = {dy, d.q, d.s, dt.q, dt.s, lddy, tokens, outer, d.ld, d.lds, dt.ld, dt.lds,
+                      0, 0, rows16(d.q, d.ld, 1)};
+    const Quant qx = {x, nullptr, nullptr, xt.q, xt.s, ldx, tokens, inner, 0, 0, xt.ld, xt.lds,
+                      0, 0, 0};
+    e = guarded([&] {
+      cudaStream_t s = static_cast<cudaStream_t>(stream);
+      if (type == ROT_TYPE_F32) return launch_both<float>(qd, qx, s);
+      if (type == ROT_TYPE_F16) return launch_both<__half>(qd, qx, s);
+      return launch_both<__nv_bfloat16>(qd, qx, s);
+    });
+  }
   // Neither product fills its last round of SMs (4099 x 2048 x 6144: 2.4 and
   // 3.5 rounds): the second starts on those that the first leaves, 10 us less for
   // both (of 95).
