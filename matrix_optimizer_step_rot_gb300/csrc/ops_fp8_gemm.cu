@@ -23,7 +23,7 @@
 // Few tiles: K is split over units whose float32 parts go to the workspace and
 // are joined in a fixed order by a second kernel.
 //
-// 8192 x 12288 x 4096: 274 us, 3005 TFLOP/s; 6144 x 2048 x 4099 into float32:
+// 8192 x 12288 x 4096: 272 us, 3030 TFLOP/s; 6144 x 2048 x 4099 into float32:
 // 49 us.  Both CTAs of a pair sharing their block of B by TMA multicast sent a
 // third less from L2 and was not faster (279 us).
 #include <cuda.h>

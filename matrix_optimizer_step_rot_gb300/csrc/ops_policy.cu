@@ -215,7 +215,7 @@ __device__ __forceinline__ ScaledSum join_row(ScaledSum t, ScaledSum* red, Scale
 // row backwards, to meet what L2 and L1 still have.  What is not needed again
 // (the second pass's reads, the gradient) leaves the caches first.
 //
-// 4096 rows of 128 KB, a fifth of them masked: 171 us (5.7 TB/s) on 512
+// 4096 rows of 128 KB, a fifth of them masked: 168 us (5.8 TB/s) on 512
 // threads, two rows per SM; four rows of 256 threads each, 6 us more, since
 // L2 no longer keeps them all.  A share of the row held in shared memory by a
 // CTA of a cluster, read once: 191 to 259 us over shares and CTA counts; the
