@@ -299,7 +299,7 @@ __device__ __forceinline__ uint32_t keep_bits(const Drop& d, uint64_t i0, int co
   uint32_t mine = 0;
 #pragma unroll
   for (int r = 0; r < N / 4 + 1; ++r) {
-    if (r == N / 4 && (int)phase + count <= 32 * N) break;
+    if (r == N / 4 && (int)phase + min(count, 32 * N) <= 32 * N) break;
     const Words w = philox(d, (i0 >> 2) + r * 32 + lane);
 #pragma unroll
     for (int k = 0; k < 4; ++k) mine |= (w.w[k] > d.bar ? 1u : 0u) << (4 * r + k);
