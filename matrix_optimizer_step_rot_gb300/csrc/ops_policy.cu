@@ -127,20 +127,28 @@ __device__ __forceinline__ int edge_of(const Share& s, int vocab, int rank, int 
 }
 
 // The log-probability (x log2(e) - o - log2(s)) ln 2 as a float32 and what its
-// rounding leaves.  x log2(e) and the products with ln 2 carry their rounding
-// errors along, and s = 2^k f has its whole exponents taken off exactly: a
-// policy's ratios and their sum lose nothing to a logp of 10 being rounded to
-// 2^-21.
+// rounding leaves.  log2(e) is the float32 that the sum's exponents were formed
+// with: whatever all of a row's logits have in common then cancels, and what
+// that float32 lacks is 1.3e-8 of the distance between logits alone.  The
+// product, both differences and the product with ln 2 carry their rounding
+// errors along (Knuth's exact sum of two), and s = 2^k f has its whole exponents
+// taken off exactly, so that a ratio loses nothing to a logp of 10 being rounded
+// to 2^-21.
+__device__ __forceinline__ float rounded_off(float a, float b, float sum) {
+  const float t = sum - a;
+  return (a - (sum - t)) + (b - t);
+}
 __device__ __forceinline__ float log_prob(float x, float o, float s, float& rest) {
-  constexpr float kLog2eRest = 1.9259629911e-8f, kLn2Rest = -1.9046542999e-9f;
+  constexpr float kLn2Rest = -1.9046542999e-9f;
   const float hi = x * kLog2e;
   rest = 0.f;
   if (!(fabsf(hi) < INFINITY) || !(s < INFINITY)) return kLn2 * (hi - o - log2f(s));
-  const float lo = fmaf(x, kLog2e, -hi) + x * kLog2eRest;
+  const float lo = fmaf(x, kLog2e, -hi);
   const int k = (__float_as_int(s) - 0x3F400000) >> 23;  // f in [0.75, 1.5)
   const float f = __int_as_float(__float_as_int(s) - (k << 23));
-  const float d = (hi - o) - (float)k, r = lo - log2f(f);
-  const float t = d + r, e = r - (t - d);
+  const float whole = -(o + (float)k), d = hi + whole;
+  const float r = (lo + rounded_off(hi, whole, d)) - log2f(f);
+  const float t = d + r, e = rounded_off(d, r, t);
   const float p = kLn2 * t, q = fmaf(kLn2, t, -p) + (kLn2Rest * t + kLn2 * e);
   const float logp = p + q;
   rest = q - (logp - p);

@@ -402,6 +402,52 @@ def test_policy_loss(tokens, vocab, dtype, pad, masked):
     near(doubled[~edge], 4 * grad[~edge], 4 * (dgrad + U[dtype] * grad.abs())[~edge] * 1.01 + 4 * TINY[dtype], "scaled")
 
 
+def logp_bound(z, targets):
+    """(log-probabilities in 64 bits, bound).  The numbers that count are the
+    distances from the row's largest entry, e = (x - max) log2(e): each
+    exponent rounds once (E |e|, and 3/4 more for the whole scale), an
+    exponential is 2^-22 off, log2(e) as a float32 turns x - mean by E / 4; 40
+    for the chains of additions and rescalings of at most 4 batches; the
+    result and its two factors round at its size.  Nothing grows with the
+    row's own level."""
+    z = z.double()
+    full = z - torch.logsumexp(z, 1, keepdim=True)
+    p = full.exp()
+    e = (z - z.max(1, keepdim=True).values) / np.log(2.0)
+    e = torch.where(p > 0, e, 0.0)
+    logp = full.gather(1, targets[:, None])[:, 0]
+    mean = (p * torch.where(p > 0, full, 0.0)).sum(1)
+    return logp, E * (44 + (p * (e.abs() + 1)).sum(1) + 3 * logp.abs() + 0.25 * (logp - mean).abs())
+
+
+LEVELS = [0.0, 1e2, -1e2, 1e3, -1e3, 1e4, -1e4, 6e4, -6e4, 1e5, -1e5, 1e6, -1e6]
+
+
+@pytest.mark.parametrize("dtype,level", [(t, x) for t in (F32, F16, BF16) for x in LEVELS
+                                         if t != F16 or abs(x) < 65000])
+def test_policy_loss_does_not_depend_on_the_rows_level(dtype, level):
+    """Logits that lie together far from zero."""
+    tokens, vocab = 48, 1000
+    g = gen(int(abs(level)) + 1)
+    z = (2 * torch.randn(tokens, vocab, generator=g, device="cuda", dtype=torch.float64) + level).to(dtype)
+    targets = torch.randint(vocab, (tokens,), generator=g, device="cuda")
+    logp, bound = logp_bound(z, targets)
+    old = (logp + 0.3 * torch.randn(tokens, generator=g, device="cuda")).float()
+    r = (logp + 0.3 * torch.randn(tokens, generator=g, device="cuda")).float()
+    adv = torch.randn(tokens, generator=g, device="cuda")
+    w = torch.rand(tokens, generator=g, device="cuda") + 0.5
+    f = np.float32
+    (loss, _, _, grad), _, dterm, dgrad = policy_bounds(z, targets, old, r, adv, w, float(f(0.2)), float(f(0.3)),
+                                                        float(f(0.1)))
+    got = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=0.2, clip_high=0.3, kl_coef=0.1)
+    near(got[1], logp, bound, "logp")
+    near(ops.token_logprobs(z, targets), logp, bound, "token_logprobs")
+    ratio = torch.exp(logp - old.double())
+    clear = ((ratio - 0.8).abs() > 1e-5) & ((ratio - 1.3).abs() > 1e-5)
+    near(got[2][clear], grad[clear], (dgrad + U[dtype] * grad.abs())[clear] * 1.01 + TINY[dtype], "dlogits")
+    assert abs(got[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item())
+
+
 def test_policy_loss_in_place_and_without_reference():
     z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
     want = ops.policy_loss(z, targets, old, adv, w)
