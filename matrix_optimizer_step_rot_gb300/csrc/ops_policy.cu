@@ -28,6 +28,9 @@ struct Policy {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kAhead = 4;  // 16-byte loads of a thread in flight
+// Up to here a float32 product is within 1/4 of x log2(e), so that the largest
+// exponential of a row is within 2^-0.75 and 2^0.75.
+constexpr float kMostScale = 4194304.f;  // 2^22
 
 // Sum of exponentials on a running scale: the sum of 2^(x log2(e) - o) with a
 // whole number o near the largest x log2(e), so that o is exact, no rounding
@@ -291,11 +294,13 @@ __global__ void __launch_bounds__(kRow, 1024 / kRow)
     sum = join(sum, one);
   }
   sum = join_row<kRow>(sum, red, &mine, ranks);
-  // With x log2(e) beyond float32's range, or nothing but -inf, the scale says
-  // nothing: the row's largest element takes its part, 2^((x - m) log2(e)).
-  // (the same for every thread of the row)
+  // Where x log2(e) is beyond float32's range, or rounds by more than a half (o
+  // is then no longer near the largest one, and the exponentials may all be 0 or
+  // infinite), or with nothing but -inf, the scale says nothing: the row's
+  // largest element takes its part, 2^((x - m) log2(e)).  (the same for every
+  // thread of the row)
   float m = 0.f;
-  if (!(fabsf(sum.o) < INFINITY) || !(sum.s < INFINITY)) {
+  if (!(fabsf(sum.o) <= kMostScale) || !(sum.s < INFINITY)) {
     ScaledSum top = {-INFINITY, 0.f};  // o: the maximum
     for (int i = sh.v0 + threadIdx.x; i < sh.v1; i += kRow) top.o = fmaxf(top.o, largest(runs[i]));
     if (edge >= 0) top.o = fmaxf(top.o, to_f32(z[edge]));

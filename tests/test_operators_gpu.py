@@ -402,6 +402,13 @@ def test_policy_loss(tokens, vocab, dtype, pad, masked):
     near(doubled[~edge], 4 * grad[~edge], 4 * (dgrad + U[dtype] * grad.abs())[~edge] * 1.01 + 4 * TINY[dtype], "scaled")
 
 
+def from_largest(z):
+    """The rows in 64 bits with their largest entry taken off: the same
+    distribution, in numbers whose 64 bits are enough at any level."""
+    z = z.double()
+    return z - z.max(1, keepdim=True).values
+
+
 def logp_bound(z, targets):
     """(log-probabilities in 64 bits, bound).  The numbers that count are the
     distances from the row's largest entry, e = (x - max) log2(e): each
@@ -410,10 +417,10 @@ def logp_bound(z, targets):
     for the chains of additions and rescalings of at most 4 batches; the
     result and its two factors round at its size.  Nothing grows with the
     row's own level."""
-    z = z.double()
+    z = from_largest(z)
     full = z - torch.logsumexp(z, 1, keepdim=True)
     p = full.exp()
-    e = (z - z.max(1, keepdim=True).values) / np.log(2.0)
+    e = z / np.log(2.0)
     e = torch.where(p > 0, e, 0.0)
     logp = full.gather(1, targets[:, None])[:, 0]
     mean = (p * torch.where(p > 0, full, 0.0)).sum(1)
@@ -445,6 +452,38 @@ def test_policy_loss_does_not_depend_on_the_rows_level(dtype, level):
     ratio = torch.exp(logp - old.double())
     clear = ((ratio - 0.8).abs() > 1e-5) & ((ratio - 1.3).abs() > 1e-5)
     near(got[2][clear], grad[clear], (dgrad + U[dtype] * grad.abs())[clear] * 1.01 + TINY[dtype], "dlogits")
+    assert abs(got[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item())
+
+
+FAR = [-1e4, -6e4, -1e8, -1e9, -1.5e9, -1e10, -1e12, -1e15, -1e30, 1e4, 1e8, 1e9, 1e10, 1e12, 1e15, 1e30]
+
+
+@pytest.mark.parametrize("dtype,level", [(t, x) for t in (F32, F16, BF16) for x in FAR if t != F16 or abs(x) < 65000])
+def test_policy_loss_far_from_zero(dtype, level):
+    """Whole rows of one number, rows next to it (spacings of the type at that
+    level apart), and rows of which a part is that number."""
+    g = gen(5)
+    vocab = 40
+    z = torch.full((12, vocab), level, device="cuda", dtype=torch.float64)
+    step = abs(level) * 2 * U[dtype]  # (about a spacing)
+    z[4:8] += step * torch.randint(-2, 3, (4, vocab), generator=g, device="cuda")
+    z[8:, 5:] = torch.randn(4, vocab - 5, generator=g, device="cuda").double()
+    z = z.to(dtype)
+    targets = torch.randint(vocab, (12,), generator=g, device="cuda")
+    targets[8:] = z[8:].argmax(1)
+    logp, bound = logp_bound(z, targets)
+    one = torch.ones(12, device="cuda")
+    old, ref_ = (logp - 0.1).float(), (logp + 0.05).float()
+    f = np.float32
+    # (a logp far below -100 rounds by more than a ratio could be told from)
+    w = torch.where(logp > -100, one, 0.0)
+    (loss, _, _, grad), _, dterm, dgrad = policy_bounds(from_largest(z), targets, old, ref_, one, w, float(f(0.2)),
+                                                        float(f(0.2)), float(f(0.1)))
+    near(ops.token_logprobs(z, targets), logp, bound, "token_logprobs")
+    got = ops.policy_loss(z, targets, old, one, w, ref_logp=ref_, kl_coef=0.1)
+    on = w != 0
+    near(got[1][on], logp[on], bound[on], "logp")
+    near(got[2], grad, (dgrad + U[dtype] * grad.abs()) * 1.01 + TINY[dtype], "dlogits")
     assert abs(got[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item())
 
 
