@@ -145,7 +145,9 @@ __device__ __forceinline__ float log_prob(float x, float o, float s, float& rest
   constexpr float kLn2Rest = -1.9046542999e-9f;
   const float hi = x * kLog2e;
   rest = 0.f;
-  if (!(fabsf(hi) < INFINITY) || !(s < INFINITY)) return kLn2 * (hi - o - log2f(s));
+  // (x log2(e) is beyond float32's range before x is: a float32's or bfloat16's
+  // lowest value as a mask stays finite)
+  if (!(fabsf(hi) < INFINITY) || !(s < INFINITY)) return x - kLn2 * (o + log2f(s));
   const float lo = fmaf(x, kLog2e, -hi);
   const int k = (__float_as_int(s) - 0x3F400000) >> 23;  // f in [0.75, 1.5)
   const float f = __int_as_float(__float_as_int(s) - (k << 23));

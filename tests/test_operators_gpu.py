@@ -487,6 +487,27 @@ def test_policy_loss_far_from_zero(dtype, level):
     assert abs(got[0].item() - loss.item()) <= dterm.sum().item() + E * abs(loss.item())
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_policy_loss_of_targets_at_the_lowest_value(dtype):
+    """A target masked with the type's lowest value has a finite
+    log-probability: its distance from the rest."""
+    lowest = torch.finfo(dtype).min
+    z = torch.randn(6, 300, generator=gen(8), device="cuda").to(dtype)
+    targets = torch.arange(6, device="cuda") * 50
+    z[torch.arange(6), targets] = lowest
+    logp, bound = logp_bound(z, targets)
+    assert torch.isfinite(logp).all()
+    got = ops.token_logprobs(z, targets)
+    near(got, logp, bound, "logp")
+    one = torch.ones(6, device="cuda")
+    loss, _, d = ops.policy_loss(z, targets, got, one, one / 6, ref_logp=got, kl_coef=0.1)
+    assert torch.isfinite(d).all()
+    if dtype == F16:  # (the ratio to the rounded log-probability: within 2^-9 of 1)
+        assert abs(loss.item() + 1) <= 2.0 ** -8
+    else:
+        assert abs(loss.item() + 1) <= 8 * E
+
+
 def test_policy_loss_in_place_and_without_reference():
     z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
     want = ops.policy_loss(z, targets, old, adv, w)
