@@ -136,7 +136,8 @@ int rot_token_logprobs(const void* logits, int64_t ldl, const int64_t* targets,
 
 /* Loss and gradient.  loss: one float32 (the terms' sum in a fixed order);
  * logp, terms: `tokens` float32 each (terms[t] = w term).  ref_logp may be
- * NULL (kl_coef must then be 0).  dlogits (type and vocab as logits, or NULL:
+ * NULL (kl_coef must then be 0), and with kl_coef == 0 it is not looked at.
+ * dlogits (type and vocab as logits, or NULL:
  * loss only) receives grad_scale times the gradient; it may be the logits
  * themselves (same ld).  tokens == 0 sets loss to 0.
  * Errors: as rot_token_logprobs, plus clip bounds or kl_coef negative or NaN,

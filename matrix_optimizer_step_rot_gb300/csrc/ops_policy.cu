@@ -500,7 +500,9 @@ int rot_policy_loss(const void* logits, int64_t ldl, const int64_t* targets, con
   Policy a = {};
   a.logits = logits, a.ldl = ldl, a.targets = targets, a.weights = weights, a.logp = logp;
   a.tokens = tokens, a.vocab = (int)vocab;
-  a.old = old_logp, a.ref = ref_logp, a.adv = advantages, a.terms = terms, a.d = dlogits;
+  // (no penalty: its exponential may be infinite, and 0 times that is not 0)
+  a.ref = kl_coef != 0.f ? ref_logp : nullptr;
+  a.old = old_logp, a.adv = advantages, a.terms = terms, a.d = dlogits;
   a.ldd = lddl, a.loss = 1, a.lo = clip_low, a.hi = clip_high, a.kl = kl_coef;
   a.scale = grad_scale;
   return guarded([&] {

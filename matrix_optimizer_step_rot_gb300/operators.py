@@ -192,8 +192,9 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     policy term with its KL penalty, each token's log-probability, and
     grad_scale times the loss's gradient with respect to the logits, in their
     type (None with grad=False).  Tokens with a weight of zero are masked: none
-    of their inputs is looked at, and their gradient row is 0.  out: written
-    instead of a new dlogits; may be `logits` itself."""
+    of their inputs is looked at, and their gradient row is 0.  With kl_coef 0
+    ref_logp is not looked at.  out: written instead of a new dlogits; may be
+    `logits` itself."""
     if stream is not None:
         return _on(stream, lambda: policy_loss(
             logits, targets, old_logp, advantages, weights, ref_logp=ref_logp, clip_low=clip_low,

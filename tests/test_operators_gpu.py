@@ -508,6 +508,14 @@ def test_policy_loss_of_targets_at_the_lowest_value(dtype):
         assert abs(loss.item() + 1) <= 8 * E
 
 
+def test_policy_loss_without_weight_on_the_penalty():
+    """kl_coef 0: a reference far above the policy is not part of the loss."""
+    z, targets, old, r, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
+    want = ops.policy_loss(z, targets, old, adv, w)
+    got = ops.policy_loss(z, targets, old, adv, w, ref_logp=old + 200.0)
+    assert torch.isfinite(want[0]) and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_policy_loss_in_place_and_without_reference():
     z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
     want = ops.policy_loss(z, targets, old, adv, w)
