@@ -516,6 +516,30 @@ def test_policy_loss_without_weight_on_the_penalty():
     assert torch.isfinite(want[0]) and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("delta", [0.0, 1e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.1, 0.24, 0.3, 0.49, 0.51, 1.0, 3.0])
+def test_policy_penalty_near_the_reference(delta):
+    """The penalty alone (advantages 0, ratio 1): exp(r) - r - 1 with r = ref -
+    logp, relative to itself.  Rows of two equal logits, whose logp of -log 2
+    the kernel holds to 48 bits: r rounds twice at most (E each, twice that in
+    the term), the series and its two products 3 E; from 1/2 on the
+    exponential's last place and the difference, 4 E of the term.  At delta 0,
+    r is what float32 leaves of log 2, good to E^2."""
+    z = torch.zeros(64, 2, device="cuda")
+    targets = torch.zeros(64, dtype=torch.int64, device="cuda")
+    sign = torch.where(torch.arange(64, device="cuda") % 2 == 0, 1.0, -1.0)
+    ref_ = (-np.log(2.0) + delta * sign.double()).float()
+    logp = torch.full((64,), -np.log(2.0), device="cuda", dtype=torch.float64)
+    r = ref_.double() - logp
+    zero, one = torch.zeros(64, device="cuda"), torch.ones(64, device="cuda")
+    want = torch.where(r.abs() < 0.02, r * r * (0.5 + r / 6 + r * r / 24 + r ** 3 / 120), torch.expm1(r) - r)
+    # (below 0.02 the series' next term is r^4 / 360 of it: 5e-10)
+    for i in (0, 1):
+        loss, _, _ = ops.policy_loss(z[i:i + 1], targets[:1], logp[:1].float(), zero[:1], one[:1],
+                                     ref_logp=ref_[i:i + 1], kl_coef=1.0, grad=False)
+        w, ri = want[i].item(), abs(r[i].item())
+        assert abs(loss.item() - w) <= 8 * E * w + 1.2 * (ri + ri * ri) * 8 * E * E + 64 * E ** 4, (loss.item(), w)
+
+
 def test_policy_loss_in_place_and_without_reference():
     z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
     want = ops.policy_loss(z, targets, old, adv, w)
