@@ -183,7 +183,9 @@ __device__ __forceinline__ void term_of(const Policy& a, float w, float adv, flo
   // (comparisons, not fminf and fmaxf: NaN has to stay)
   const float lo = 1.f - a.lo, hi = 1.f + a.hi;
   const float clipped = ratio < lo ? lo : ratio > hi ? hi : ratio;
-  const float plain = ratio * adv, bounded = clipped * adv;
+  // (an advantage of 0 takes any ratio out, one beyond float32's range too)
+  const float plain = adv == 0.f && ratio == INFINITY ? 0.f : ratio * adv;
+  const float bounded = clipped * adv;
   const bool through = plain <= bounded;
   // min(plain, bounded) and its derivative's share; a NaN on either side stays
   float v = -(plain != plain || through ? plain : bounded);

@@ -540,6 +540,15 @@ def test_policy_penalty_near_the_reference(delta):
         assert abs(loss.item() - w) <= 8 * E * w + 1.2 * (ri + ri * ri) * 8 * E * E + 64 * E ** 4, (loss.item(), w)
 
 
+def test_policy_loss_of_no_advantage_is_the_penalty_alone():
+    """Advantage 0 under a ratio beyond float32: 0, not 0 times infinity."""
+    z, targets, old, r, adv, w = policy_inputs(40, 1000, F32, 0, 0.3, 1)
+    adv = torch.where(w != 0, 0.0, adv)
+    want = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, kl_coef=0.1)
+    got = ops.policy_loss(z, targets, old - 200.0, adv, w, ref_logp=r, kl_coef=0.1)
+    assert torch.isfinite(want[0]) and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_policy_loss_in_place_and_without_reference():
     z, targets, old, _, adv, w = policy_inputs(40, 1000, BF16, 0, 0.3, 1)
     want = ops.policy_loss(z, targets, old, adv, w)
