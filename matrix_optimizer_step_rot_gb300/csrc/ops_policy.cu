@@ -215,7 +215,8 @@ __device__ __forceinline__ Run<T, U> last_read(const Run<T, U>* p) {
 }
 
 // The row's sum over the CTA's warps and the row's CTAs; the same in every
-// thread.
+// thread.  A barrier on memory for all of them: the gradient may be written where
+// others have read the logits before (shuffles alone do not order that).
 template <int kRow>
 __device__ __forceinline__ ScaledSum join_row(ScaledSum t, ScaledSum* red, ScaledSum* mine,
                                               int ranks) {
@@ -228,6 +229,8 @@ __device__ __forceinline__ ScaledSum join_row(ScaledSum t, ScaledSum* red, Scale
     __syncthreads();
     const ScaledSum none = {-INFINITY, 0.f};
     t = join_warp(lane < W ? red[lane] : none);
+  } else {
+    __syncwarp();
   }
   if (ranks > 1) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();

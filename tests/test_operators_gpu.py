@@ -557,6 +557,18 @@ def test_policy_loss_in_place_and_without_reference():
     assert got[2] is own and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("tokens,vocab,dtype,pad", [
+    (1300, 325, BF16, 0), (1300, 1024, BF16, 0), (1400, 1999, F32, 1), (1300, 4000, F16, 0), (400, 20000, BF16, 0),
+    (5, 70001, F32, 0)])
+def test_policy_gradient_in_the_logits_place(tokens, vocab, dtype, pad):
+    """One plan after the other (a warp, 128 or 512 threads, a cluster): the same bits as in a new tensor."""
+    z, targets, old, r, adv, w = policy_inputs(tokens, vocab, dtype, pad, 0.2, 3)
+    want = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, kl_coef=0.1)
+    own = torch.empty(tokens, vocab + pad, device="cuda", dtype=dtype)[:, :vocab].copy_(z)
+    got = ops.policy_loss(own, targets, old, adv, w, ref_logp=r, kl_coef=0.1, out=own)
+    assert got[2] is own and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_policy_loss_special_rows():
     """Masked vocabulary entries (-inf), the type's lowest value, an empty
     distribution, targets outside the vocabulary, infinite logits: as the
