@@ -103,7 +103,8 @@ Rows rows_of(const Tensor& t, const char* name, const Tensor* like = nullptr) {
   Rows r;
   r.p = t.data_ptr();
   r.cols = t.size(dims - 1);
-  r.rows = r.cols ? t.numel() / r.cols : (dims == 2 ? t.size(0) : 0);
+  r.rows = 1;  // (rows of no elements are rows, too)
+  for (int64_t d = 0; d < dims - 1; ++d) r.rows *= t.size(d);
   r.ld = std::max<int64_t>(r.cols, 1);
   if (t.is_contiguous()) return r;
   if (r.cols > 1 && t.stride(dims - 1) != 1) fail(n + ": its last dimension is not contiguous");

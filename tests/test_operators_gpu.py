@@ -867,6 +867,32 @@ def test_linear(tokens, inner, outer, dtype):
     near(twice, 2 * want, 2 * bound + 4 * E * want.abs(), "dw accumulated")
 
 
+def test_layers_of_no_inner_or_outer_features():
+    """A last dimension of 0 under any number of leading ones: sums of nothing
+    are 0, and the shapes are the leading ones'."""
+    def weights(outer, inner):
+        return ops.fp8_quantize(torch.zeros(outer, inner, device="cuda"), block_rows=128, transposed=True)
+
+    junk = [torch.full((1 << 16,), float("nan"), device="cuda") for _ in range(8)]
+    del junk  # (what an unwritten output would hold)
+    for lead in ((3,), (2, 3), (), (2, 1, 5)):
+        q, qt = weights(24, 0)
+        x = torch.empty(*lead, 0, device="cuda")
+        y = ops.fp8_linear(x, q)
+        assert y.shape == (*lead, 24) and torch.equal(y, torch.zeros_like(y))
+        dy = torch.ones(*lead, 24, device="cuda")
+        dx, dw = ops.fp8_linear_backward(dy, x, qt)
+        assert dx.shape == x.shape and dw.shape == (24, 0)
+        q, qt = weights(0, 24)
+        x = torch.ones(*lead, 24, device="cuda")
+        assert ops.fp8_linear(x, q).shape == (*lead, 0)
+        dx, dw = ops.fp8_linear_backward(torch.empty(*lead, 0, device="cuda"), x, qt)
+        assert dx.shape == x.shape and torch.equal(dx, torch.zeros_like(dx)) and dw.shape == (0, 24)
+    m, t = ops.fp8_quantize(torch.empty(2, 3, 0, device="cuda"), transposed=True)
+    assert m.data.shape == (6, 0) and t.data.shape == (0, 6)
+    assert ops.dropout(torch.empty(2, 3, 0, device="cuda"), 0.5, 1).shape == (2, 3, 0)
+
+
 # ---------------------------------------------------------------------------
 # large operands, streams, graphs, all together
 # ---------------------------------------------------------------------------
