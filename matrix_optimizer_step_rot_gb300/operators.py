@@ -20,6 +20,7 @@ allocates its status word: let it run before a stream capture.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -211,6 +212,7 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
 # ---------------------------------------------------------------------------
 
 _status = {}  # device index -> (the products' status word, its address)
+_making = threading.Lock()
 
 
 def _status_word(like: torch.Tensor) -> int:
@@ -220,9 +222,11 @@ def _status_word(like: torch.Tensor) -> int:
     if i < 0:
         return 0
     if i not in _status:
-        word = torch.zeros(1, dtype=torch.int32, device=like.device)
-        torch.cuda.synchronize(word.device)  # (later calls may be on any stream)
-        _status[i] = word, word.data_ptr()
+        with _making:  # (one word for all threads: launched kernels keep its address)
+            if i not in _status:
+                word = torch.zeros(1, dtype=torch.int32, device=like.device)
+                torch.cuda.synchronize(word.device)  # (later calls may be on any stream)
+                _status[i] = word, word.data_ptr()
     return _status[i][1]
 
 

@@ -2,6 +2,8 @@
 vectors, what the entry points refuse, and sizes with nothing to do."""
 
 import random
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -159,6 +161,48 @@ def test_dequantize():
     assert torch.equal(m.dequantize(), torch.tensor([[1.5, -448.0], [0.0, 8.0]]))
     m = ops.Fp8Matrix(q, torch.tensor([[255]], dtype=torch.uint8), 128)
     assert torch.isnan(m.dequantize()).all()
+
+
+def test_threads_share_a_device_status_word(monkeypatch):
+    """First products of several threads on one device: one word for all of them."""
+    made = []
+
+    class Word:
+        device = "cuda:0"
+
+        def data_ptr(self):
+            return id(self)
+
+    class Torch:
+        int32 = torch.int32
+
+        class cuda:
+            synchronize = staticmethod(lambda device: time.sleep(0.02))
+
+        @staticmethod
+        def zeros(*_, **__):
+            made.append(Word())
+            time.sleep(0.02)
+            return made[-1]
+
+    class Operand:
+        device = "cuda:0"
+        get_device = staticmethod(lambda: 0)
+
+    monkeypatch.setattr(ops, "torch", Torch)
+    monkeypatch.setattr(ops, "_status", {})
+    got, start = [], threading.Barrier(8)
+
+    def first():
+        start.wait()
+        got.append(ops._status_word(Operand))
+
+    threads = [threading.Thread(target=first) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 8 and len(set(got)) == 1 and got[0] == ops._status[0][1] and len(made) == 1
 
 
 def _ring(r, bars, lengths, stages=5, most=4):
