@@ -241,7 +241,8 @@ def status(device="cuda") -> int:
         return B.ROT_OK
     word = _status[i][0]
     code = int(word.item())
-    word.zero_()
+    if code != B.ROT_OK:  # (what another thread's product writes from here on is left for the next call)
+        word.zero_()
     return code
 
 

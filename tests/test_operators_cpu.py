@@ -205,6 +205,26 @@ def test_threads_share_a_device_status_word(monkeypatch):
     assert len(got) == 8 and len(set(got)) == 1 and got[0] == ops._status[0][1] and len(made) == 1
 
 
+def test_status_clears_no_timeout_that_it_did_not_report(monkeypatch):
+    """A product of another thread gives up right after the word was read as 0."""
+
+    class Word:
+        value = B.ROT_OK
+
+        def item(self):
+            seen, self.value = self.value, B.ROT_ETIMEOUT
+            return seen
+
+        def zero_(self):
+            self.value = B.ROT_OK
+
+    word = Word()
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
+    monkeypatch.setattr(ops, "_status", {0: (word, 0)})
+    assert ops.status("cuda:0") == B.ROT_OK
+    assert ops.status("cuda:0") == B.ROT_ETIMEOUT
+
+
 def _ring(r, bars, lengths, stages=5, most=4):
     """A model of the 8-bit product's ring: one warp loads blocks of K into
     `stages` places in order, loads arrive and products end in any order, and
