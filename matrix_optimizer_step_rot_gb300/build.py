@@ -28,6 +28,7 @@ LIB_CHECK = os.path.join(PKG, "librot_check.so")
 # points by address (it does not link against the library)
 TORCH_SRC = os.path.join(CSRC, "torch", "torch_ops.cpp")
 TORCH_EXT = os.path.join(PKG, "_rot_torch.so")
+TORCH_STAMP = os.path.join(BUILD, "torch_stamp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off",
@@ -53,27 +54,36 @@ def _headers():
 
 
 def _torch_command():
-    """Compile command of _rot_torch.so, or None if it is up to date (for the
-    torch at hand)."""
+    """Compile command of _rot_torch.so, or None if it is up to date."""
     import sysconfig
 
     import torch
 
-    stamp = os.path.join(BUILD, "torch_version")
-    if os.path.exists(TORCH_EXT) and os.path.exists(stamp) \
-            and open(stamp).read() == torch.__version__ \
-            and os.path.getmtime(TORCH_EXT) > max(map(os.path.getmtime, [TORCH_SRC, *_headers()])):
-        return None
     root = os.path.dirname(torch.__file__)
     nvcc = _nvcc()
     cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            "-I", INCLUDE, "-I", os.path.join(root, "include"),
-            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
-            TORCH_SRC, "-o", TORCH_EXT + ".tmp", "-L", os.path.join(root, "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           TORCH_SRC, "-o", TORCH_EXT + ".tmp", "-L", os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    newest = max(map(os.path.getmtime, [TORCH_SRC, *_headers()]))
+    if os.path.exists(TORCH_EXT) and os.path.exists(TORCH_STAMP) \
+            and open(TORCH_STAMP).read() == _torch_stamp(cmd) and os.path.getmtime(TORCH_EXT) > newest:
+        return None
+    return cmd
+
+
+def _torch_stamp(cmd) -> str:
+    """What _rot_torch.so was built for and how: torch, the interpreter's ABI
+    and the whole command."""
+    import sysconfig
+
+    import torch
+
+    return "\n".join([torch.__version__, sysconfig.get_config_var("EXT_SUFFIX"), *cmd])
 
 
 def build(verbose: bool = False, extra_flags=None, check: bool = False) -> str:
@@ -110,11 +120,9 @@ def build(verbose: bool = False, extra_flags=None, check: bool = False) -> str:
                 if r.returncode != 0:
                     raise RuntimeError(f"{cmd[0]} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     if torch_cmd:
-        import torch
-
         os.replace(TORCH_EXT + ".tmp", TORCH_EXT)
-        with open(os.path.join(BUILD, "torch_version"), "w") as f:
-            f.write(torch.__version__)
+        with open(TORCH_STAMP, "w") as f:
+            f.write(_torch_stamp(torch_cmd))
     objs = [o for _, _, o in jobs]
     if stale_cmds or not os.path.exists(lib):
         cmd = [nvcc, *ARCH, "-shared", "-o", lib + ".tmp", *objs]

@@ -2,6 +2,7 @@
 vectors, what the entry points refuse, and sizes with nothing to do."""
 
 import random
+import sysconfig
 import threading
 import time
 
@@ -203,6 +204,23 @@ def test_threads_share_a_device_status_word(monkeypatch):
     for t in threads:
         t.join()
     assert len(got) == 8 and len(set(got)) == 1 and got[0] == ops._status[0][1] and len(made) == 1
+
+
+def test_extension_is_rebuilt_for_another_interpreter_or_compiler(monkeypatch):
+    """Up to date once built, and no longer with another ABI tag, compiler or
+    CUDA to include."""
+    assert build._torch_command() is None
+    with monkeypatch.context() as m:
+        config = sysconfig.get_config_var
+        m.setattr(sysconfig, "get_config_var", lambda n: ".other.so" if n == "EXT_SUFFIX" else config(n))
+        assert build._torch_command() is not None
+    with monkeypatch.context() as m:
+        m.setenv("CXX", "another-c++")
+        assert build._torch_command()[0] == "another-c++"
+    with monkeypatch.context() as m:
+        m.setattr(build, "_nvcc", lambda: "/another/cuda/bin/nvcc")
+        assert "/another/cuda/include" in build._torch_command()
+    assert build._torch_command() is None
 
 
 def test_status_clears_no_timeout_that_it_did_not_report(monkeypatch):
