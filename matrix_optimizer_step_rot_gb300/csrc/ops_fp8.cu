@@ -481,14 +481,11 @@ uint64_t rot_fp8_gemm_work_bytes(int64_t M, int64_t N, int64_t K) {
   return fp8_few(M, N, K) ? 0 : fp8_work_bytes(M, N, K);
 }
 
-namespace {
-
-// rot_fp8_gemm, alone or one of two in a row.
-int gemm(int chain, int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
-         const uint8_t* a_scale, int64_t a_lds, int32_t a_block_rows, const void* b, int64_t ldb,
-         int32_t b_format, const uint8_t* b_scale, int64_t b_lds, int32_t b_block_rows, void* c,
-         int64_t ldc, int32_t ctype, int32_t accumulate, void* work, uint64_t work_bytes,
-         int32_t* status, void* stream) {
+int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
+                 const uint8_t* a_scale, int64_t a_lds, int32_t a_block_rows, const void* b,
+                 int64_t ldb, int32_t b_format, const uint8_t* b_scale, int64_t b_lds,
+                 int32_t b_block_rows, void* c, int64_t ldc, int32_t ctype, int32_t accumulate,
+                 void* work, uint64_t work_bytes, int32_t* status, void* stream) {
   if (M < 0 || N < 0 || K < 0 || M > kMost || N > kMost || K > kMost) return ROT_EINVAL;
   if (bad_operand(a, lda, a_format, a_scale, a_lds, a_block_rows, M, K) ||
       bad_operand(b, ldb, b_format, b_scale, b_lds, b_block_rows, N, K))
@@ -503,7 +500,7 @@ int gemm(int chain, int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
   Prod p = {(const uint8_t*)a, (const uint8_t*)b, a_scale, b_scale, c, lda, ldb, a_lds, b_lds, ldc,
             (int)M, (int)N, (int)K, ctype, accumulate, a_format == ROT_TYPE_E5M2,
             b_format == ROT_TYPE_E5M2, a_block_rows == 1 ? 0 : 7, b_block_rows == 1 ? 0 : 7,
-            static_cast<float*>(work), chain};
+            static_cast<float*>(work)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0)  // all bits zero is 0 in every type
     return cudaMemset2DAsync(c, ldc * type_bytes(ctype), 0, N * type_bytes(ctype), M, s) ==
@@ -514,18 +511,6 @@ int gemm(int chain, int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
     if (fp8_few(M, N, K)) return fp8_few_product(p, a, lda, a_format, s);
     return fp8_product(p, reinterpret_cast<int*>(status), s);
   });
-}
-
-}  // namespace
-
-int rot_fp8_gemm(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, int32_t a_format,
-                 const uint8_t* a_scale, int64_t a_lds, int32_t a_block_rows, const void* b,
-                 int64_t ldb, int32_t b_format, const uint8_t* b_scale, int64_t b_lds,
-                 int32_t b_block_rows, void* c, int64_t ldc, int32_t ctype, int32_t accumulate,
-                 void* work, uint64_t work_bytes, int32_t* status, void* stream) {
-  return gemm(kAlone, M, N, K, a, lda, a_format, a_scale, a_lds, a_block_rows, b, ldb, b_format,
-              b_scale, b_lds, b_block_rows, c, ldc, ctype, accumulate, work, work_bytes, status,
-              stream);
 }
 
 namespace {
@@ -644,19 +629,28 @@ int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const 
       return launch_both<__nv_bfloat16>(qd, qx, s);
     });
   }
-  // Neither product fills its last round of SMs (4099 x 2048 x 6144: 2.4 and
-  // 3.5 rounds): the second starts on those that the first leaves, 10 us less for
-  // both (of 95).
-  const bool chained = fp8_one_launch(tokens, inner, outer) &&
-                       fp8_one_launch(outer, inner, tokens);
-  if (e == ROT_OK)
-    e = gemm(chained ? kFirst : kAlone, tokens, inner, outer, d.q, d.ld, ROT_TYPE_E4M3, d.s, d.lds,
-             1, wt, ldwt, wt_format, wt_scale, wt_lds, wt_block_rows, dx, lddx, type, 0, part, more,
-             status, stream);
   if (e != ROT_OK) return e;
-  return gemm(chained ? kSecond : kAlone, outer, inner, tokens, dt.q, dt.ld, ROT_TYPE_E4M3, dt.s,
-              dt.lds, 1, xt.q, xt.ld, ROT_TYPE_E4M3, xt.s, xt.lds, 1, dw, lddw, ROT_TYPE_F32,
-              accumulate, part, more, status, stream);
+  // Neither product fills its last round of SMs (4099 x 2048 x 6144: 2.4 and
+  // 3.5 rounds): in one launch the second starts where the first leaves them.
+  if (fp8_takes_two(tokens, inner, outer, outer, inner, tokens)) {
+    const Prod px = {d.q, (const uint8_t*)wt, d.s, wt_scale, dx, d.ld, ldwt, d.lds, wt_lds, lddx,
+                     (int)tokens, (int)inner, (int)outer, type, 0, 0, wt_format == ROT_TYPE_E5M2,
+                     0, wt_block_rows == 1 ? 0 : 7, nullptr};
+    const Prod pw = {dt.q, xt.q, dt.s, xt.s, dw, dt.ld, xt.ld, dt.lds, xt.lds, lddw,
+                     (int)outer, (int)inner, (int)tokens, ROT_TYPE_F32, accumulate, 0, 0,
+                     0, 0, nullptr};
+    return guarded([&] {
+      return fp8_two_products(px, pw, reinterpret_cast<int*>(status),
+                              static_cast<cudaStream_t>(stream));
+    });
+  }
+  e = rot_fp8_gemm(tokens, inner, outer, d.q, d.ld, ROT_TYPE_E4M3, d.s, d.lds, 1, wt, ldwt,
+                   wt_format, wt_scale, wt_lds, wt_block_rows, dx, lddx, type, 0, part, more, status,
+                   stream);
+  if (e != ROT_OK) return e;
+  return rot_fp8_gemm(outer, inner, tokens, dt.q, dt.ld, ROT_TYPE_E4M3, dt.s, dt.lds, 1, xt.q,
+                      xt.ld, ROT_TYPE_E4M3, xt.s, xt.lds, 1, dw, lddw, ROT_TYPE_F32, accumulate,
+                      part, more, status, stream);
 }
 
 }  // extern "C"

@@ -10,10 +10,6 @@
 namespace rot {
 namespace ops {
 
-// Two products in a row, neither an operand of the other: the first lets the
-// second's CTAs start where its own have ended, and the second ends after it.
-enum { kAlone, kFirst, kSecond };
-
 // C = A B^T (rot_fp8_gemm's checked arguments, K > 0).  The scale of row r and
 // K block j of A is sa[j * ldsa + (r >> ash)].
 struct Prod {
@@ -24,7 +20,6 @@ struct Prod {
   int a5, b5;    // operands in E5M2
   int ash, bsh;  // 0 (a scale per row) or 7 (per 128 rows)
   float* part;   // workspace
-  int chain = kAlone;
 };
 
 // Products with few rows of A (ops_fp8_few.cu): fp8_few where that kernel
@@ -35,9 +30,11 @@ bool fp8_self_rounded(int64_t M, int64_t N, int64_t K);
 int fp8_few_product(const Prod& p, const void* x, int64_t ldx, int32_t xtype, cudaStream_t stream);
 
 uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K);
-// Whether the large kernel takes the product in one launch, without parts.
-bool fp8_one_launch(int64_t M, int64_t N, int64_t K);
 int fp8_product(const Prod& p, int* status, cudaStream_t stream);
+// Two products in one launch of the large kernel, where neither needs parts;
+// neither may be an operand of the other, and the second one's C is float32.
+bool fp8_takes_two(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1);
+int fp8_two_products(const Prod& p, const Prod& q, int* status, cudaStream_t stream);
 
 // The scale's byte for a block whose largest finite magnitude is `amax`: the
 // least e >= -127 with amax <= max 2^e.  max is 1.75 2^top (448: top 8;

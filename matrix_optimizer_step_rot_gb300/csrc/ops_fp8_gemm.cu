@@ -23,6 +23,10 @@
 // Few tiles: K is split over units whose float32 parts go to the workspace and
 // are joined in a fixed order by a second kernel.
 //
+// Two products that do not wait for one another (a layer's gradients) are the
+// units of one launch, the first one's and then the second one's, so that the
+// second starts on the SMs that the first's last round leaves.
+//
 // 8192 x 12288 x 4096: 272 us, 3030 TFLOP/s; 6144 x 2048 x 4099 into float32:
 // 49 us.  Both CTAs of a pair sharing their block of B by TMA multicast sent a
 // third less from L2 and was not faster (279 us).
@@ -30,6 +34,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 #include "ops_fp8.h"
@@ -64,14 +69,20 @@ constexpr int kScaleCols = 12;  // TMEM columns of a stretch's scales: 4 of A, 8
 constexpr int kTmemCols = 512;
 static_assert(2 * BN + kSlots * kScaleCols <= kTmemCols, "TMEM");
 
-struct Mx {
+struct Part {
   CUtensorMap a, b;
   Prod p;
   int tiles_m, tiles_n, kblocks, splits, per;  // per: K blocks of a unit
   int units;
-  void* c;
+  void* c;  // C, or with split K the parts (float32)
   int64_t ldc;
   int accumulate;
+};
+// The products of one launch: the first one's units come first.
+template <int N>
+struct Mx {
+  Part part[N];
+  int units;
   int* status;
   unsigned long long limit_ns;
 };
@@ -84,14 +95,18 @@ struct Mx {
 constexpr int kGroupM = 16;
 
 struct Unit {
-  int m0, n0, k0, k1, split;
+  int m0, n0, k0, k1, split, which;  // which: the product
 };
-__device__ __forceinline__ Unit unit_of(const Mx& g, int u) {
+template <int N>
+__device__ __forceinline__ Unit unit_of(const Mx<N>& all, int u) {
+  Unit t;
+  t.which = N > 1 && u >= all.part[0].units;
+  if (t.which) u -= all.part[0].units;
+  const Part& g = all.part[t.which];
   const int tile = u / g.splits;
   const int per_group = kGroupM * g.tiles_n;
   const int grp = tile / per_group, r = tile - grp * per_group;
   const int h = min(kGroupM, g.tiles_m - grp * kGroupM);
-  Unit t;
   t.split = u - tile * g.splits;
   t.m0 = (grp * kGroupM + r % h) * BM;
   t.n0 = r / h * BN;
@@ -215,9 +230,9 @@ __device__ __forceinline__ void store_tile(uint8_t* stage, T* c, int64_t ldc, in
   __syncwarp();
 }
 
-// C of type T; g.c and g.ldc: C, or with split K the parts (float32).
-template <class T>
-__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Mx g) {
+// C of type T, a second product's of float32.
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Mx<N> g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -236,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   // (the same in every lane, and known to be)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t limit = g.limit_ns;
-  const Prod& p = g.p;
   auto ready = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, abort_flag, limit)) != 0;
   };
@@ -268,10 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  // The operands may come from the kernel before; not those of a product's
-  // second, whose first has waited for them before it let this one start.
-  if (p.chain != kSecond) wait_for_prior();
-  if (p.chain == kFirst) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_prior();  // (the operands may come from the kernel before)
 
   // Warps 0 and 1 run their loops as a whole, with one lane's copies and MMAs
   // in between: operands and addresses stay in uniform registers.  From a
@@ -281,13 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // ------------------------------------------------------------ loads
     const bool one = ptx::elect_one();
     if (one) {
-      ptx::tma_prefetch_desc(&g.a);
-      ptx::tma_prefetch_desc(&g.b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ptx::tma_prefetch_desc(&g.part[i].a);
+        ptx::tma_prefetch_desc(&g.part[i].b);
+      }
     }
     int turn = 0;  // block mod kFulls
     uint32_t phase = 0, armed = 0, armed_parity = 0;  // phase: of full[turn]
     for (int u = blockIdx.x; u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
+      const Part& q = g.part[t.which];
       int kb = t.k0;
       while (kb < t.k1 && !aborted()) {
         const int k1 = min(t.k1, kb + kStretch);
@@ -299,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           uint8_t* st = smem + stage * kStageBytes;
           if (one) {
             ptx::mbar_arrive_expect_tx(&full[turn], kStageBytes);
-            ptx::tma_load_2d(st, &g.a, &full[turn], kb * BK, t.m0);
-            ptx::tma_load_2d(st + kABytes, &g.b, &full[turn], kb * BK, t.n0);
+            ptx::tma_load_2d(st, &q.a, &full[turn], kb * BK, t.m0);
+            ptx::tma_load_2d(st + kABytes, &q.b, &full[turn], kb * BK, t.n0);
           }
           armed |= 1u << turn;
           armed_parity = (armed_parity & ~(1u << turn)) | (phase << turn);
@@ -321,13 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // accumulator: the issue of a block takes one warp longer than its MMAs.
     const int odd = warp >> 1;
     const bool one = ptx::elect_one();
-    const uint32_t idesc = ptx::idesc_mxf8(BM, BN, p.a5, p.b5);
     int block = 0, turn = 0, slot = 0;  // block: mod kFulls; phase: of full[block]
     uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
     const uint32_t d = tmem + (uint32_t)(odd * BN);
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const Unit t = unit_of(g, u);
+      const uint32_t idesc =
+          ptx::idesc_mxf8(BM, BN, g.part[t.which].p.a5, g.part[t.which].p.b5);
       for (int kb = t.k0; kb < t.k1; kb += kStretch) {
         const int n = min(t.k1 - kb, kStretch);
         if (turn == odd) {
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     if (u < g.units) {
       t = unit_of(g, u);
       kb = t.k0;
-      load_scales(p, t, kb, lane, s);
+      load_scales(g.part[t.which].p, t, kb, lane, s);
     }
     while (u < g.units) {
       uint32_t w[10];
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           kb = t.k0;
         }
       }
-      if (u < g.units) load_scales(p, t, kb, lane, s);
+      if (u < g.units) load_scales(g.part[t.which].p, t, kb, lane, s);
       if (!ready(&sempty[slot], phase ^ 1u)) break;
       uint4* q = reinterpret_cast<uint4*>(scales + slot * kScaleBytes);
       q[lane] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -463,12 +479,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
+      const Part& q = g.part[t.which];
       const int row = t.m0 + quarter * 32, n0 = t.n0 + half * kEpiCols;
-      const int rows = p.M - row, cols = p.N - n0;
+      const int rows = q.p.M - row, cols = q.p.N - n0;
       if (!ok || rows <= 0 || cols <= 0) continue;
       uint8_t* stage = staging + (warp - 4) * kStagingBytes;
-      store_tile(stage, static_cast<T*>(g.c) + ((int64_t)t.split * p.M + row) * g.ldc + n0, g.ldc,
-                 rows, cols, sum, g.accumulate);
+      const int64_t at = ((int64_t)t.split * q.p.M + row) * q.ldc + n0;
+      if (N == 1 || std::is_same<T, float>::value || t.which == 0)
+        store_tile(stage, static_cast<T*>(q.c) + at, q.ldc, rows, cols, sum, q.accumulate);
+      else
+        store_tile(stage, static_cast<float*>(q.c) + at, q.ldc, rows, cols, sum, q.accumulate);
     }
   }
 
@@ -478,8 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
   if (threadIdx.x == 0 && *abort_flag && g.status) atomicExch(g.status, ROT_ETIMEOUT);
-  // (what comes after this kernel takes the first product for done, too)
-  if (p.chain == kSecond) wait_for_prior();
 }
 
 // C from the parts, added in order of K.
@@ -558,14 +576,40 @@ int encode(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, int64
   return r == CUDA_SUCCESS ? ROT_OK : ROT_EINVAL;
 }
 
-template <class T>
-int launch_gemm(const Mx& g, cudaStream_t stream) {
+template <class T, int N>
+int launch_gemm(const Mx<N>& g, cudaStream_t stream) {
   static const cudaError_t attr = cudaFuncSetAttribute(
-      fp8_gemm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      fp8_gemm_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (attr != cudaSuccess) return ROT_ECUDA;
-  ProfScope prof(ROT_PROF_GEMM_F8, 2.0 * g.p.M * (double)g.p.N * g.p.K, stream);
-  return launch_behind(fp8_gemm_kernel<T>, (unsigned)std::min(g.units, sm_count()), kThreads, kSmem,
-                       stream, g);
+  double flops = 0.0;
+  for (const Part& q : g.part) flops += 2.0 * q.p.M * (double)q.p.N * q.p.K;
+  ProfScope prof(ROT_PROF_GEMM_F8, flops, stream);
+  return launch_behind(fp8_gemm_kernel<T, N>, (unsigned)std::min(g.units, sm_count()), kThreads,
+                       kSmem, stream, g);
+}
+// ctype: the first product's.
+template <int N>
+int launch_gemm(const Mx<N>& g, int ctype, cudaStream_t stream) {
+  if (ctype == ROT_TYPE_F32) return launch_gemm<float, N>(g, stream);
+  if (ctype == ROT_TYPE_F16) return launch_gemm<__half, N>(g, stream);
+  return launch_gemm<__nv_bfloat16, N>(g, stream);
+}
+
+// A product's part of a launch.
+int part_of(const Prod& p, const Shape& s, Part* g) {
+  if (!encoder()) return ROT_ECUDA;
+  if (s.tiles_m * s.tiles_n * s.splits > 0x7FFFFFFF) return ROT_EINVAL;  // (C beyond any memory)
+  int e = encode(&g->a, p.a, p.M, p.K, p.lda, BM);
+  if (e == ROT_OK) e = encode(&g->b, p.b, p.N, p.K, p.ldb, BN);
+  if (e != ROT_OK) return e;
+  g->p = p;
+  g->tiles_m = (int)s.tiles_m, g->tiles_n = (int)s.tiles_n, g->kblocks = (int)s.kblocks;
+  g->splits = (int)s.splits, g->per = (int)s.per;
+  g->units = (int)(s.tiles_m * s.tiles_n * s.splits);
+  const bool parts = s.splits > 1;
+  g->c = parts ? p.part : p.c, g->ldc = parts ? s.ldp : p.ldc;
+  g->accumulate = !parts && p.accumulate;
+  return ROT_OK;
 }
 
 }  // namespace
@@ -576,37 +620,37 @@ uint64_t fp8_work_bytes(int64_t M, int64_t N, int64_t K) {
   return s.splits > 1 ? align256(4ull * s.splits * M * s.ldp) : 0;
 }
 
-bool fp8_one_launch(int64_t M, int64_t N, int64_t K) {
-  return M > 0 && N > 0 && K > 0 && !fp8_few(M, N, K) && shape_of(M, N, K).splits == 1;
-}
-
 int fp8_product(const Prod& p, int* status, cudaStream_t stream) {
-  if (!encoder()) return ROT_ECUDA;
   const Shape s = shape_of(p.M, p.N, p.K);
-  if (s.tiles_m * s.tiles_n * s.splits > 0x7FFFFFFF) return ROT_EINVAL;  // (C beyond any memory)
-  Mx g;
-  int e = encode(&g.a, p.a, p.M, p.K, p.lda, BM);
-  if (e == ROT_OK) e = encode(&g.b, p.b, p.N, p.K, p.ldb, BN);
+  Mx<1> g;
+  int e = part_of(p, s, &g.part[0]);
   if (e != ROT_OK) return e;
-  g.p = p;
-  g.tiles_m = (int)s.tiles_m, g.tiles_n = (int)s.tiles_n, g.kblocks = (int)s.kblocks;
-  g.splits = (int)s.splits, g.per = (int)s.per;
   const bool parts = s.splits > 1;
-  g.c = parts ? p.part : p.c, g.ldc = parts ? s.ldp : p.ldc, g.accumulate = !parts && p.accumulate;
-  g.units = (int)(s.tiles_m * s.tiles_n * s.splits);
-  g.status = status;
-  g.limit_ns = g_wait_limit_ns;
-  if (parts || p.ctype == ROT_TYPE_F32)
-    e = launch_gemm<float>(g, stream);
-  else if (p.ctype == ROT_TYPE_F16)
-    e = launch_gemm<__half>(g, stream);
-  else
-    e = launch_gemm<__nv_bfloat16>(g, stream);
+  g.units = g.part[0].units, g.status = status, g.limit_ns = g_wait_limit_ns;
+  e = launch_gemm(g, parts ? ROT_TYPE_F32 : p.ctype, stream);
   if (e != ROT_OK || !parts) return e;
   ProfScope prof(ROT_PROF_ELEMENTWISE, 4.0 * (s.splits + 1) * p.M * (double)p.N, stream);
   const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
   return launch_behind(fp8_join_kernel, (unsigned)std::min<int64_t>(blocks, 8ll * sm_count()), 256, 0,
                        stream, p, (int)s.splits, s.ldp);
+}
+
+bool fp8_takes_two(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1) {
+  if (std::min({M0, N0, K0, M1, N1, K1}) <= 0 || fp8_few(M0, N0, K0) || fp8_few(M1, N1, K1))
+    return false;
+  const Shape s = shape_of(M0, N0, K0), t = shape_of(M1, N1, K1);
+  return s.splits == 1 && t.splits == 1 &&
+         s.tiles_m * s.tiles_n + t.tiles_m * t.tiles_n <= 0x7FFFFFFF;
+}
+
+int fp8_two_products(const Prod& p, const Prod& q, int* status, cudaStream_t stream) {
+  Mx<2> g;
+  int e = part_of(p, shape_of(p.M, p.N, p.K), &g.part[0]);
+  if (e == ROT_OK) e = part_of(q, shape_of(q.M, q.N, q.K), &g.part[1]);
+  if (e != ROT_OK) return e;
+  g.units = g.part[0].units + g.part[1].units;
+  g.status = status, g.limit_ns = g_wait_limit_ns;
+  return launch_gemm(g, p.ctype, stream);
 }
 
 }  // namespace ops

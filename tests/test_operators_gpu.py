@@ -867,6 +867,80 @@ def test_linear(tokens, inner, outer, dtype):
     near(twice, 2 * want, 2 * bound + 4 * E * want.abs(), "dw accumulated")
 
 
+def separate_gradients(dy, x, t, dtype):
+    """A layer's gradients as quantisation and two products, one after the other."""
+    d, dt = ops.fp8_quantize(dy, transposed=True)
+    xt = ops.fp8_quantize(x, rows=False, transposed=True)[1]
+    return ops.fp8_matmul(d, t, dtype=dtype), ops.fp8_matmul(dt, xt)
+
+
+# either product's tiles against the 152 SMs: both fewer, the first fewer, the
+# second fewer, both more; cut rows, columns and blocks of K
+PAIRS = [(257, 384, 500), (2500, 200, 2500), (2500, 2500, 200), (300, 4100, 3900), (4099, 2048, 6144),
+         (5001, 1990, 3001), (3000, 2049, 2047)]
+
+
+@pytest.mark.parametrize("tokens,inner,outer", PAIRS)
+@pytest.mark.parametrize("dtype,fmt", [(BF16, E4), (F16, E5), (F32, E4)])
+def test_gradients_are_those_of_the_separate_products(tokens, inner, outer, dtype, fmt):
+    """Bit for bit, with gradients of one call after the other in the same
+    memory, added to, and read by the call that follows."""
+    g = gen(tokens)
+    t = ops.fp8_quantize(torch.randn(outer, inner, generator=g, device="cuda") * 0.02, block_rows=128, rows=False,
+                         transposed=True, dtype=fmt)[1]
+    given = [((torch.randn(tokens, outer, generator=g, device="cuda") * 1e-2).to(dtype),
+              torch.randn(tokens, inner, generator=g, device="cuda").to(dtype)) for _ in range(3)]
+    want = [separate_gradients(dy, x, t, dtype) for dy, x in given]
+    torch.cuda.synchronize()
+    sums = [(dx.double().sum(), dw.double().sum()) for dx, dw in want]
+    for turn in range(4):
+        for (dy, x), (wx, ww), (sx, sw) in zip(given, want, sums):
+            dx, dw = ops.fp8_linear_backward(dy, x, t)
+            seen = dx.double().sum(), dw.double().sum()
+            assert torch.equal(dx, wx) and torch.equal(dw, ww)
+            assert torch.equal(seen[0], sx) and torch.equal(seen[1], sw)
+            del dx, dw, seen
+    total = torch.zeros(outer, inner, device="cuda")
+    add = torch.zeros_like(total)
+    for (dy, x), (_, ww) in zip(given, want):
+        ops.fp8_linear_backward(dy, x, t, dw=total, accumulate=True)
+        add += ww
+    assert torch.equal(total, add)
+    assert ops.status() == B.ROT_OK
+
+
+def test_gradients_in_a_graph():
+    """Both products in one launch, replayed with other inputs, two layers in a row."""
+    tokens, inner, outer = 4099, 2048, 2304
+    g = gen(12)
+    t = ops.fp8_quantize(torch.randn(outer, inner, generator=g, device="cuda") * 0.02, block_rows=128, rows=False,
+                         transposed=True)[1]
+    back = ops.fp8_quantize(torch.randn(inner, outer, generator=g, device="cuda") * 0.02, block_rows=128, rows=False,
+                            transposed=True)[1]
+    dy = torch.randn(tokens, outer, generator=g, device="cuda").to(BF16)
+    x = torch.randn(tokens, inner, generator=g, device="cuda").to(BF16)
+
+    def step():
+        dx, dw = ops.fp8_linear_backward(dy, x, t)
+        return (dx, dw, *ops.fp8_linear_backward(dx, dy, back))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in range(3):
+        dy.copy_(torch.randn(tokens, outer, generator=gen(seed), device="cuda"))
+        x.copy_(torch.randn(tokens, inner, generator=gen(seed + 10), device="cuda"))
+        dx, dw = separate_gradients(dy, x, t, BF16)
+        want = (dx, dw, *separate_gradients(dx, dy, back, BF16))
+        for _ in range(3):
+            for c in captured:
+                c.zero_()
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(want, captured))
+    assert ops.status() == B.ROT_OK
+
+
 def test_layers_of_no_inner_or_outer_features():
     """A last dimension of 0 under any number of leading ones: sums of nothing
     are 0, and the shapes are the leading ones'."""
