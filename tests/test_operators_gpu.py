@@ -242,6 +242,90 @@ def test_layer_norm_backward(rows, cols, dtype, pad, residual, p, wtype, bias):
         assert db is None
 
 
+# Every plan of the norm: rows of single elements by their widths, then those of
+# 16-byte runs; the last of each are too wide for the registers.  The rows are
+# more than four times those that the blocks of the backward pass take at once
+# (152 to 2432).
+PLANS = [  # rows, cols, type, pad
+    (9800, 77, BF16, 0), (9800, 128, F16, 1), (9800, 129, F32, 0), (9800, 199, BF16, 2), (9800, 256, BF16, 3),
+    (4900, 257, F16, 0), (4900, 389, BF16, 0), (4900, 512, F32, 1), (2500, 513, BF16, 0), (2500, 777, F32, 0),
+    (1300, 1025, BF16, 0), (2500, 1325, BF16, 0), (1300, 2047, F32, 2), (1300, 2049, F16, 0), (1300, 3001, BF16, 0),
+    (650, 4097, F32, 0), (650, 6001, BF16, 0), (650, 8191, F16, 0), (270, 8195, BF16, 0),
+    (9800, 264, BF16, 0), (9800, 512, F16, 8), (2500, 1040, BF16, 0), (2500, 516, F32, 0), (1300, 2056, BF16, 8),
+    (1300, 1028, F32, 4), (650, 4104, F16, 0), (650, 2052, F32, 0), (650, 8200, BF16, 0), (650, 4100, F32, 0),
+    (270, 16392, BF16, 0), (270, 8196, F32, 0)]
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("rows,cols,dtype,pad", PLANS)
+def test_layer_norm_plans(rows, cols, dtype, pad, p):
+    test_layer_norm(min(rows, 50), cols, dtype, pad, True, p, F32, True)
+    test_layer_norm(min(rows, 50), cols, dtype, pad, False, p, dtype, False)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("rows,cols,dtype,pad", PLANS)
+def test_layer_norm_backward_plans(rows, cols, dtype, pad, p):
+    """Rows as above.  The columns' sums: 8 rows of a block (or of a share of
+    the columns' own kernel), 4 groups of it, 19 parts and 16 of the join, so
+    that a row lost or taken twice is far beyond the bound."""
+    test_layer_norm_backward(rows, cols, dtype, pad, True, p, F32, True)
+    h, dh, w, _ = norm_inputs(rows, cols, dtype, pad, True, dtype, False, rows + cols)
+    dy = rows_of(gen(7), rows, cols, 1, dtype)
+    _, mean, rstd, _ = ref.norm(h, w, None, 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    hat = (h.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for stream in (None, dh):
+        _, _, dw, db = ops.layer_norm_backward(dy, h, mean, rstd, w, dh=stream, p=p, seed=SEED, offset=OFFSET)
+        dhat = 3 * E * (hat.abs() + (h.double().abs() * rstd.double()[:, None]))
+        sums = (dy.double() * hat).abs().sum(0)
+        bound = (47 * E * sums + (dy.double().abs() * dhat).sum(0)) * 1.01
+        assert bound.max().item() < 0.1  # (a row's share is of the order of 1)
+        near(dw, (dy.double() * hat).sum(0), bound, "dweight")
+        near(db, dy.double().sum(0), 47 * E * dy.double().abs().sum(0) * 1.01, "dbias")
+
+
+@pytest.mark.parametrize("p", [0.0, 0.2])
+@pytest.mark.parametrize("rows,cols,dtype,pad", [
+    (301, 200, BF16, 0), (301, 77, F32, 0), (301, 389, BF16, 0), (301, 1325, F16, 3), (301, 2048, BF16, 0),
+    (161, 6001, BF16, 0), (161, 8200, F16, 0), (161, 8195, F32, 0), (70, 33000, BF16, 0)])
+def test_layer_norm_in_its_inputs_place(rows, cols, dtype, pad, p):
+    """The C entry points: the stream may take x's or the residual's place, the
+    gradients that of the stream's gradient."""
+    code = {F32: B.ROT_TYPE_F32, F16: B.ROT_TYPE_F16, BF16: B.ROT_TYPE_BF16}[dtype]
+    lib, stream, ld = B.lib(), torch.cuda.current_stream().cuda_stream, cols + pad
+    x, res, w, b = norm_inputs(rows, cols, dtype, pad, True, F32, True, 4)
+    res = torch.empty(rows, ld, dtype=dtype, device="cuda")[:, :cols].copy_(res)
+    y, h, mean, rstd = ops.layer_norm(x, w, b, residual=res, p=p, seed=SEED, offset=OFFSET)
+
+    def copied(t):
+        return torch.empty(rows, ld, dtype=dtype, device="cuda")[:, :cols].copy_(t)
+
+    for own in (0, 1):
+        given, y2 = [copied(x), copied(res)], torch.empty_like(y)
+        mean2, rstd2 = torch.empty_like(mean), torch.empty_like(rstd)
+        assert lib.rot_layer_norm_forward(
+            given[0].data_ptr(), ld, given[1].data_ptr(), ld, w.data_ptr(), b.data_ptr(), B.ROT_TYPE_F32,
+            given[own].data_ptr(), ld, y2.data_ptr(), cols, mean2.data_ptr(), rstd2.data_ptr(), rows, cols, code,
+            1e-5, p, SEED, OFFSET, stream) == B.ROT_OK
+        assert torch.equal(given[own], h) and torch.equal(given[1 - own], (res, x)[own])
+        assert torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+    dy, dh = copied(torch.randn(rows, cols, device="cuda")), copied(torch.randn(rows, cols, device="cuda"))
+    dx, dres, dw, db = ops.layer_norm_backward(dy, h, mean, rstd, w, dh=dh, p=p, seed=SEED, offset=OFFSET)
+    need = lib.rot_layer_norm_work_bytes(rows, cols)
+    for own in (0, 1) if p > 0 else (0,):
+        place, other = copied(dh), copied(torch.zeros(rows, cols, device="cuda"))
+        outs = [place, other] if own == 0 else [other, place]
+        work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        dw2, db2 = torch.empty_like(dw), torch.empty_like(db)
+        assert lib.rot_layer_norm_backward(
+            dy.data_ptr(), ld, h.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), w.data_ptr(), B.ROT_TYPE_F32,
+            place.data_ptr(), ld, outs[1].data_ptr() if p > 0 else None, ld, outs[0].data_ptr(), ld, dw2.data_ptr(),
+            db2.data_ptr(), rows, cols, code, p, SEED, OFFSET, work.data_ptr(), need, stream) == B.ROT_OK
+        assert torch.equal(outs[0], dx) and (p == 0 or torch.equal(outs[1], dres))
+        assert torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
 def test_layer_norm_gradient_against_differences():
     """Directional derivatives of the forward kernel: central differences of
     sum(y r) in float32 with step 2^-6.  Rounding: outputs of magnitude <= 8
@@ -400,6 +484,14 @@ def test_policy_loss(tokens, vocab, dtype, pad, masked):
     doubled = ops.policy_loss(z, targets, old, adv, w, ref_logp=r, clip_low=lo, clip_high=hi, kl_coef=kl,
                               grad_scale=4.0)[2]
     near(doubled[~edge], 4 * grad[~edge], 4 * (dgrad + U[dtype] * grad.abs())[~edge] * 1.01 + 4 * TINY[dtype], "scaled")
+
+
+@pytest.mark.parametrize("tokens,vocab,dtype,pad,masked", [
+    (1300, 325, BF16, 0, 0.2), (1300, 2047, F32, 1, 0.2), (2500, 4000, F16, 0, 0.1), (320, 5003, BF16, 5, 0.2),
+    (310, 16384, F32, 0, 0.0), (400, 20000, BF16, 0, 0.2)])
+def test_policy_loss_of_many_short_rows(tokens, vocab, dtype, pad, masked):
+    """Rows of a warp, and of 128 threads."""
+    test_policy_loss(tokens, vocab, dtype, pad, masked)
 
 
 def from_largest(z):
