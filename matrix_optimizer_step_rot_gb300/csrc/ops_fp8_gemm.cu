@@ -28,8 +28,8 @@
 // second starts on the SMs that the first's last round leaves.
 //
 // 8192 x 12288 x 4096: 272 us, 3030 TFLOP/s; 6144 x 2048 x 4099 into float32:
-// 49 us.  Both CTAs of a pair sharing their block of B by TMA multicast sent a
-// third less from L2 and was not faster (279 us).
+// 49 us; with 4099 x 2048 x 6144 into bfloat16 in the same launch 82 us, 101 in
+// two.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -11,9 +11,10 @@ stream (csrc/torch/torch_ops.cpp), or on `stream` (a torch.cuda.Stream: outputs
 and workspaces then belong to it, and the inputs are marked as used on it;
 ordering it after their producers is the caller's).  Tensors are on the current
 device; a tensor of more than two dimensions is rows of its last one.  There is
-no other path than the library's, and no part in torch's autograd: the
-backward functions are calls of their own, as the optimizer step is
-(examples/policy_step.py has them together).  The first 8-bit product on a device
+no other path than the library's, and no part in torch's autograd: results do
+not require gradients, whatever the inputs do, and the backward functions are
+calls of their own, as the optimizer step is (examples/policy_step.py has them
+together).  The first 8-bit product on a device
 allocates its status word: let it run before a stream capture.
 """
 
