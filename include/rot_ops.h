@@ -1,10 +1,12 @@
 /*
  * rot_ops.h - training operators next to the optimizer step: dropout from a
  * counter-based generator, layer norm (with the residual stream and dropout
- * in front of it), the clipped policy loss on logits, and products of 8-bit
- * matrices with power-of-two block scales.  Between them they carry a
- * training step from hidden states to the float32 gradients that rot_step
- * reads.
+ * in front of it), the heads' entry to attention (rotary positions, the norm
+ * of queries and keys), the clipped policy loss on logits, products of 8-bit
+ * matrices with power-of-two block scales, and the step of the parameters
+ * that are not rot_step's matrices (AdamW over many tensors, the gradient's
+ * norm).  Between them they carry a training step from hidden states to the
+ * float32 gradients that rot_step reads, and step the rest.
  *
  * Conventions: those of rot.h (0 or a negative ROT_E* code, caller-owned
  * device memory, work enqueued on `stream` without waiting, nothing
@@ -108,6 +110,82 @@ int rot_layer_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t
                             int64_t lddres, void* dx, int64_t lddx, float* dweight, float* dbias,
                             int64_t rows, int64_t cols, int32_t type, double p, uint64_t seed,
                             uint64_t offset, void* work, uint64_t work_bytes, void* stream);
+
+/* ---- heads: rotary positions, norm of queries and keys -------------------
+ *
+ * Queries and keys lie as [batch][token][head][dim] under any strides (a
+ * part of a fused projection, heads before tokens), a head's elements next to
+ * one another.
+ *
+ * Rotation of the first `rotated` elements of a head by its token's position
+ * p: pair i turns by the angle 2 pi t, t the fractional part of p turns[i] /
+ * 2^64.  The product is exact (modulo 2^64), so that an angle is as good at
+ * position 2^31 as at 1: turns[i] is the part of a turn that one position
+ * adds, to the nearest 2^-64.  With c = magnitude cos, s = magnitude sin:
+ *   a' = a c - b s,  b' = b c + a s
+ * on the pairs (i, i + rotated / 2), or interleaved (2 i, 2 i + 1).  The rest
+ * of the head passes through.  `inverse` turns the other way, with the same
+ * magnitude: the rotation's gradient.
+ *
+ * Norm, per head x with the weight w (dim elements, one for all heads):
+ *   r = 1 / sqrt(sum x^2 / dim + eps),  y = rotation(x r w)
+ * Backward, with g the inverse rotation of dy and hat = x r:
+ *   dx = r (g w - hat mean(g w hat)),  dw = sum over tokens and heads of g hat
+ */
+#define ROT_MAX_HEAD_DIM 512
+
+typedef struct rot_heads {
+  void* data; /* the first head of the first token */
+  int64_t heads;
+  int64_t batch_stride, token_stride, head_stride; /* in elements */
+} rot_heads;
+
+typedef struct rot_rotary {
+  const uint64_t* turns; /* rotated / 2 device words */
+  int64_t rotated;       /* even, 0 to dim */
+  float magnitude;
+  int32_t interleaved;
+  const void* positions;  /* device, of position_bytes (4 or 8, signed); NULL: token t is at start + t */
+  int32_t position_bytes;
+  int64_t position_batch_stride, position_token_stride; /* in positions; 0 shares them */
+  int64_t start;
+} rot_rotary;
+
+/* q_out (and k_out) = the rotation of q (and k) of `type` (F32, F16, BF16).
+ * k and k_out may both be NULL.  An output may be its input (same strides).
+ * batch * tokens <= 2^30, heads <= 2^16.  Strides are not negative; the
+ * outputs' rows must not overlap, the inputs' may (stride 0).
+ * Errors: ROT_EINVAL (sizes out of range, dim outside [1, ROT_MAX_HEAD_DIM],
+ * null pointers, unknown type, outputs with another number of heads or with
+ * rows that overlap, rotated odd, negative or above dim, position_bytes,
+ * magnitude NaN). */
+int rot_rotate(const rot_heads* q, const rot_heads* q_out, const rot_heads* k,
+               const rot_heads* k_out, int64_t batch, int64_t tokens, int64_t dim, int32_t type,
+               const rot_rotary* rotary, int32_t inverse, void* stream);
+
+/* The norm with the rotation behind it; rotary may be NULL (no rotation).
+ * Weights: dim elements of wtype (F32 or `type`).  k, k_weight and k_out may
+ * all be NULL.  An output may be its input.  Squares are float32.
+ * Errors: as rot_rotate, plus eps negative or NaN, wtype. */
+int rot_head_norm_forward(const rot_heads* q, const void* q_weight, const rot_heads* q_out,
+                          const rot_heads* k, const void* k_weight, const rot_heads* k_out,
+                          int32_t wtype, int64_t batch, int64_t tokens, int64_t dim, int32_t type,
+                          float eps, const rot_rotary* rotary, void* stream);
+
+/* Workspace bytes of rot_head_norm_backward (256-byte aligned device memory);
+ * 0 for a dim that it refuses. */
+uint64_t rot_head_norm_work_bytes(int64_t dim);
+
+/* dq_out, dq_weight (dim float32, overwritten) from dq and the forward pass's
+ * q; the same of k where it is given.  dq_out may be dq or q.
+ * Errors: as the forward pass, plus a missing, misaligned or too small
+ * workspace. */
+int rot_head_norm_backward(const rot_heads* dq, const rot_heads* q, const void* q_weight,
+                           const rot_heads* dq_out, float* dq_weight, const rot_heads* dk,
+                           const rot_heads* k, const void* k_weight, const rot_heads* dk_out,
+                           float* dk_weight, int32_t wtype, int64_t batch, int64_t tokens,
+                           int64_t dim, int32_t type, float eps, const rot_rotary* rotary,
+                           void* work, uint64_t work_bytes, void* stream);
 
 /* ---- policy loss ---------------------------------------------------------
  *
@@ -226,6 +304,84 @@ int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const 
                             const uint8_t* wt_scale, int64_t wt_lds, int32_t wt_block_rows,
                             void* dx, int64_t lddx, float* dw, int64_t lddw, int32_t accumulate,
                             void* work, uint64_t work_bytes, int32_t* status, void* stream);
+
+/* ---- AdamW over many tensors ---------------------------------------------
+ *
+ * Per element (decoupled weight decay; Loshchilov and Hutter, "Decoupled
+ * weight decay regularization", ICLR 2019), t the step from 1:
+ *   g = scale grad min(1, max_norm / (|scale| norm))
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in float32, p read from and written to `master` where that is given (p then
+ * receives its value, rounded to nearest).  A norm that is not finite and a
+ * device step below 1 leave every tensor as it was.
+ *
+ * States in 8 bits: m and sqrt(v) as E4M3 numbers, under one power-of-two
+ * scale for every 128 consecutive elements (a byte e for 2^(e - 127), 255 for
+ * NaN; e the least for which all finite elements are within 448 of it).
+ * Rounding is random: an average that moves by 1 - beta2 = 0.001 of the way
+ * each step would stay where it is for good if it were rounded to nearest at
+ * three fraction bits.  With w the generator's word of an element, a number
+ * between two neighbours goes to the upper one where its place between them,
+ * from 0 to 1, plus ((w mod 2^16) + 1/2) / 2^16 is at least 1.  A root above 0
+ * is at least the least number above 0.  NaN and infinities become NaN, in
+ * their own place only.
+ * A bfloat16 p without a master is rounded likewise, by floor(w / 2^16) /
+ * 2^16 (a step of it is often below half of p's last place).
+ * The word of element i of a tensor: word i mod 4 of Philox4x32-10 at the
+ * counter (j low, j high, t low, t high) under the key seed, with j = b / 4 +
+ * floor(i / 4) and b the elements of the tensors before it in the list, each
+ * rounded up to a multiple of 128.  Calls of the same step need seeds of
+ * their own.
+ */
+typedef struct rot_adamw_tensor {
+  void* p;
+  const void* g;
+  void* m; /* float32; or E4M3 where m_scale is given */
+  void* v; /* float32; or E4M3 of the root where v_scale is given */
+  uint8_t *m_scale, *v_scale; /* ceil(n / 128) bytes each, or both NULL */
+  float* master;              /* NULL: p itself (F32 or BF16) */
+  int64_t n;
+  int32_t p_type, g_type; /* ROT_TYPE_F32, F16 or BF16 */
+} rot_adamw_tensor;
+
+typedef struct rot_adamw_hyper {
+  double lr, beta1, beta2, eps, weight_decay, scale, max_norm;
+  int64_t step; /* from 1 */
+  uint64_t seed;
+  const float* lr_device;     /* device word read instead of lr, or NULL */
+  const int64_t* step_device; /* device word read instead of step, or NULL */
+  const float* norm;          /* device word: the norm of all gradients; NULL: no clipping */
+} rot_adamw_hyper;
+
+/* One step of `count` tensors, in place.  Tensors hold n consecutive
+ * elements; pointers are aligned to their elements (16 bytes is best).  The
+ * written arrays must not overlap.  Tensors of no elements are left out.
+ * Errors: ROT_EINVAL (count < 0, n < 0, more than 2^40 elements in all, null
+ * or misaligned pointers, unknown types, one scale without the other, F16
+ * without a master, F32 with one, an array given twice, hyper-parameters that
+ * are negative or NaN, betas not below 1, scale not finite, step < 1, max_norm
+ * not above 0). */
+int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_adamw_hyper* hyper,
+                   void* stream);
+
+/* Workspace bytes of rot_gradient_norm (256-byte aligned device memory). */
+uint64_t rot_gradient_norm_work_bytes(int32_t count);
+
+/* norm (one float32) = sqrt of the sum of the squares of all elements of the
+ * tensors (n consecutive elements of `type` each).  Squares and a block's sums
+ * are float32, the blocks' sum float64: elements near 2^64 give infinity, and
+ * those below 2^-75 count as 0.
+ * Errors: ROT_EINVAL (count < 0, null pointers, n < 0, more than 2^40 elements
+ * in all, misaligned elements, unknown types, workspace). */
+typedef struct rot_gradient {
+  const void* g;
+  int64_t n;
+  int32_t type;
+} rot_gradient;
+int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm, void* work,
+                      uint64_t work_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -50,6 +50,39 @@ class rot_shape(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32)]
 
 
+class rot_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class rot_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotated", ctypes.c_int64),
+                ("magnitude", ctypes.c_float), ("interleaved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("position_bytes", ctypes.c_int32),
+                ("position_batch_stride", ctypes.c_int64),
+                ("position_token_stride", ctypes.c_int64), ("start", ctypes.c_int64)]
+
+
+class rot_adamw_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("p_type", ctypes.c_int32), ("g_type", ctypes.c_int32)]
+
+
+class rot_adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay",
+                                               "scale", "max_norm")] + \
+               [("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p),
+                ("norm", ctypes.c_void_p)]
+
+
+class rot_gradient(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -57,6 +90,9 @@ _u64 = ctypes.c_uint64
 _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 _f64 = ctypes.c_double
+
+_HEADS = ctypes.POINTER(rot_heads)
+_ROTARY = ctypes.POINTER(rot_rotary)
 
 _SIGS = {
     "rot_plan_create": (_i32, [ctypes.POINTER(rot_shape), _i32, _u64, ctypes.POINTER(_vp)]),
@@ -116,6 +152,18 @@ _SIGS = {
     "rot_fp8_linear_backward": (_i32, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64,
                                        _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp,
                                        _u64, _vp, _vp]),
+    "rot_rotate": (_i32, [_HEADS, _HEADS, _HEADS, _HEADS, _i64, _i64, _i64, _i32, _ROTARY, _i32,
+                          _vp]),
+    "rot_head_norm_forward": (_i32, [_HEADS, _vp, _HEADS, _HEADS, _vp, _HEADS, _i32, _i64, _i64,
+                                     _i64, _i32, _f32, _ROTARY, _vp]),
+    "rot_head_norm_work_bytes": (_u64, [_i64]),
+    "rot_head_norm_backward": (_i32, [_HEADS, _HEADS, _vp, _HEADS, _vp, _HEADS, _HEADS, _vp,
+                                      _HEADS, _vp, _i32, _i64, _i64, _i64, _i32, _f32, _ROTARY,
+                                      _vp, _u64, _vp]),
+    "rot_adamw_step": (_i32, [ctypes.POINTER(rot_adamw_tensor), _i32,
+                              ctypes.POINTER(rot_adamw_hyper), _vp]),
+    "rot_gradient_norm_work_bytes": (_u64, [_i32]),
+    "rot_gradient_norm": (_i32, [ctypes.POINTER(rot_gradient), _i32, _vp, _vp, _u64, _vp]),
     "rot_item_work": (_i32, [ctypes.POINTER(rot_shape), _i32, ctypes.POINTER(_u64)]),
     "rot_partition_static": (_i32, [ctypes.POINTER(_u64), _i32, ctypes.POINTER(_i32), _i32, _i32,
                                     ctypes.POINTER(_i32)]),

@@ -38,7 +38,14 @@ namespace {
   X(rot_fp8_linear_work_bytes) \
   X(rot_fp8_linear)           \
   X(rot_fp8_linear_backward_work_bytes) \
-  X(rot_fp8_linear_backward)
+  X(rot_fp8_linear_backward)  \
+  X(rot_rotate)               \
+  X(rot_head_norm_forward)    \
+  X(rot_head_norm_work_bytes) \
+  X(rot_head_norm_backward)   \
+  X(rot_adamw_step)           \
+  X(rot_gradient_norm_work_bytes) \
+  X(rot_gradient_norm)
 
 struct Entries {
 #define X(name) decltype(&::name) name = nullptr;
@@ -420,6 +427,267 @@ std::tuple<Tensor, Tensor> fp8_linear_backward(const Tensor& dy, const Tensor& x
   return {dx, g};
 }
 
+// -------------------------------------------------------------------- heads
+// [batch, tokens, heads, dim] or [tokens, heads, dim], a head's elements next
+// to one another.
+struct Shape {
+  int64_t batch, tokens, dim;
+};
+rot_heads heads_of(const Tensor& t, const char* name, const Tensor& first) {
+  const std::string n = name;
+  if (!t.defined() || !t.is_cuda()) fail(n + ": expected a CUDA tensor");
+  const int64_t d = t.dim();
+  if (&t == &first) {
+    if (type_of(t) < 0) fail(n + ": expected float32, float16 or bfloat16");
+    if (t.get_device() != c10::cuda::current_device()) fail(n + ": not on the current device");
+    if (d != 3 && d != 4) fail(n + ": expected [tokens, heads, dim] or [batch, tokens, heads, dim]");
+  } else if (t.scalar_type() != first.scalar_type() || t.device() != first.device() ||
+             d != first.dim() || t.size(d - 1) != first.size(d - 1) ||
+             t.sizes().slice(0, d - 2) != first.sizes().slice(0, d - 2)) {
+    fail(n + ": expected the first tensor's type, device, tokens and head size");
+  }
+  if (t.size(d - 1) > 1 && t.stride(d - 1) != 1) fail(n + ": its last dimension is not contiguous");
+  rot_heads h;
+  h.data = t.data_ptr();
+  h.heads = t.size(d - 2);
+  h.head_stride = t.stride(d - 2), h.token_stride = t.stride(d - 3);
+  h.batch_stride = d == 4 ? t.stride(0) : 0;
+  return h;
+}
+rot_heads like_heads(const Tensor& t, const char* name, const Tensor& other, const Tensor& first) {
+  if (t.defined() && t.sizes() != other.sizes()) fail(std::string(name) + ": expected the shape of its input");
+  return heads_of(t, name, first);
+}
+Shape shape_of(const Tensor& t) {
+  const int64_t d = t.dim();
+  return {d == 4 ? t.size(0) : 1, t.size(d - 3), t.size(d - 1)};
+}
+
+struct Rotation {
+  rot_rotary r = {};
+  const rot_rotary* p = nullptr;
+};
+Rotation rotation_of(const MaybeTensor& turns, double magnitude, bool interleaved,
+                     const MaybeTensor& positions, int64_t start, const Tensor& q) {
+  Rotation o;
+  if (!turns) return o;
+  if (!turns->defined() || turns->scalar_type() != at::kLong || turns->dim() != 1 ||
+      !turns->is_contiguous() || turns->device() != q.device())
+    fail("rotary: expected contiguous int64 turns on the first tensor's device");
+  o.p = &o.r;
+  o.r.turns = reinterpret_cast<const uint64_t*>(turns->data_ptr());
+  o.r.rotated = 2 * turns->numel();
+  if (o.r.rotated > q.size(q.dim() - 1)) fail("rotary: more pairs than the heads have");
+  o.r.magnitude = (float)magnitude, o.r.interleaved = interleaved, o.r.start = start;
+  if (!positions) return o;
+  const Tensor& p = *positions;
+  if (!p.defined() || (p.scalar_type() != at::kLong && p.scalar_type() != at::kInt) ||
+      p.device() != q.device())
+    fail("positions: expected int64 or int32 on the first tensor's device");
+  const Shape s = shape_of(q);
+  const int64_t d = p.dim();
+  if (d < 1 || d > q.dim() - 2 || p.size(d - 1) != s.tokens || (d == 2 && p.size(0) != s.batch))
+    fail("positions: expected one for each token, or one for each token of a batch entry");
+  o.r.positions = p.data_ptr();
+  o.r.position_bytes = p.scalar_type() == at::kLong ? 8 : 4;
+  o.r.position_token_stride = p.stride(d - 1);
+  o.r.position_batch_stride = d == 2 ? p.stride(0) : 0;
+  return o;
+}
+
+std::tuple<Tensor, MaybeTensor> rotate(const Tensor& q, const MaybeTensor& k, const Tensor& turns,
+                                       double magnitude, bool interleaved,
+                                       const MaybeTensor& positions, int64_t start, bool inverse,
+                                       const MaybeTensor& out, const MaybeTensor& k_out) {
+  const rot_heads a = heads_of(q, "q", q);
+  if (!k && k_out) fail("k_out: there is no k");
+  Tensor y = out ? *out : at::empty(q.sizes(), q.options());
+  const rot_heads b = like_heads(y, "out", q, q);
+  MaybeTensor z;
+  rot_heads c, d;
+  if (k) {
+    c = heads_of(*k, "k", q);
+    z = k_out ? *k_out : at::empty(k->sizes(), k->options());
+    d = like_heads(*z, "k_out", *k, q);
+  }
+  const Rotation r = rotation_of(turns, magnitude, interleaved, positions, start, q);
+  const Shape s = shape_of(q);
+  check(lib.rot_rotate(&a, &b, k ? &c : nullptr, k ? &d : nullptr, s.batch, s.tokens, s.dim,
+                       type_of(q), r.p, inverse, stream()),
+        "rot_rotate");
+  return {y, z};
+}
+
+const void* head_weight(const Tensor& w, const char* name, const Tensor& q) {
+  return vector_of(w, name, q.size(q.dim() - 1), q, at::kFloat, q.scalar_type());
+}
+
+std::tuple<Tensor, MaybeTensor> head_norm(const Tensor& q, const Tensor& q_weight,
+                                          const MaybeTensor& k, const MaybeTensor& k_weight,
+                                          double eps, const MaybeTensor& turns, double magnitude,
+                                          bool interleaved, const MaybeTensor& positions,
+                                          int64_t start, const MaybeTensor& out,
+                                          const MaybeTensor& k_out) {
+  const rot_heads a = heads_of(q, "q", q);
+  if (k.has_value() != k_weight.has_value()) fail("k, k_weight: expected both or neither");
+  if (!k && k_out) fail("k_out: there is no k");
+  const void *w = head_weight(q_weight, "q_weight", q), *v = nullptr;
+  Tensor y = out ? *out : at::empty(q.sizes(), q.options());
+  const rot_heads b = like_heads(y, "out", q, q);
+  MaybeTensor z;
+  rot_heads c, d;
+  if (k) {
+    c = heads_of(*k, "k", q);
+    if (k_weight->scalar_type() != q_weight.scalar_type()) fail("k_weight: expected q_weight's type");
+    v = head_weight(*k_weight, "k_weight", q);
+    z = k_out ? *k_out : at::empty(k->sizes(), k->options());
+    d = like_heads(*z, "k_out", *k, q);
+  }
+  const Rotation r = rotation_of(turns, magnitude, interleaved, positions, start, q);
+  const Shape s = shape_of(q);
+  check(lib.rot_head_norm_forward(&a, w, &b, k ? &c : nullptr, v, k ? &d : nullptr,
+                                  type_of(q_weight), s.batch, s.tokens, s.dim, type_of(q),
+                                  (float)eps, r.p, stream()),
+        "rot_head_norm_forward");
+  return {y, z};
+}
+
+std::tuple<Tensor, MaybeTensor, Tensor, MaybeTensor> head_norm_backward(
+    const Tensor& dq, const Tensor& q, const Tensor& q_weight, const MaybeTensor& dk,
+    const MaybeTensor& k, const MaybeTensor& k_weight, double eps, const MaybeTensor& turns,
+    double magnitude, bool interleaved, const MaybeTensor& positions, int64_t start,
+    const MaybeTensor& out, const MaybeTensor& k_out) {
+  const rot_heads a = heads_of(dq, "dq", dq), b = like_heads(q, "q", dq, dq);
+  if (k.has_value() != k_weight.has_value() || k.has_value() != dk.has_value())
+    fail("dk, k, k_weight: expected all or none");
+  if (!k && k_out) fail("k_out: there is no k");
+  const void *w = head_weight(q_weight, "q_weight", dq), *v = nullptr;
+  Tensor y = out ? *out : at::empty(dq.sizes(), dq.options());
+  const rot_heads o = like_heads(y, "out", dq, dq);
+  Tensor dw = floats({dq.size(dq.dim() - 1)}, dq);
+  MaybeTensor z, dv;
+  rot_heads c, d, p;
+  if (k) {
+    c = heads_of(*dk, "dk", dq), d = like_heads(*k, "k", *dk, dq);
+    if (k_weight->scalar_type() != q_weight.scalar_type()) fail("k_weight: expected q_weight's type");
+    v = head_weight(*k_weight, "k_weight", dq);
+    z = k_out ? *k_out : at::empty(dk->sizes(), dk->options());
+    p = like_heads(*z, "k_out", *dk, dq);
+    dv = floats({dq.size(dq.dim() - 1)}, dq);
+  }
+  const Rotation r = rotation_of(turns, magnitude, interleaved, positions, start, dq);
+  const Shape s = shape_of(dq);
+  const uint64_t need = lib.rot_head_norm_work_bytes(s.dim);
+  Tensor work = bytes(need, dq);
+  check(lib.rot_head_norm_backward(&a, &b, w, &o, dw.data_ptr<float>(), k ? &c : nullptr,
+                                   k ? &d : nullptr, v, k ? &p : nullptr,
+                                   k ? dv->data_ptr<float>() : nullptr, type_of(q_weight), s.batch,
+                                   s.tokens, s.dim, type_of(dq), (float)eps, r.p, work.data_ptr(),
+                                   need, stream()),
+        "rot_head_norm_backward");
+  return {y, z, dw, dv};
+}
+
+// -------------------------------------------------------------------- AdamW
+// The current device, asked for once a tensor is a CUDA tensor.
+struct Current {
+  c10::DeviceIndex index = -1;
+  bool has(const Tensor& t) {
+    if (!t.defined() || !t.is_cuda()) return false;
+    if (index < 0) index = c10::cuda::current_device();
+    return t.get_device() == index;
+  }
+};
+// A flat tensor of a list.
+void* flat(const Tensor& t, const char* name, int64_t n, Current& device) {
+  if (!device.has(t)) fail(std::string(name) + ": expected CUDA tensors on the current device");
+  if (!t.is_contiguous() || t.numel() != n)
+    fail(std::string(name) + ": expected contiguous tensors with as many elements as the parameters");
+  return t.data_ptr();
+}
+template <class T>
+const T* word_of(const MaybeTensor& t, const char* name, at::ScalarType type,
+                 Current& device) {
+  if (!t) return nullptr;
+  if (!device.has(*t) || t->scalar_type() != type || t->numel() != 1)
+    fail(std::string(name) + ": expected one element of the right type on the current device");
+  return t->data_ptr<T>();
+}
+
+void adamw(const std::vector<Tensor>& params, const std::vector<Tensor>& grads,
+           const std::vector<Tensor>& m, const std::vector<Tensor>& v,
+           const std::vector<MaybeTensor>& m_scale, const std::vector<MaybeTensor>& v_scale,
+           const std::vector<MaybeTensor>& masters, int64_t step, const MaybeTensor& step_device,
+           double lr, const MaybeTensor& lr_device, double beta1, double beta2, double eps,
+           double weight_decay, const MaybeTensor& norm, double max_norm, double scale,
+           uint64_t seed) {
+  const size_t n = params.size();
+  if (grads.size() != n || m.size() != n || v.size() != n || m_scale.size() != v_scale.size() ||
+      (!m_scale.empty() && m_scale.size() != n) || (!masters.empty() && masters.size() != n))
+    fail("grads, m, v, masters: expected an entry for each parameter");
+  Current device;
+  std::vector<rot_adamw_tensor> list(n);
+  for (size_t i = 0; i < n; ++i) {
+    rot_adamw_tensor& t = list[i];
+    const int64_t count = params[i].numel();
+    t.p = flat(params[i], "params", count, device);
+    t.g = flat(grads[i], "grads", count, device);
+    t.m = flat(m[i], "m", count, device);
+    t.v = flat(v[i], "v", count, device);
+    t.p_type = type_of(params[i]), t.g_type = type_of(grads[i]);
+    if (t.p_type < 0 || t.g_type < 0)
+      fail("params, grads: expected float32, float16 or bfloat16");
+    if (grads[i].sizes() != params[i].sizes()) fail("grads: expected the parameters' shapes");
+    t.m_scale = t.v_scale = nullptr;
+    t.master = nullptr;
+    const bool eight = !m_scale.empty() && m_scale[i];
+    if (eight != (!v_scale.empty() && v_scale[i])) fail("m, v: one in 8 bits, the other not");
+    const at::ScalarType state = eight ? at::kFloat8_e4m3fn : at::kFloat;
+    if (m[i].scalar_type() != state || v[i].scalar_type() != state)
+      fail("m, v: expected float32 tensors, or Fp8Vectors of float8_e4m3fn");
+    if (eight) {
+      for (const MaybeTensor* s : {&m_scale[i], &v_scale[i]})
+        if ((*s)->scalar_type() != at::kByte) fail("m, v: expected uint8 scales");
+      t.m_scale = static_cast<uint8_t*>(flat(*m_scale[i], "m.scale", up(count, 128), device));
+      t.v_scale = static_cast<uint8_t*>(flat(*v_scale[i], "v.scale", up(count, 128), device));
+    }
+    if (!masters.empty() && masters[i]) {
+      if (masters[i]->scalar_type() != at::kFloat) fail("masters: expected float32 tensors");
+      t.master = static_cast<float*>(flat(*masters[i], "masters", count, device));
+      if (t.p_type == ROT_TYPE_F32) fail("masters: a float32 parameter has none");
+    } else if (t.p_type == ROT_TYPE_F16) {
+      fail("masters: a float16 parameter needs one");
+    }
+    t.n = count;
+  }
+  rot_adamw_hyper h = {};
+  h.lr = lr, h.beta1 = beta1, h.beta2 = beta2, h.eps = eps, h.weight_decay = weight_decay;
+  h.scale = scale, h.max_norm = max_norm, h.step = step, h.seed = seed;
+  h.lr_device = word_of<float>(lr_device, "lr", at::kFloat, device);
+  h.step_device = word_of<int64_t>(step_device, "step", at::kLong, device);
+  h.norm = word_of<float>(norm, "norm", at::kFloat, device);
+  check(lib.rot_adamw_step(list.data(), (int32_t)n, &h, stream()), "rot_adamw_step");
+}
+
+Tensor gradient_norm(const std::vector<Tensor>& grads) {
+  Current device;
+  std::vector<rot_gradient> list(grads.size());
+  for (size_t i = 0; i < grads.size(); ++i) {
+    list[i].g = flat(grads[i], "grads", grads[i].numel(), device);
+    list[i].n = grads[i].numel();
+    list[i].type = type_of(grads[i]);
+    if (list[i].type < 0) fail("grads: expected float32, float16 or bfloat16");
+  }
+  const auto on = at::TensorOptions().device(at::kCUDA, c10::cuda::current_device());
+  Tensor norm = at::empty({}, on.dtype(at::kFloat));
+  const uint64_t need = lib.rot_gradient_norm_work_bytes((int32_t)list.size());
+  Tensor work = at::empty({(int64_t)need}, on.dtype(at::kByte));
+  check(lib.rot_gradient_norm(list.data(), (int32_t)list.size(), norm.data_ptr<float>(),
+                              work.data_ptr(), need, stream()),
+        "rot_gradient_norm");
+  return norm;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_rot_torch, m) {
@@ -433,4 +701,9 @@ PYBIND11_MODULE(_rot_torch, m) {
   m.def("fp8_matmul", &fp8_matmul);
   m.def("fp8_linear", &fp8_linear);
   m.def("fp8_linear_backward", &fp8_linear_backward);
+  m.def("rotate", &rotate);
+  m.def("head_norm", &head_norm);
+  m.def("head_norm_backward", &head_norm_backward);
+  m.def("adamw", &adamw);
+  m.def("gradient_norm", &gradient_norm);
 }

@@ -1,10 +1,12 @@
 """Training operators next to the optimizer step, on torch tensors.
 
 Dropout from a counter-based generator, layer norm with the residual stream and
-dropout in front of it, the clipped policy loss with its gradient, and linear
-layers in 8-bit floating point with power-of-two block scales.  Between them
-they carry a training step from hidden states to the float32 gradients that
-`optimizer.RotatedAdam` reads.  include/rot_ops.h states the formulas, layouts
+dropout in front of it, rotary positions and the norm of queries and keys, the
+clipped policy loss with its gradient, linear layers in 8-bit floating point
+with power-of-two block scales, and AdamW over many tensors with the norm of
+their gradients.  Between them they carry a training step from hidden states to
+the float32 gradients that `optimizer.RotatedAdam` reads, and step the
+parameters that it does not take.  include/rot_ops.h states the formulas, layouts
 and errors.  Every function checks its tensors (ValueError), allocates its
 outputs and workspace with torch and runs the library's kernels on the current
 stream (csrc/torch/torch_ops.cpp), or on `stream` (a torch.cuda.Stream: outputs
@@ -21,8 +23,9 @@ allocates its status word: let it run before a stream capture.
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
-from typing import NamedTuple, Optional, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -94,8 +97,12 @@ def _on(stream, call, *inputs):
     with torch.cuda.stream(stream):
         result = call()
     for t in inputs:
-        for u in (t[:2] if isinstance(t, Fp8Matrix) else (t,)):
-            if u is not None:
+        for u in t if isinstance(t, (tuple, list)) else (t,):
+            if isinstance(u, tuple):
+                for w in u:
+                    if isinstance(w, torch.Tensor):
+                        w.record_stream(stream)
+            elif isinstance(u, torch.Tensor):
                 u.record_stream(stream)
     return result
 
@@ -165,6 +172,144 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, r
     return (_native or _load()).layer_norm_backward(dy, h, mean, rstd, weight, dh, p,
                                                     _word(seed, "seed"), _word(offset, "offset"),
                                                     bias)
+
+
+# ---------------------------------------------------------------------------
+# heads: rotary positions, norm of queries and keys
+# ---------------------------------------------------------------------------
+
+
+class Rotary(NamedTuple):
+    """What the heads of a model are rotated by: `turns` (int64, one for each
+    pair: the part of a turn that a position adds, in units of 2^-64), a factor
+    on the rotated pairs, and whether the pairs are neighbours (2i, 2i + 1) or
+    (i, i + pairs).  A head's elements past the pairs are not rotated."""
+    turns: torch.Tensor
+    magnitude: float = 1.0
+    interleaved: bool = False
+
+
+def rotary_frequencies(rotated: int, base: float = 10000.0, *, factor: float = 1.0,
+                       original_length: Optional[float] = None, low: float = 1.0,
+                       high: float = 4.0, by_index: bool = False) -> torch.Tensor:
+    """Radians that a position adds, for each pair of `rotated` elements
+    (float64): base^(-2i / rotated).  For contexts `factor` times as long: all
+    of them divided by it; or, with the original length, those pairs alone that
+    make at most `low` turns over it, while those of `high` and more keep
+    theirs, with a straight line in between over the turns, or over the pairs'
+    indices (by_index)."""
+    if rotated < 0 or rotated % 2:
+        raise ValueError("rotated: expected an even number of elements")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base, factor: expected numbers above 0")
+    f = base ** (-torch.arange(0, rotated, 2, dtype=torch.float64) / max(rotated, 1))
+    if original_length is None:
+        return f / factor
+    if not 0 < low < high:
+        raise ValueError("low, high: expected 0 < low < high")
+    turns = f * original_length / (2 * math.pi)
+    if by_index:  # (turns fall with the index as a power of the base)
+        keep = torch.log(turns / low) / math.log(high / low)
+    else:
+        keep = (turns - low) / (high - low)
+    keep = keep.clamp(0, 1)
+    return f * (keep + (1 - keep) / factor)
+
+
+def rotary_table(frequencies, *, magnitude: float = 1.0, interleaved: bool = False,
+                 device="cuda") -> Rotary:
+    """A Rotary from radians per position (numbers, or a tensor; float64)."""
+    if isinstance(frequencies, torch.Tensor):
+        frequencies = frequencies.double().tolist()
+    words = []
+    for f in frequencies:
+        x = f / (2 * math.pi)
+        n = round((x - math.floor(x)) * 2.0 ** 64) % (1 << 64)
+        words.append(n - (1 << 64) if n >= 1 << 63 else n)
+    return Rotary(torch.tensor(words, dtype=torch.int64, device=device), magnitude, interleaved)
+
+
+def _rotary(r, required: bool):
+    if r is None and not required:
+        return None, 1.0, False
+    if not isinstance(r, Rotary) or not isinstance(r.turns, torch.Tensor):
+        raise ValueError(f"rotary: expected a Rotary, got {type(r).__name__}")
+    return r
+
+
+def rotate(q: torch.Tensor, rotary: Rotary, k: Optional[torch.Tensor] = None, *,
+           positions: Optional[torch.Tensor] = None, start: int = 0,
+           out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None
+           ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(q, k) turned by their tokens' positions.  [tokens, heads, dim] or
+    [batch, tokens, heads, dim] of any strides (heads before tokens: pass the
+    transposed view), a head's elements next to one another.  positions (int64
+    or int32): one for each token, or [tokens] for all batch entries; without,
+    token t is at start + t.  out, k_out: written instead of new tensors; may be
+    q and k."""
+    if stream is not None:
+        return _on(stream, lambda: rotate(q, rotary, k, positions=positions, start=start, out=out,
+                                          k_out=k_out), q, rotary, k, positions, out, k_out)
+    _tensors(q=q)
+    return (_native or _load()).rotate(q, k, *_rotary(rotary, True), positions, start, False, out,
+                                       k_out)
+
+
+def rotate_backward(dq: torch.Tensor, rotary: Rotary, dk: Optional[torch.Tensor] = None, *,
+                    positions: Optional[torch.Tensor] = None, start: int = 0,
+                    out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gradients of rotate()'s q and k from those of its results: turned
+    back, with the same magnitude."""
+    if stream is not None:
+        return _on(stream, lambda: rotate_backward(dq, rotary, dk, positions=positions,
+                                                   start=start, out=out, k_out=k_out),
+                   dq, rotary, dk, positions, out, k_out)
+    _tensors(dq=dq)
+    return (_native or _load()).rotate(dq, dk, *_rotary(rotary, True), positions, start, True, out,
+                                       k_out)
+
+
+def head_norm(q: torch.Tensor, q_weight: torch.Tensor, k: Optional[torch.Tensor] = None,
+              k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+              rotary: Optional[Rotary] = None, positions: Optional[torch.Tensor] = None,
+              start: int = 0, out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, stream=None
+              ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(q, k), each head x as x / sqrt(mean(x^2) + eps) weight, rotated behind
+    that where `rotary` is given, in one pass.  Layouts, positions and outputs
+    as rotate().  Weights: dim elements, float32 or q's type."""
+    if stream is not None:
+        return _on(stream, lambda: head_norm(q, q_weight, k, k_weight, eps, rotary=rotary,
+                                             positions=positions, start=start, out=out,
+                                             k_out=k_out),
+                   q, q_weight, k, k_weight, rotary, positions, out, k_out)
+    _tensors(q=q, q_weight=q_weight)
+    return (_native or _load()).head_norm(q, q_weight, k, k_weight, eps, *_rotary(rotary, False),
+                                          positions, start, out, k_out)
+
+
+def head_norm_backward(dq: torch.Tensor, q: torch.Tensor, q_weight: torch.Tensor,
+                       dk: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                       rotary: Optional[Rotary] = None, positions: Optional[torch.Tensor] = None,
+                       start: int = 0, out: Optional[torch.Tensor] = None,
+                       k_out: Optional[torch.Tensor] = None, stream=None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor], torch.Tensor,
+                                  Optional[torch.Tensor]]:
+    """(dq, dk, dq_weight, dk_weight) of head_norm from the gradients of its
+    results and its inputs.  The weights' gradients are float32: sums over all
+    tokens and heads.  out, k_out: written instead of new dq and dk; may be the
+    given gradients."""
+    if stream is not None:
+        return _on(stream, lambda: head_norm_backward(dq, q, q_weight, dk, k, k_weight, eps,
+                                                      rotary=rotary, positions=positions,
+                                                      start=start, out=out, k_out=k_out),
+                   dq, q, q_weight, dk, k, k_weight, rotary, positions, out, k_out)
+    _tensors(dq=dq, q=q, q_weight=q_weight)
+    return (_native or _load()).head_norm_backward(dq, q, q_weight, dk, k, k_weight, eps,
+                                                   *_rotary(rotary, False), positions, start, out,
+                                                   k_out)
 
 
 # ---------------------------------------------------------------------------
@@ -301,3 +446,104 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight_t: Fp8Matrix, 
     _tensors(x=x)
     return (_native or _load()).fp8_linear_backward(dy, x, *_fp8(weight_t, "weight_t"), dw,
                                                     accumulate, _status_word(x))
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------
+
+
+class Fp8Vector(NamedTuple):
+    """Elements in 8 bits: `data` (float8_e4m3fn, any shape) under one
+    power-of-two scale (uint8, a byte e for 2^(e - 127), 255 for NaN) for every
+    128 consecutive elements."""
+    data: torch.Tensor
+    scale: torch.Tensor
+
+    def dequantize(self) -> torch.Tensor:
+        """The float32 tensor it stands for (a diagnostic, in torch)."""
+        e = self.scale.int()
+        s = torch.where(e > 0, e << 23, 1 << 22).view(torch.float32)
+        s = torch.where(e == 255, float("nan"), s).repeat_interleave(128)
+        return (self.data.float().flatten() * s[:self.data.numel()]).view(self.data.shape)
+
+
+State = Union[torch.Tensor, Fp8Vector]
+
+
+def adamw_state(param: torch.Tensor, *, bits: int = 32) -> Tuple[State, State]:
+    """(m, v) of a parameter before its first step: zeros, in float32 or (bits
+    8) as Fp8Vectors, v's of its root."""
+    if bits == 32:
+        return (torch.zeros(param.shape, dtype=torch.float32, device=param.device),
+                torch.zeros(param.shape, dtype=torch.float32, device=param.device))
+    if bits != 8:
+        raise ValueError("bits: expected 32 or 8")
+    blocks = -(-param.numel() // 128)
+    return tuple(Fp8Vector(torch.zeros(param.shape, dtype=torch.uint8, device=param.device)
+                           .view(torch.float8_e4m3fn),
+                           torch.zeros(blocks, dtype=torch.uint8, device=param.device))
+                 for _ in range(2))
+
+
+def gradient_norm(grads: Sequence[torch.Tensor], *, stream=None) -> torch.Tensor:
+    """The root of the sum of all elements' squares (float32, on the device):
+    contiguous tensors of any types and shapes, in two launches for up to a
+    thousand of them."""
+    if stream is not None:
+        return _on(stream, lambda: gradient_norm(grads), list(grads))
+    _tensors(**{f"grads[{i}]": g for i, g in enumerate(grads)})
+    return (_native or _load()).gradient_norm(grads)
+
+
+def _states(states: Sequence[State], name: str) -> Tuple[List[torch.Tensor], list]:
+    """The tensors, and the scales of those in 8 bits (none at all: an empty
+    list)."""
+    data, scale = [], []
+    for i, s in enumerate(states):
+        if isinstance(s, Fp8Vector):
+            _tensors(**{f"{name}[{i}].data": s.data, f"{name}[{i}].scale": s.scale})
+            scale += [None] * (i - len(scale)) + [s.scale]
+            data.append(s.data)
+        else:
+            _tensors(**{f"{name}[{i}]": s})
+            data.append(s)
+    return data, scale + [None] * (len(data) - len(scale)) if scale else scale
+
+
+def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequence[State],
+          v: Sequence[State], step, *, lr, beta1: float = 0.9, beta2: float = 0.999,
+          eps: float = 1e-8, weight_decay: float = 0.0,
+          masters: Optional[Sequence[Optional[torch.Tensor]]] = None,
+          norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, scale: float = 1.0,
+          seed: int = 0, stream=None) -> None:
+    """One AdamW step of all `params`, in place, with their states and masters:
+    contiguous tensors of any shapes; float32 (and bfloat16, rounded at random)
+    parameters, or 16-bit ones with a float32 master; gradients of any type;
+    states as adamw_state() makes them.  Gradients are multiplied by `scale`,
+    and clipped to max_norm where `norm` (gradient_norm()'s of them before
+    `scale`) is given; a norm that is not finite leaves everything as it was.
+    step counts from 1; it and lr may be tensors of one element on the device
+    (int64, float32), which a captured call reads when it is replayed.  seed:
+    the random rounding's, whose other half is the step: calls of the same step
+    need different ones.  State and masters that are given twice are refused."""
+    if stream is not None:
+        return _on(stream, lambda: adamw(params, grads, m, v, step, lr=lr, beta1=beta1,
+                                         beta2=beta2, eps=eps, weight_decay=weight_decay,
+                                         masters=masters, norm=norm, max_norm=max_norm,
+                                         scale=scale, seed=seed),
+                   list(params), list(grads), list(m), list(v), masters and list(masters), norm,
+                   step, lr)
+    native = _native or _load()
+    for name, ts in (("params", params), ("grads", grads)):
+        for i, t in enumerate(ts):
+            if not isinstance(t, torch.Tensor):
+                _tensors(**{f"{name}[{i}]": t})
+    md, ms = _states(m, "m")
+    vd, vs = _states(v, "v")
+    if bool(ms) != bool(vs):
+        raise ValueError("m, v: one in 8 bits, the other not")
+    on = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
+    native.adamw(params, grads, md, vd, ms, vs, masters or [], 1 if on[0] else step,
+                 step if on[0] else None, 0.0 if on[1] else lr, lr if on[1] else None, beta1,
+                 beta2, eps, weight_decay, norm, max_norm, scale, _word(seed, "seed"))

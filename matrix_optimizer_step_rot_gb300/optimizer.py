@@ -3,11 +3,12 @@ workspace blobs, stream handles, and exports.  No optimizer arithmetic here."""
 
 from __future__ import annotations
 
-from typing import Sequence, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
 from . import binding as B
+from . import operators as ops
 
 
 class RotatedAdam:
@@ -61,3 +62,48 @@ class RotatedAdam:
 
     def status(self) -> int:
         return B.rot_status(self.plan, self.state.data_ptr(), self._stream())
+
+
+class AdamW:
+    """AdamW over the parameters that RotatedAdam does not take (vectors,
+    embeddings; operators.adamw): keeps their moments and counts the steps.
+
+    bits: 32 or 8, of the moments.  masters: float32 masters of 16-bit
+    parameters (float16 always has one; bfloat16 without is rounded at random).
+    seed: the random rounding's; instances that step in the same run need
+    different ones.  captured: the step's number is kept on the device, so that
+    a captured step() counts on when it is replayed."""
+
+    def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, beta1: float = 0.9,
+                 beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, *,
+                 bits: int = 32, masters: bool = False, seed: int = 0, captured: bool = False):
+        self.params = list(params)
+        states = [ops.adamw_state(p, bits=bits) for p in self.params]
+        self.m, self.v = [s[0] for s in states], [s[1] for s in states]
+        keep = {torch.float16: True, torch.bfloat16: masters}
+        self.masters = [p.float() if keep.get(p.dtype, False) else None for p in self.params]
+        self.lr, self.hyper = lr, dict(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
+        self.seed = seed
+        self.count = 0
+        if captured:
+            device = self.params[0].device if self.params else "cuda"
+            self.count = torch.zeros(1, dtype=torch.int64, device=device)
+
+    def step(self, grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
+             max_norm: float = 1.0, scale: float = 1.0, stream=None) -> None:
+        """One step; norm, max_norm, scale as operators.adamw."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                self.count += 1
+        else:
+            self.count += 1
+        ops.adamw(self.params, grads, self.m, self.v, self.count, lr=self.lr,
+                  masters=self.masters, norm=norm, max_norm=max_norm, scale=scale, seed=self.seed,
+                  stream=stream, **self.hyper)
+
+    def moments(self, item: int) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(m, v) of a parameter in float32."""
+        m, v = self.m[item], self.v[item]
+        if isinstance(m, ops.Fp8Vector):
+            return m.dequantize(), v.dequantize().square()
+        return m.clone(), v.clone()
