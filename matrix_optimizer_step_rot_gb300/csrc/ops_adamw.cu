@@ -2,12 +2,13 @@
 // Bound by HBM: every array is read once and written once.
 //
 // A launch takes a table of tensors as its parameter (nothing is copied to the
-// device, and a captured launch keeps its table).  A block takes kChunk
-// elements of one tensor, found by bisection in the tensors' first chunks.  A
-// warp takes 128 consecutive elements at a time, four to a lane: the elements
-// that share a scale in 8 bits, and one call of the generator to a lane.
+// device, and a captured launch keeps its table).  A block takes a chunk of one
+// tensor, found by bisection in the tensors' first chunks.  A lane takes four
+// or eight consecutive elements: whole calls of the generator, and 16 lanes
+// share a scale.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "ops_common.cuh"
@@ -17,9 +18,15 @@ namespace rot {
 namespace ops {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kAhead = 4;                        // times 128 elements that a warp loads at once
-constexpr int kChunk = kWarps * kAhead * 128;    // elements to a block
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the gradients' squares
+// A block's threads, the elements that a lane takes at once and how often, and
+// the blocks per SM that the registers are made to fit.
+constexpr int threads_of(bool eight) { return eight ? 64 : 256; }
+constexpr int lane_elements(bool eight) { return eight ? 8 : 4; }
+constexpr int times_of(bool eight) { return eight ? 8 : 4; }
+constexpr int chunk_of(bool eight) {
+  return threads_of(eight) * times_of(eight) * lane_elements(eight);
+}
 
 // What is stepped: p itself, rounded at random to bfloat16, or a float32
 // master with p as its 16-bit copy.
@@ -71,60 +78,112 @@ __device__ __forceinline__ int tensor_of(const uint32_t (&first)[CAP], int count
   return lo;
 }
 
-// Four elements from i on, of which `left` are there (the rest 0).
-template <class T>
-__device__ __forceinline__ Run<T, 4> four(const void* p, int64_t i, int left, bool whole) {
-  const T* q = (const T*)p + i;
-  if (whole && left >= 4) return *reinterpret_cast<const Run<T, 4>*>(q);
-  Run<T, 4> r{};
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < left) r.v[k] = q[k];
-  return r;
-}
-template <class T>
-__device__ __forceinline__ void put_four(void* p, int64_t i, int left, bool whole,
-                                         const Run<T, 4>& r) {
-  T* q = (T*)p + i;
-  if (whole && left >= 4) {
-    *reinterpret_cast<Run<T, 4>*>(q) = r;
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < left) q[k] = r.v[k];
+// A block's chunk: its arrays from there on, and how much of them there is (at
+// most a chunk).  The same for every thread, so that an address is a uniform
+// register and 32 bits.
+struct Here {
+  void* p;
+  const void* g;
+  void *m, *v;
+  uint8_t *ms, *vs;
+  float* master;
+  uint64_t word;
+  int32_t n, g_type;
+};
+template <Kept KEPT, bool EIGHT>
+__device__ __forceinline__ Here here_of(const Entry& e, uint32_t chunk) {
+  constexpr int P = KEPT == kF32 ? 4 : 2, S = EIGHT ? 1 : 4;
+  const int64_t at = (int64_t)chunk * chunk_of(EIGHT);
+  Here h;
+  h.p = (char*)e.p + at * P;
+  h.g = (const char*)e.g + at * (e.g_type == ROT_TYPE_F32 ? 4 : 2);
+  h.m = (char*)e.m + at * S, h.v = (char*)e.v + at * S;
+  h.ms = e.ms + at / 128, h.vs = e.vs + at / 128;
+  h.master = e.master + at;
+  h.word = e.word + (uint64_t)at / 4;
+  h.n = (int32_t)min((int64_t)chunk_of(EIGHT), e.n - at);
+  h.g_type = e.g_type;
+  return h;
 }
 
-// Four gradients as they came, of any type.
-struct Raw4 {
-  uint32_t w[4];
+// What a call's constants come to on the device.
+struct Now {
+  float scale, decay, step_size, inv_root;
+  uint64_t t;
+  uint32_t first[3];  // the generator's round 0 with the step and the key worked in
 };
-__device__ __forceinline__ Raw4 four_raw(const Entry& e, int64_t i, int left) {
-  Raw4 r{};
-  if (e.g_type == ROT_TYPE_F32) {
-    const Run<uint32_t, 4> f = four<uint32_t>(e.g, i, left, e.whole);
+
+// N elements of `ES` bytes as they lie in memory, 32 bits at a time.  FULL: all
+// there and reached by accesses of 16 bytes (or all of them), else `left` of
+// them one by one (the rest 0).
+template <int W>
+struct Words {
+  uint32_t w[W];
+};
+template <int ES>
+using Bits = std::conditional_t<ES == 4, uint32_t, std::conditional_t<ES == 2, uint16_t, uint8_t>>;
+
+template <int ES, int N, bool FULL>
+__device__ __forceinline__ Words<N * ES / 4> some(const void* p, uint32_t i, int left) {
+  using T = Bits<ES>;
+  constexpr int W = N * ES / 4;
+  const T* q = (const T*)p + i;
+  Words<W> r;
+  if constexpr (!FULL) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r.w[k] = f.v[k];
+    for (int k = 0; k < W; ++k) r.w[k] = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < left) r.w[k * ES / 4] |= (uint32_t)q[k] << (k * ES % 4 * 8);
+  } else if constexpr (W == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(q);
+    r.w[0] = x.x, r.w[1] = x.y;
   } else {
-    const Run<uint16_t, 4> f = four<uint16_t>(e.g, i, left, e.whole);
-    r.w[0] = f.v[0] | (uint32_t)f.v[1] << 16;
-    r.w[1] = f.v[2] | (uint32_t)f.v[3] << 16;
+    static_assert(W % 4 == 0, "whole accesses");
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      const uint4 x = reinterpret_cast<const uint4*>(q)[k / 4];
+      r.w[k] = x.x, r.w[k + 1] = x.y, r.w[k + 2] = x.z, r.w[k + 3] = x.w;
+    }
   }
   return r;
 }
-__device__ __forceinline__ void floats_of(const Raw4& r, int type, float (&f)[4]) {
-  if (type == ROT_TYPE_F32) {
+template <int ES, int N, bool FULL>
+__device__ __forceinline__ void put_some(void* p, uint32_t i, int left, const Words<N * ES / 4>& r) {
+  using T = Bits<ES>;
+  constexpr int W = N * ES / 4;
+  T* q = (T*)p + i;
+  if constexpr (!FULL) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(r.w[k]);
-  } else if (type == ROT_TYPE_BF16) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      f[k] = __uint_as_float(k & 1 ? r.w[k / 2] & 0xffff0000u : r.w[k / 2] << 16);
+    for (int k = 0; k < N; ++k)
+      if (k < left) q[k] = (T)(r.w[k * ES / 4] >> (k * ES % 4 * 8));
+  } else if constexpr (W == 2) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(r.w[0], r.w[1]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      f[k] = __half2float(__ushort_as_half((unsigned short)(r.w[k / 2] >> (k & 1 ? 16 : 0))));
+    for (int k = 0; k < W; k += 4)
+      reinterpret_cast<uint4*>(q)[k / 4] =
+          make_uint4(r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
   }
+}
+__device__ __forceinline__ float2 f32_pair(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+template <int N>
+__device__ __forceinline__ Words<N> words_of(const float2 (&x)[N / 2]) {
+  Words<N> r;
+#pragma unroll
+  for (int k = 0; k < N / 2; ++k)
+    r.w[2 * k] = __float_as_uint(x[k].x), r.w[2 * k + 1] = __float_as_uint(x[k].y);
+  return r;
+}
+
+// 16-bit numbers in pairs.
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 f16_pair(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 // ---- 8 bits ----
@@ -133,69 +192,96 @@ __device__ __forceinline__ void floats_of(const Raw4& r, int type, float (&f)[4]
 __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 1u << 22 : byte == 255 ? 0x7fc00000u : byte << 23);
 }
-__device__ __forceinline__ void values8(uint32_t q, float scale, float (&f)[4]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(h)
-        : "r"(k ? q >> 16 : q & 0xffffu));
-    f[2 * k] = __half2float(__ushort_as_half((unsigned short)h)) * scale;
-    f[2 * k + 1] = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * scale;
-  }
+// Four E4M3 numbers.
+__device__ __forceinline__ void numbers8(uint32_t q, float2& a, float2& b) {
+  uint32_t h, k;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(h), "=r"(k)
+      : "r"(q));
+  a = f16_pair(h), b = f16_pair(k);
 }
 
-// Four numbers of a warp's 128 in E4M3, rounded by each one's 16 random bits
-// (the low half of its word), and the scale byte.  root: nothing above 0
-// becomes 0.
-//
-// A number's bits times 2^-120 as float32 are E4M3's above 20 more (their
-// least exponents meet there, below it both count in fixed steps), so that an
-// addition to the bits and a shift round it at any size.
+// The largest of three sizes; NaN if there is one.
+__device__ __forceinline__ float top_of(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float top_of(const float2 (&x)[4]) {
+  return top_of(top_of(top_of(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x),
+                top_of(x[2].y, x[3].x, x[3].y), 0.f);
+}
+
+// The scale byte for a largest size of these bits, 8 more than it (0 below
+// that): size = (1 + f) 2^(t - 127) <= 448 2^(byte - 127), 448 = 1.75 2^8.
+// 255 and more: NaN or infinity.
+__device__ __forceinline__ uint32_t byte8_of(uint32_t size) { return (size + 0x1fffffu) >> 23; }
+
+// A number in E4M3, in the upper byte, rounded by `part` (its 16 random bits 4
+// up, and 8 for the half).  y: the number under its scale, times 2^-120: its
+// bits as float32 are E4M3's above 20 more (their least exponents meet there,
+// below it both count in fixed steps), so that an addition to the bits and a
+// shift round it at any size.  ROOT: x is not negative, and not rounded to 0
+// where it is not 0 (its bits are then above 2^20).
 template <bool ROOT>
-__device__ __forceinline__ uint32_t rounded8(const float (&x)[4], const uint32_t (&word)[4],
-                                             uint32_t& byte) {
-  uint32_t b[4], top = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    b[k] = __float_as_uint(x[k]);
-    top = max(top, b[k] & 0x7fffffffu);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const bool odd = top >= 0x7f800000u;  // NaN or infinity among the 128
-  if (odd) {
-    top = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t a = b[k] & 0x7fffffffu;
-      if (a < 0x7f800000u) top = max(top, a);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-  }
-  // top = (1 + f) 2^(t - 127) <= 448 2^(byte - 127), 448 = 1.75 2^8
-  const int t = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
-  byte = (uint32_t)max(t, 0);
-  const float back = __uint_as_float((254u - byte) << 23);
-  uint32_t out = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t y = __float_as_uint(x[k] * back * 0x1p-120f);
-    const uint32_t s = y + ((word[k] & 0xffffu) << 4) + 8u;
-    uint32_t code = s >> 20 & 0x7fu;
-    if (ROOT) code = max(code, (uint32_t)(x[k] > 0.f));
-    code |= y >> 24 & 0x80u;
-    if (odd && (b[k] & 0x7fffffffu) >= 0x7f800000u) code = 0x7fu;
-    out |= code << (8 * k);
-  }
-  return out;
+__device__ __forceinline__ uint32_t code8(float x, float y, uint32_t part) {
+  const uint32_t b = __float_as_uint(y);
+  if constexpr (ROOT) return __viaddmax_u32(b, part, min(__float_as_uint(x), 1u << 20)) << 4;
+  return ((b + part) << 4 & 0x7fffffffu) | (b & 0x80000000u);
+}
+__device__ __forceinline__ uint32_t packed8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x73), __byte_perm(c, d, 0x73), 0x5410);
 }
 
-__device__ __forceinline__ void words_of(const Hyper& h, uint64_t counter, uint64_t offset,
-                                         uint32_t (&w)[4]) {
-  uint32_t c0 = (uint32_t)counter, c1 = (uint32_t)(counter >> 32);
-  uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+// Eight numbers of a half warp's 128 in E4M3.
+template <bool ROOT>
+__device__ __forceinline__ uint2 rounded8(const float2 (&x)[4], const uint32_t (&part)[8],
+                                          uint32_t byte) {
+  const float2 back = both(__uint_as_float((134u - byte) << 23));
+  uint32_t c[8];
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
+  for (int k = 0; k < 4; ++k) {
+    const float2 y = mul2(x[k], back);
+    c[2 * k] = code8<ROOT>(x[k].x, y.x, part[2 * k]);
+    c[2 * k + 1] = code8<ROOT>(x[k].y, y.y, part[2 * k + 1]);
+  }
+  return make_uint2(packed8(c[0], c[1], c[2], c[3]), packed8(c[4], c[5], c[6], c[7]));
+}
+// The same where there is a NaN or an infinity among the 128 or their scale is
+// large (2^(127 - byte) 2^-120 is no normal number).
+template <bool ROOT>
+__device__ __noinline__ uint3 rounded8_any(float2 x0, float2 x1, float2 x2, float2 x3, uint4 p0,
+                                           uint4 p1) {
+  const float x[8] = {x0.x, x0.y, x1.x, x1.y, x2.x, x2.y, x3.x, x3.y};
+  const uint32_t part[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t a = __float_as_uint(x[k]) & 0x7fffffffu;
+    if (a < 0x7f800000u) top = max(top, a);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+  const uint32_t byte = (uint32_t)max((int)byte8_of(top) - 8, 0);
+  uint32_t c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float y = x[k] * __uint_as_float((254u - byte) << 23) * 0x1p-120f;
+    c[k] = (__float_as_uint(x[k]) & 0x7fffffffu) < 0x7f800000u ? code8<ROOT>(x[k], y, part[k])
+                                                               : 0x7f000000u;
+  }
+  return make_uint3(packed8(c[0], c[1], c[2], c[3]), packed8(c[4], c[5], c[6], c[7]), byte);
+}
+
+__device__ __forceinline__ void random_of(const Hyper& h, const Now& c, uint64_t counter,
+                                          uint32_t* w) {
+  const uint2 a0 = mul_wide((uint32_t)counter, kPhiloxM0);
+  uint32_t c0 = c.first[0] ^ (uint32_t)(counter >> 32), c1 = c.first[1];
+  uint32_t c2 = a0.y ^ c.first[2], c3 = a0.x;
+#pragma unroll
+  for (int r = 1; r < 10; ++r) {
     const uint2 a = mul_wide(c0, kPhiloxM0), b = mul_wide(c2, kPhiloxM1);
     c0 = b.y ^ c1 ^ h.key[r][0];
     c1 = b.x;
@@ -205,140 +291,236 @@ __device__ __forceinline__ void words_of(const Hyper& h, uint64_t counter, uint6
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
 
-template <Kept KEPT>
-struct Stepped {
-  using T = float;
-};
-template <>
-struct Stepped<kBf16Random> {
-  using T = uint16_t;
+__device__ __forceinline__ float root(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A lane's elements of one turn as they lie in memory.
+template <Kept KEPT, bool EIGHT, bool WIDE>
+struct Raw {
+  static constexpr int N = lane_elements(EIGHT);
+  static constexpr int G = WIDE ? 4 : 2, P = KEPT == kBf16Random ? 2 : 4, S = EIGHT ? 1 : 4;
+  Words<N * G / 4> g;
+  Words<N * P / 4> p;
+  Words<N * S / 4> m, v;
+  uint32_t sm, sv;  // (8 bits: the scales' bytes)
+
+  template <bool FULL>
+  __device__ __forceinline__ void load(const Here& e, uint32_t i, int left) {
+    g = some<G, N, FULL>(e.g, i, left);
+    p = some<P, N, FULL>(KEPT >= kBf16Master ? (const void*)e.master : e.p, i, left);
+    m = some<S, N, FULL>(e.m, i, left);
+    v = some<S, N, FULL>(e.v, i, left);
+    if constexpr (EIGHT) {
+      sm = FULL || left > 0 ? e.ms[i >> 7] : 0u;
+      sv = FULL || left > 0 ? e.vs[i >> 7] : 0u;
+    }
+  }
 };
 
-template <Kept KEPT, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> a) {
-  using P = typename Stepped<KEPT>::T;
+// A lane's N elements from i on: one step, and the results stored.
+template <Kept KEPT, bool EIGHT, bool WIDE, bool FULL>
+__device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const Here& e,
+                                          const Raw<KEPT, EIGHT, WIDE>& raw, uint32_t i, int left) {
+  constexpr int N = lane_elements(EIGHT), H = N / 2;
   constexpr bool kWords = EIGHT || KEPT == kBf16Random;
-  const Hyper& h = a.h;
-  const Entry& e = a.e[tensor_of(a.first, a.count, blockIdx.x)];
-  const int64_t start =
-      (int64_t)(blockIdx.x - a.first[&e - a.e]) * kChunk + (threadIdx.x >> 5) * 128;
-  const int lane = threadIdx.x & 31;
-  void* const at = KEPT >= kBf16Master ? (void*)e.master : e.p;
-  Raw4 rg[kAhead];
-  Run<P, 4> rp[kAhead];
-  Run<float, 4> rm[EIGHT ? 1 : kAhead], rv[EIGHT ? 1 : kAhead];
-  uint32_t qm[EIGHT ? kAhead : 1], qv[EIGHT ? kAhead : 1];
-  uint32_t sm[EIGHT ? kAhead : 1], sv[EIGHT ? kAhead : 1];
+  float2 g[H], m[H], v[H], r[H], p[H];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int64_t i = start + k * kWarps * 128 + lane * 4;
-    const int left = (int)max((int64_t)0, min((int64_t)4, e.n - i));
-    rg[k] = four_raw(e, i, left);
-    rp[k] = four<P>(at, i, left, e.whole);
-    if constexpr (EIGHT) {
-      const Run<uint8_t, 4> x = four<uint8_t>(e.m, i, left, e.whole);
-      const Run<uint8_t, 4> y = four<uint8_t>(e.v, i, left, e.whole);
-      qm[k] = x.v[0] | x.v[1] << 8 | x.v[2] << 16 | (uint32_t)x.v[3] << 24;
-      qv[k] = y.v[0] | y.v[1] << 8 | y.v[2] << 16 | (uint32_t)y.v[3] << 24;
-      sm[k] = left > 0 ? e.ms[i / 128] : 0u;
-      sv[k] = left > 0 ? e.vs[i / 128] : 0u;
-    } else {
-      rm[k] = four<float>(e.m, i, left, e.whole);
-      rv[k] = four<float>(e.v, i, left, e.whole);
+  for (int k = 0; k < H; ++k) {
+    if constexpr (WIDE)
+      g[k] = f32_pair(raw.g.w[2 * k], raw.g.w[2 * k + 1]);
+    else
+      g[k] = bf16_pair(raw.g.w[k]);
+    if constexpr (KEPT == kBf16Random)
+      p[k] = bf16_pair(raw.p.w[k]);
+    else
+      p[k] = f32_pair(raw.p.w[2 * k], raw.p.w[2 * k + 1]);
+    if constexpr (!EIGHT) {
+      m[k] = f32_pair(raw.m.w[2 * k], raw.m.w[2 * k + 1]);
+      v[k] = f32_pair(raw.v.w[2 * k], raw.v.w[2 * k + 1]);
     }
   }
-  float scale = h.scale;
-  if (h.norm) {
-    const float norm = fabsf(scale) * *h.norm;
-    if (!isfinite(norm)) return;  // (the same for every thread)
-    if (norm > h.max_norm) scale *= h.max_norm / norm;
+  if constexpr (!WIDE) {
+    if (e.g_type == ROT_TYPE_F16) {  // (the same for every thread)
+#pragma unroll
+      for (int k = 0; k < H; ++k) g[k] = f16_pair(raw.g.w[k]);
+    }
   }
-  float decay = h.decay, step_size = h.step_size, inv_root = h.inv_root;
-  uint64_t t = h.step;
+  float ms = h.beta1;
+  if constexpr (EIGHT) {
+    ms *= scale_of(raw.sm);
+    const float2 vs = both(scale_of(raw.sv));
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      numbers8(raw.m.w[k], m[2 * k], m[2 * k + 1]);
+      numbers8(raw.v.w[k], v[2 * k], v[2 * k + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < H; ++k) v[k] = mul2(v[k], vs), v[k] = mul2(v[k], v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    g[k] = mul2(g[k], both(c.scale));
+    m[k] = fma2(m[k], both(ms), mul2(g[k], both(h.rest1)));
+    v[k] = fma2(v[k], both(h.beta2), mul2(mul2(g[k], both(h.rest2)), g[k]));
+    r[k] = make_float2(root(v[k].x), root(v[k].y));
+    const float2 under = fma2(r[k], both(c.inv_root), both(h.eps));
+    const float2 u = mul2(m[k], both(-c.step_size));
+    p[k] = fma2(u, make_float2(inverse(under.x), inverse(under.y)), mul2(p[k], both(c.decay)));
+  }
+  uint32_t w[N];
+  if constexpr (kWords) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) random_of(h, c, e.word + ((i >> 2) + k), w + 4 * k);
+  }
+  if constexpr (EIGHT) {
+    uint32_t part[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[k] = (w[k] & 0xffffu) * 16u + 8u;
+    uint32_t t = byte8_of(__float_as_uint(top_of(m))) | byte8_of(__float_as_uint(top_of(r))) << 16;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+    const uint32_t tm = t & 0xffffu, tv = t >> 16;
+    uint32_t bm, bv;
+    uint2 nm, nv;
+    if (max(tm, tv) <= 133 + 8) {  // (the same for a half warp)
+      bm = (uint32_t)max((int)tm - 8, 0), bv = (uint32_t)max((int)tv - 8, 0);
+      nm = rounded8<false>(m, part, bm), nv = rounded8<true>(r, part, bv);
+    } else {
+      const uint4 p0 = make_uint4(part[0], part[1], part[2], part[3]);
+      const uint4 p1 = make_uint4(part[4], part[5], part[6], part[7]);
+      const uint3 am = rounded8_any<false>(m[0], m[1], m[2], m[3], p0, p1);
+      const uint3 av = rounded8_any<true>(r[0], r[1], r[2], r[3], p0, p1);
+      nm = make_uint2(am.x, am.y), bm = am.z;
+      nv = make_uint2(av.x, av.y), bv = av.z;
+    }
+    put_some<1, 8, FULL>(e.m, i, left, {{nm.x, nm.y}});
+    put_some<1, 8, FULL>(e.v, i, left, {{nv.x, nv.y}});
+    if ((threadIdx.x & 15) == 0 && (FULL || left > 0))
+      e.ms[i >> 7] = (uint8_t)bm, e.vs[i >> 7] = (uint8_t)bv;
+  } else {
+    put_some<4, N, FULL>(e.m, i, left, words_of<N>(m));
+    put_some<4, N, FULL>(e.v, i, left, words_of<N>(v));
+  }
+  if constexpr (KEPT == kBf16Random) {
+    // (a NaN stays one without an addition to its bits, as infinity does)
+    float top = top_of(p[0].x, p[0].y, 0.f);
+#pragma unroll
+    for (int k = 1; k < H; ++k) top = top_of(p[k].x, p[k].y, top);
+    const bool odd = !(top < __int_as_float(0x7f800000));
+    Words<H> q;
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      const uint32_t a = __float_as_uint(p[k].x), b = __float_as_uint(p[k].y);
+      q.w[k] = __byte_perm(a + (w[2 * k] >> 16), b + (w[2 * k + 1] >> 16), 0x7632);
+    }
+    if (odd) {
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const bool fx = fabsf(p[k].x) < __int_as_float(0x7f800000);
+        const bool fy = fabsf(p[k].y) < __int_as_float(0x7f800000);
+        q.w[k] = __byte_perm(__float_as_uint(p[k].x) + (fx ? w[2 * k] >> 16 : 0u),
+                           __float_as_uint(p[k].y) + (fy ? w[2 * k + 1] >> 16 : 0u), 0x7632);
+      }
+    }
+    put_some<2, N, FULL>(e.p, i, left, q);
+  } else if constexpr (KEPT == kF32) {
+    put_some<4, N, FULL>(e.p, i, left, words_of<N>(p));
+  } else {
+    put_some<4, N, FULL>(e.master, i, left, words_of<N>(p));
+    Words<H> q;
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      if constexpr (KEPT == kBf16Master) {
+        const __nv_bfloat162 x = __float22bfloat162_rn(p[k]);
+        q.w[k] = *reinterpret_cast<const uint32_t*>(&x);
+      } else {
+        const __half2 x = __float22half2_rn(p[k]);
+        q.w[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+    put_some<2, N, FULL>(e.p, i, left, q);
+  }
+}
+
+// A warp's turns from its lane's element i on: `full` of them whole (and every
+// array reached by vector accesses), and what is left of its share.
+template <Kept KEPT, bool EIGHT, bool WIDE>
+__device__ __forceinline__ void step_warp(const Hyper& h, const Now& c, const Here& e, uint32_t i,
+                                          int full) {
+  constexpr int N = lane_elements(EIGHT), kStep = 32 * N, kTimes = times_of(EIGHT);
+  const uint32_t end = i + kTimes * kStep;
+  if (EIGHT || full < kTimes) {  // the next turn's elements are on their way meanwhile
+    Raw<KEPT, EIGHT, WIDE> a, b;
+    if (full > 0) a.template load<true>(e, i, N);
+#pragma unroll 1
+    while (full > 0) {
+      if (full > 1) b.template load<true>(e, i + kStep, N);
+      step_lane<KEPT, EIGHT, WIDE, true>(h, c, e, a, i, N);
+      i += kStep;
+      if (--full == 0) break;
+      if (full > 1) a.template load<true>(e, i + kStep, N);
+      step_lane<KEPT, EIGHT, WIDE, true>(h, c, e, b, i, N);
+      i += kStep;
+      --full;
+    }
+  } else {  // all turns' elements first
+    Raw<KEPT, EIGHT, WIDE> raw[kTimes];
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k) raw[k].template load<true>(e, i + k * kStep, N);
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k, i += kStep)
+      step_lane<KEPT, EIGHT, WIDE, true>(h, c, e, raw[k], i, N);
+  }
+#pragma unroll 1
+  for (; i < end; i += kStep) {
+    const int left = max(0, min(N, e.n - (int)i));
+    if (!__any_sync(0xffffffffu, left > 0)) return;
+    Raw<KEPT, EIGHT, WIDE> raw;
+    raw.template load<false>(e, i, left);
+    step_lane<KEPT, EIGHT, WIDE, false>(h, c, e, raw, i, left);
+  }
+}
+
+template <Kept KEPT, bool EIGHT, int CAP>
+__global__ void __launch_bounds__(threads_of(EIGHT), EIGHT ? 11 : 2)
+    adamw_kernel(const __grid_constant__ Table<CAP> a) {
+  const Hyper& h = a.h;
+  const int of = tensor_of(a.first, a.count, blockIdx.x);
+  const Here e = here_of<KEPT, EIGHT>(a.e[of], blockIdx.x - a.first[of]);
+  Now c = {h.scale, h.decay, h.step_size, h.inv_root, h.step, {}};
+  if (h.norm) {
+    const float norm = fabsf(c.scale) * *h.norm;
+    if (!isfinite(norm)) return;
+    if (norm > h.max_norm) c.scale *= h.max_norm / norm;
+  }
   if (h.lr_device || h.step_device) {
     const float lr = h.lr_device ? *h.lr_device : h.lr;
-    if (h.step_device) t = (uint64_t)*h.step_device;
-    if ((int64_t)t < 1) return;
+    if (h.step_device) c.t = (uint64_t)*h.step_device;
+    if ((int64_t)c.t < 1) return;
     // 1 - beta^t = -(e^(t log beta) - 1)
-    step_size = lr / -expm1f((float)(int64_t)t * h.log1);
-    inv_root = 1.f / sqrtf(-expm1f((float)(int64_t)t * h.log2));
-    decay = 1.f - lr * h.weight_decay;
+    c.step_size = lr / -expm1f((float)(int64_t)c.t * h.log1);
+    c.inv_root = 1.f / sqrtf(-expm1f((float)(int64_t)c.t * h.log2));
+    c.decay = 1.f - lr * h.weight_decay;
   }
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int64_t i = start + k * kWarps * 128 + lane * 4;
-    const int left = (int)max((int64_t)0, min((int64_t)4, e.n - i));
-    if (i - lane * 4 >= e.n) break;  // (the same for a warp)
-    float g[4], m[4], v[4], r[4], p[4];
-    floats_of(rg[k], e.g_type, g);
-    if constexpr (EIGHT) {
-      values8(qm[k], scale_of(sm[k]), m);
-      values8(qv[k], scale_of(sv[k]), v);
-    }
-    uint32_t w[4];
-    if constexpr (kWords) words_of(h, e.word + (uint64_t)i / 4, t, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (!EIGHT) m[j] = rm[k].v[j], v[j] = rv[k].v[j];
-      if constexpr (KEPT == kBf16Random)
-        p[j] = __uint_as_float((uint32_t)rp[k].v[j] << 16);
-      else
-        p[j] = rp[k].v[j];
-      if constexpr (EIGHT) v[j] = __fmul_rn(v[j], v[j]);
-      g[j] = __fmul_rn(g[j], scale);
-      // (products and sums rounded one by one: the 8-bit scales' borders are
-      // then where the formula's float32 steps put them)
-      m[j] = __fadd_rn(__fmul_rn(h.beta1, m[j]), __fmul_rn(h.rest1, g[j]));
-      v[j] = __fadd_rn(__fmul_rn(h.beta2, v[j]), __fmul_rn(__fmul_rn(h.rest2, g[j]), g[j]));
-      r[j] = __fsqrt_rn(v[j]);
-      p[j] = p[j] * decay - __fdividef(step_size * m[j], r[j] * inv_root + h.eps);
-    }
-    if constexpr (EIGHT) {
-      uint32_t bm, bv;
-      const uint32_t nm = rounded8<false>(m, w, bm), nv = rounded8<true>(r, w, bv);
-      Run<uint8_t, 4> x, y;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x.v[j] = (uint8_t)(nm >> 8 * j), y.v[j] = (uint8_t)(nv >> 8 * j);
-      put_four<uint8_t>(e.m, i, left, e.whole, x);
-      put_four<uint8_t>(e.v, i, left, e.whole, y);
-      if (lane == 0) e.ms[i / 128] = (uint8_t)bm, e.vs[i / 128] = (uint8_t)bv;
-    } else {
-      Run<float, 4> x, y;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x.v[j] = m[j], y.v[j] = v[j];
-      put_four<float>(e.m, i, left, e.whole, x);
-      put_four<float>(e.v, i, left, e.whole, y);
-    }
-    if constexpr (KEPT == kBf16Random) {
-      Run<uint16_t, 4> o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = __float_as_uint(p[j]);
-        const bool fine = (bits & 0x7fffffffu) < 0x7f800000u;
-        // (not finite: to nearest, which keeps a NaN one)
-        o.v[j] = fine ? (uint16_t)((bits + (w[j] >> 16)) >> 16)
-                      : __bfloat16_as_ushort(__float2bfloat16_rn(p[j]));
-      }
-      put_four<uint16_t>(e.p, i, left, e.whole, o);
-    } else {
-      Run<float, 4> o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o.v[j] = p[j];
-      put_four<float>(at, i, left, e.whole, o);
-      if constexpr (KEPT == kBf16Master) {
-        Run<__nv_bfloat16, 4> c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c.v[j] = __float2bfloat16_rn(p[j]);
-        put_four<__nv_bfloat16>(e.p, i, left, e.whole, c);
-      } else if constexpr (KEPT == kF16Master) {
-        Run<__half, 4> c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c.v[j] = __float2half_rn(p[j]);
-        put_four<__half>(e.p, i, left, e.whole, c);
-      }
-    }
-  }
+  const uint2 b = mul_wide((uint32_t)c.t, kPhiloxM1);
+  c.first[0] = b.y ^ h.key[0][0], c.first[1] = b.x;
+  c.first[2] = (uint32_t)(c.t >> 32) ^ h.key[0][1];
+  constexpr int kStep = 32 * lane_elements(EIGHT), kTimes = times_of(EIGHT);
+  const int begin = (threadIdx.x >> 5) * (kTimes * kStep);
+  const int full = a.e[of].whole ? max(0, min(kTimes, (e.n - begin) / kStep)) : 0;
+  const uint32_t i = begin + (threadIdx.x & 31) * lane_elements(EIGHT);
+  if (e.g_type == ROT_TYPE_F32)
+    step_warp<KEPT, EIGHT, true>(h, c, e, i, full);
+  else
+    step_warp<KEPT, EIGHT, false>(h, c, e, i, full);
 }
 
 template <Kept KEPT, bool EIGHT, int CAP>
@@ -349,9 +531,9 @@ int launch_table(const Hyper& h, const Entry* e, int count, cudaStream_t s) {
   for (int i = 0; i < count; ++i) {
     t.first[i] = (uint32_t)chunks;
     t.e[i] = e[i];
-    chunks += (e[i].n + kChunk - 1) / kChunk;
+    chunks += (e[i].n + chunk_of(EIGHT) - 1) / chunk_of(EIGHT);
   }
-  adamw_kernel<KEPT, EIGHT, CAP><<<(unsigned)chunks, kThreads, 0, s>>>(t);
+  adamw_kernel<KEPT, EIGHT, CAP><<<(unsigned)chunks, threads_of(EIGHT), 0, s>>>(t);
   return launched();
 }
 
@@ -378,7 +560,6 @@ int launch_adamw(const Hyper& h, const std::vector<Entry>& all, cudaStream_t s) 
 }
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-int word_bytes(int32_t type) { return type == ROT_TYPE_F32 ? 16 : 8; }
 
 // ---- norm ----
 
@@ -521,8 +702,10 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
       Entry e;
       e.p = t.p, e.g = t.g, e.m = t.m, e.v = t.v, e.ms = t.m_scale, e.vs = t.v_scale;
       e.master = t.master, e.n = t.n, e.word = word, e.g_type = t.g_type;
-      e.whole = aligned(t.p, word_bytes(t.p_type)) && aligned(t.g, word_bytes(t.g_type)) &&
-                aligned(t.m, 4 * state) && aligned(t.v, 4 * state) && aligned(t.master, 16);
+      const int lane = lane_elements(eight);
+      auto fits = [&](const void* p, int es) { return aligned(p, std::min(16, lane * es)); };
+      e.whole = fits(t.p, type_bytes(t.p_type)) && fits(t.g, type_bytes(t.g_type)) &&
+                fits(t.m, state) && fits(t.v, state) && fits(t.master, 4);
       of[kept][eight].push_back(e);
     }
     std::sort(written.begin(), written.end());
@@ -531,7 +714,10 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
     const int dev = check_device();
     if (dev != ROT_OK) return dev;
     Hyper h;
-    h.lr = (float)y.lr, h.eps = (float)y.eps, h.weight_decay = (float)y.weight_decay;
+    h.lr = (float)y.lr;
+    // (the quotient's approximate reciprocal takes subnormal numbers for 0)
+    h.eps = y.eps > 0.0 ? std::max((float)y.eps, 0x1p-126f) : 0.f;
+    h.weight_decay = (float)y.weight_decay;
     h.beta1 = (float)y.beta1, h.rest1 = (float)(1.0 - y.beta1);
     h.beta2 = (float)y.beta2, h.rest2 = (float)(1.0 - y.beta2);
     h.decay = (float)(1.0 - y.lr * y.weight_decay);

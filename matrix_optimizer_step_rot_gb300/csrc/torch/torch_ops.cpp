@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -53,14 +54,6 @@ struct Entries {
 #undef X
 } lib;
 PyObject* rot_error = nullptr;  // binding.RotError
-
-void bind(const py::dict& addresses, py::object error) {
-#define X(name) \
-  lib.name = reinterpret_cast<decltype(lib.name)>(addresses[#name].cast<uintptr_t>());
-  ROT_ENTRIES(X)
-#undef X
-  rot_error = error.release().ptr();
-}
 
 void check(int code, const char* where) {
   if (code == ROT_OK) return;
@@ -589,6 +582,11 @@ std::tuple<Tensor, MaybeTensor, Tensor, MaybeTensor> head_norm_backward(
 }
 
 // -------------------------------------------------------------------- AdamW
+// Lists are read in place: a list of a hundred vectors is host time alone (113
+// of them: 13 us a call here; as std::vector<Tensor> with the checks in Python
+// 148).
+PyObject* fp8_vector = nullptr;  // operators.Fp8Vector
+
 // The current device, asked for once a tensor is a CUDA tensor.
 struct Current {
   c10::DeviceIndex index = -1;
@@ -598,6 +596,27 @@ struct Current {
     return t.get_device() == index;
   }
 };
+
+// A Python list or tuple.
+struct List {
+  py::object keep;
+  Py_ssize_t size = 0;
+  List(const py::object& o, const char* name) {
+    PyObject* p = PySequence_Fast(o.ptr(), "");
+    if (!p) {
+      PyErr_Clear();
+      fail(std::string(name) + ": expected a list");
+    }
+    keep = py::reinterpret_steal<py::object>(p);
+    size = PySequence_Fast_GET_SIZE(p);
+  }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(keep.ptr(), i); }
+};
+const Tensor& tensor_of(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) fail(std::string(name) + ": expected tensors, got " + Py_TYPE(o)->tp_name);
+  return THPVariable_Unpack(o);
+}
+
 // A flat tensor of a list.
 void* flat(const Tensor& t, const char* name, int64_t n, Current& device) {
   if (!device.has(t)) fail(std::string(name) + ": expected CUDA tensors on the current device");
@@ -606,59 +625,66 @@ void* flat(const Tensor& t, const char* name, int64_t n, Current& device) {
   return t.data_ptr();
 }
 template <class T>
-const T* word_of(const MaybeTensor& t, const char* name, at::ScalarType type,
-                 Current& device) {
+const T* word_of(const MaybeTensor& t, const char* name, at::ScalarType type, Current& device) {
   if (!t) return nullptr;
   if (!device.has(*t) || t->scalar_type() != type || t->numel() != 1)
     fail(std::string(name) + ": expected one element of the right type on the current device");
   return t->data_ptr<T>();
 }
 
-void adamw(const std::vector<Tensor>& params, const std::vector<Tensor>& grads,
-           const std::vector<Tensor>& m, const std::vector<Tensor>& v,
-           const std::vector<MaybeTensor>& m_scale, const std::vector<MaybeTensor>& v_scale,
-           const std::vector<MaybeTensor>& masters, int64_t step, const MaybeTensor& step_device,
-           double lr, const MaybeTensor& lr_device, double beta1, double beta2, double eps,
-           double weight_decay, const MaybeTensor& norm, double max_norm, double scale,
-           uint64_t seed) {
-  const size_t n = params.size();
-  if (grads.size() != n || m.size() != n || v.size() != n || m_scale.size() != v_scale.size() ||
-      (!m_scale.empty() && m_scale.size() != n) || (!masters.empty() && masters.size() != n))
+// A moment: a float32 tensor, or an Fp8Vector (scale is then set).
+void* state_of(PyObject* o, const char* name, int64_t n, Current& device, uint8_t** scale) {
+  *scale = nullptr;
+  at::ScalarType type = at::kFloat;
+  if (PyTuple_Check(o) && PyObject_TypeCheck(o, (PyTypeObject*)fp8_vector)) {
+    const Tensor& s = tensor_of(PyTuple_GET_ITEM(o, 1), name);
+    if (s.scalar_type() != at::kByte) fail(std::string(name) + ": expected uint8 scales");
+    *scale = static_cast<uint8_t*>(flat(s, name, up(n, 128), device));
+    o = PyTuple_GET_ITEM(o, 0);
+    type = at::kFloat8_e4m3fn;
+  }
+  const Tensor& t = tensor_of(o, name);
+  if (t.scalar_type() != type)
+    fail(std::string(name) + ": expected float32 tensors, or Fp8Vectors of float8_e4m3fn");
+  return flat(t, name, n, device);
+}
+
+void adamw(const py::object& params, const py::object& grads, const py::object& m,
+           const py::object& v, const py::object& masters, int64_t step,
+           const MaybeTensor& step_device, double lr, const MaybeTensor& lr_device, double beta1,
+           double beta2, double eps, double weight_decay, const MaybeTensor& norm, double max_norm,
+           double scale, uint64_t seed) {
+  const List ps(params, "params"), gs(grads, "grads"), m1(m, "m"), v1(v, "v");
+  const bool has_masters = !masters.is_none();
+  const List ms(has_masters ? masters : params, "masters");
+  const Py_ssize_t n = ps.size;
+  if (gs.size != n || m1.size != n || v1.size != n || ms.size != n)
     fail("grads, m, v, masters: expected an entry for each parameter");
   Current device;
   std::vector<rot_adamw_tensor> list(n);
-  for (size_t i = 0; i < n; ++i) {
+  for (Py_ssize_t i = 0; i < n; ++i) {
     rot_adamw_tensor& t = list[i];
-    const int64_t count = params[i].numel();
-    t.p = flat(params[i], "params", count, device);
-    t.g = flat(grads[i], "grads", count, device);
-    t.m = flat(m[i], "m", count, device);
-    t.v = flat(v[i], "v", count, device);
-    t.p_type = type_of(params[i]), t.g_type = type_of(grads[i]);
+    const Tensor &p = tensor_of(ps[i], "params"), &g = tensor_of(gs[i], "grads");
+    t.n = p.numel();
+    t.p = flat(p, "params", t.n, device);
+    t.g = flat(g, "grads", t.n, device);
+    t.p_type = type_of(p), t.g_type = type_of(g);
     if (t.p_type < 0 || t.g_type < 0)
       fail("params, grads: expected float32, float16 or bfloat16");
-    if (grads[i].sizes() != params[i].sizes()) fail("grads: expected the parameters' shapes");
-    t.m_scale = t.v_scale = nullptr;
+    if (g.sizes() != p.sizes()) fail("grads: expected the parameters' shapes");
+    t.m = state_of(m1[i], "m", t.n, device, &t.m_scale);
+    t.v = state_of(v1[i], "v", t.n, device, &t.v_scale);
+    if (!t.m_scale != !t.v_scale && t.n > 0)
+      fail("m, v: one in 8 bits, the other not");
     t.master = nullptr;
-    const bool eight = !m_scale.empty() && m_scale[i];
-    if (eight != (!v_scale.empty() && v_scale[i])) fail("m, v: one in 8 bits, the other not");
-    const at::ScalarType state = eight ? at::kFloat8_e4m3fn : at::kFloat;
-    if (m[i].scalar_type() != state || v[i].scalar_type() != state)
-      fail("m, v: expected float32 tensors, or Fp8Vectors of float8_e4m3fn");
-    if (eight) {
-      for (const MaybeTensor* s : {&m_scale[i], &v_scale[i]})
-        if ((*s)->scalar_type() != at::kByte) fail("m, v: expected uint8 scales");
-      t.m_scale = static_cast<uint8_t*>(flat(*m_scale[i], "m.scale", up(count, 128), device));
-      t.v_scale = static_cast<uint8_t*>(flat(*v_scale[i], "v.scale", up(count, 128), device));
-    }
-    if (!masters.empty() && masters[i]) {
-      if (masters[i]->scalar_type() != at::kFloat) fail("masters: expected float32 tensors");
-      t.master = static_cast<float*>(flat(*masters[i], "masters", count, device));
+    if (has_masters && ms[i] != Py_None) {
+      const Tensor& w = tensor_of(ms[i], "masters");
+      if (w.scalar_type() != at::kFloat) fail("masters: expected float32 tensors");
+      t.master = static_cast<float*>(flat(w, "masters", t.n, device));
       if (t.p_type == ROT_TYPE_F32) fail("masters: a float32 parameter has none");
     } else if (t.p_type == ROT_TYPE_F16) {
       fail("masters: a float16 parameter needs one");
     }
-    t.n = count;
   }
   rot_adamw_hyper h = {};
   h.lr = lr, h.beta1 = beta1, h.beta2 = beta2, h.eps = eps, h.weight_decay = weight_decay;
@@ -669,13 +695,15 @@ void adamw(const std::vector<Tensor>& params, const std::vector<Tensor>& grads,
   check(lib.rot_adamw_step(list.data(), (int32_t)n, &h, stream()), "rot_adamw_step");
 }
 
-Tensor gradient_norm(const std::vector<Tensor>& grads) {
+Tensor gradient_norm(const py::object& grads) {
+  const List gs(grads, "grads");
   Current device;
-  std::vector<rot_gradient> list(grads.size());
-  for (size_t i = 0; i < grads.size(); ++i) {
-    list[i].g = flat(grads[i], "grads", grads[i].numel(), device);
-    list[i].n = grads[i].numel();
-    list[i].type = type_of(grads[i]);
+  std::vector<rot_gradient> list(gs.size);
+  for (Py_ssize_t i = 0; i < gs.size; ++i) {
+    const Tensor& g = tensor_of(gs[i], "grads");
+    list[i].g = flat(g, "grads", g.numel(), device);
+    list[i].n = g.numel();
+    list[i].type = type_of(g);
     if (list[i].type < 0) fail("grads: expected float32, float16 or bfloat16");
   }
   const auto on = at::TensorOptions().device(at::kCUDA, c10::cuda::current_device());
@@ -686,6 +714,15 @@ Tensor gradient_norm(const std::vector<Tensor>& grads) {
                               work.data_ptr(), need, stream()),
         "rot_gradient_norm");
   return norm;
+}
+
+void bind(const py::dict& addresses, py::object error, py::object vector_class) {
+#define X(name) \
+  lib.name = reinterpret_cast<decltype(lib.name)>(addresses[#name].cast<uintptr_t>());
+  ROT_ENTRIES(X)
+#undef X
+  rot_error = error.release().ptr();
+  fp8_vector = vector_class.release().ptr();
 }
 
 }  // namespace

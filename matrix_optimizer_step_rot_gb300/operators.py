@@ -25,7 +25,7 @@ from __future__ import annotations
 import ctypes
 import math
 import threading
-from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -68,7 +68,7 @@ def _load():
         raise RuntimeError("_rot_torch.so is missing or does not load: build it with "
                            "matrix_optimizer_step_rot_gb300.build.build()") from e
     _rot_torch.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value
-                     for n in B.header_symbols()}, B.RotError)
+                     for n in B.header_symbols()}, B.RotError, Fp8Vector)
     _native = _rot_torch
     return _native
 
@@ -492,23 +492,7 @@ def gradient_norm(grads: Sequence[torch.Tensor], *, stream=None) -> torch.Tensor
     thousand of them."""
     if stream is not None:
         return _on(stream, lambda: gradient_norm(grads), list(grads))
-    _tensors(**{f"grads[{i}]": g for i, g in enumerate(grads)})
     return (_native or _load()).gradient_norm(grads)
-
-
-def _states(states: Sequence[State], name: str) -> Tuple[List[torch.Tensor], list]:
-    """The tensors, and the scales of those in 8 bits (none at all: an empty
-    list)."""
-    data, scale = [], []
-    for i, s in enumerate(states):
-        if isinstance(s, Fp8Vector):
-            _tensors(**{f"{name}[{i}].data": s.data, f"{name}[{i}].scale": s.scale})
-            scale += [None] * (i - len(scale)) + [s.scale]
-            data.append(s.data)
-        else:
-            _tensors(**{f"{name}[{i}]": s})
-            data.append(s)
-    return data, scale + [None] * (len(data) - len(scale)) if scale else scale
 
 
 def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequence[State],
@@ -534,16 +518,8 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequ
                                          scale=scale, seed=seed),
                    list(params), list(grads), list(m), list(v), masters and list(masters), norm,
                    step, lr)
-    native = _native or _load()
-    for name, ts in (("params", params), ("grads", grads)):
-        for i, t in enumerate(ts):
-            if not isinstance(t, torch.Tensor):
-                _tensors(**{f"{name}[{i}]": t})
-    md, ms = _states(m, "m")
-    vd, vs = _states(v, "v")
-    if bool(ms) != bool(vs):
-        raise ValueError("m, v: one in 8 bits, the other not")
     on = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
-    native.adamw(params, grads, md, vd, ms, vs, masters or [], 1 if on[0] else step,
-                 step if on[0] else None, 0.0 if on[1] else lr, lr if on[1] else None, beta1,
-                 beta2, eps, weight_decay, norm, max_norm, scale, _word(seed, "seed"))
+    (_native or _load()).adamw(params, grads, m, v, masters, 1 if on[0] else step,
+                               step if on[0] else None, 0.0 if on[1] else lr,
+                               lr if on[1] else None, beta1, beta2, eps, weight_decay, norm,
+                               max_norm, scale, _word(seed, "seed"))
