@@ -117,18 +117,18 @@ struct Now {
 // there and reached by accesses of 16 bytes (or all of them), else `left` of
 // them one by one (the rest 0).
 template <int W>
-struct Words {
+struct Piece {
   uint32_t w[W];
 };
 template <int ES>
 using Bits = std::conditional_t<ES == 4, uint32_t, std::conditional_t<ES == 2, uint16_t, uint8_t>>;
 
 template <int ES, int N, bool FULL>
-__device__ __forceinline__ Words<N * ES / 4> some(const void* p, uint32_t i, int left) {
+__device__ __forceinline__ Piece<N * ES / 4> some(const void* p, uint32_t i, int left) {
   using T = Bits<ES>;
   constexpr int W = N * ES / 4;
   const T* q = (const T*)p + i;
-  Words<W> r;
+  Piece<W> r;
   if constexpr (!FULL) {
 #pragma unroll
     for (int k = 0; k < W; ++k) r.w[k] = 0;
@@ -149,7 +149,7 @@ __device__ __forceinline__ Words<N * ES / 4> some(const void* p, uint32_t i, int
   return r;
 }
 template <int ES, int N, bool FULL>
-__device__ __forceinline__ void put_some(void* p, uint32_t i, int left, const Words<N * ES / 4>& r) {
+__device__ __forceinline__ void put_some(void* p, uint32_t i, int left, const Piece<N * ES / 4>& r) {
   using T = Bits<ES>;
   constexpr int W = N * ES / 4;
   T* q = (T*)p + i;
@@ -170,8 +170,8 @@ __device__ __forceinline__ float2 f32_pair(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 template <int N>
-__device__ __forceinline__ Words<N> words_of(const float2 (&x)[N / 2]) {
-  Words<N> r;
+__device__ __forceinline__ Piece<N> words_of(const float2 (&x)[N / 2]) {
+  Piece<N> r;
 #pragma unroll
   for (int k = 0; k < N / 2; ++k)
     r.w[2 * k] = __float_as_uint(x[k].x), r.w[2 * k + 1] = __float_as_uint(x[k].y);
@@ -307,9 +307,9 @@ template <Kept KEPT, bool EIGHT, bool WIDE>
 struct Raw {
   static constexpr int N = lane_elements(EIGHT);
   static constexpr int G = WIDE ? 4 : 2, P = KEPT == kBf16Random ? 2 : 4, S = EIGHT ? 1 : 4;
-  Words<N * G / 4> g;
-  Words<N * P / 4> p;
-  Words<N * S / 4> m, v;
+  Piece<N * G / 4> g;
+  Piece<N * P / 4> p;
+  Piece<N * S / 4> m, v;
   uint32_t sm, sv;  // (8 bits: the scales' bytes)
 
   template <bool FULL>
@@ -415,7 +415,7 @@ __device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const He
 #pragma unroll
     for (int k = 1; k < H; ++k) top = top_of(p[k].x, p[k].y, top);
     const bool odd = !(top < __int_as_float(0x7f800000));
-    Words<H> q;
+    Piece<H> q;
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       const uint32_t a = __float_as_uint(p[k].x), b = __float_as_uint(p[k].y);
@@ -435,7 +435,7 @@ __device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const He
     put_some<4, N, FULL>(e.p, i, left, words_of<N>(p));
   } else {
     put_some<4, N, FULL>(e.master, i, left, words_of<N>(p));
-    Words<H> q;
+    Piece<H> q;
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       if constexpr (KEPT == kBf16Master) {
@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(threads_of(EIGHT), EIGHT ? 11 : 2)
   const int of = tensor_of(a.first, a.count, blockIdx.x);
   const Here e = here_of<KEPT, EIGHT>(a.e[of], blockIdx.x - a.first[of]);
   Now c = {h.scale, h.decay, h.step_size, h.inv_root, h.step, {}};
+  wait_for_prior();
   if (h.norm) {
     const float norm = fabsf(c.scale) * *h.norm;
     if (!isfinite(norm)) return;
@@ -533,8 +534,7 @@ int launch_table(const Hyper& h, const Entry* e, int count, cudaStream_t s) {
     t.e[i] = e[i];
     chunks += (e[i].n + chunk_of(EIGHT) - 1) / chunk_of(EIGHT);
   }
-  adamw_kernel<KEPT, EIGHT, CAP><<<(unsigned)chunks, threads_of(EIGHT), 0, s>>>(t);
-  return launched();
+  return launch_behind(adamw_kernel<KEPT, EIGHT, CAP>, (unsigned)chunks, threads_of(EIGHT), 0, s, t);
 }
 
 // Launches of at most kMany tensors (of 2^40 elements in all).
@@ -605,6 +605,7 @@ __device__ __forceinline__ float squares(const Square& e, int64_t i0, int64_t en
 // A block sums the squares of a run of chunks.
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ SquareTable a) {
   __shared__ float red[kWarps];
+  wait_for_prior();
   const uint32_t c0 = (uint32_t)((uint64_t)a.chunks * blockIdx.x / gridDim.x);
   const uint32_t c1 = (uint32_t)((uint64_t)a.chunks * (blockIdx.x + 1) / gridDim.x);
   float sum = 0.f;
@@ -791,8 +792,7 @@ int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm,
       t.chunks = (uint32_t)chunks;
       const unsigned blocks = (unsigned)std::min<uint64_t>(chunks, most);
       ProfScope prof(ROT_PROF_ELEMENTWISE, bytes, s);
-      squares_kernel<<<blocks, kThreads, 0, s>>>(t);
-      const int e = launched();
+      const int e = launch_behind(squares_kernel, blocks, kThreads, 0, s, t);
       if (e != ROT_OK) return e;
       parts += (int)blocks;
     }

@@ -13,19 +13,19 @@ int heads_rotate(int32_t type, HeadArgs& q, int64_t tokens, bool il, cudaStream_
 
 namespace {
 
-// The weights' gradients: each side's parts, 32 columns by 32 strided shares
+// The weights' gradients: the blocks' parts, 32 columns by 32 strided shares
 // per block, joined in a fixed order.
-__global__ void __launch_bounds__(1024) heads_join_kernel(const float* part, int parts0, int parts1,
-                                                          int dim, float* dw0, float* dw1) {
+__global__ void __launch_bounds__(1024) heads_join_kernel(const float* part, int parts, int dim,
+                                                          float* dw0, float* dw1) {
   __shared__ float share[32][33];
   wait_for_prior();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks = (dim + 31) / 32, second = blockIdx.x >= blocks;
-  const int first = second ? parts0 : 0, last = second ? parts0 + parts1 : parts0;
   const int base = (blockIdx.x - second * blocks) * 32;
   float sum = 0.f;
   if (base + lane < dim)
-    for (int p = first + warp; p < last; p += 32) sum += part[(int64_t)p * dim + base + lane];
+    for (int p = warp; p < parts; p += 32)
+      sum += part[((int64_t)p * 2 + second) * dim + base + lane];
   share[warp][lane] = sum;
   __syncthreads();
   sum = warp_sum(share[lane][warp]);  // column `warp` of this block
@@ -159,7 +159,7 @@ int rot_head_norm_forward(const rot_heads* q, const void* q_weight, const rot_he
 
 uint64_t rot_head_norm_work_bytes(int64_t dim) {
   if (dim < 1 || dim > ROT_MAX_HEAD_DIM) return 0;
-  return align256(4ull * (uint64_t)dim * kHeadParts);
+  return align256(8ull * (uint64_t)dim * kHeadParts);
 }
 
 int rot_head_norm_backward(const rot_heads* dq, const rot_heads* q, const void* q_weight,
@@ -182,16 +182,15 @@ int rot_head_norm_backward(const rot_heads* dq, const rot_heads* q, const void* 
   a.w32 = wtype == ROT_TYPE_F32, a.eps = eps, a.part = static_cast<float*>(work);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return guarded([&] {
-    int parts0 = 0, parts1 = 0;
+    a.blocks = 0;
     if (a.side[0].heads || a.side[1].heads) {
       ProfScope prof(ROT_PROF_ELEMENTWISE, moved(a, batch * tokens, type, 3), s);
       const int code = heads_norm_grad(type, a, batch * tokens, rotary && rotary->interleaved, s);
       if (code != ROT_OK) return code;
-      parts0 = (int)a.blocks0, parts1 = (int)a.blocks1;
     }
     ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
     return launch_behind(heads_join_kernel, ((int)dim + 31) / 32 * (k ? 2 : 1), 1024, 0, s,
-                         (const float*)a.part, parts0, parts1, (int)dim, dq_weight, dk_weight);
+                         (const float*)a.part, (int)a.blocks, (int)dim, dq_weight, dk_weight);
   });
 }
 
