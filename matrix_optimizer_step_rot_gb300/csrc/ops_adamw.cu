@@ -559,6 +559,28 @@ int launch_adamw(const Hyper& h, const std::vector<Entry>& all, cudaStream_t s) 
   return ROT_OK;
 }
 
+// The addresses that a call writes: each one once.  (A table twice as large: a
+// list of 300 tensors takes 58 us of the host with their addresses sorted.)
+class Written {
+ public:
+  explicit Written(size_t most) {
+    size_t size = 16;
+    while (size < 2 * most) size *= 2;
+    at_.resize(size);
+  }
+  bool again(const void* p) {  // whether p was there
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+    size_t i = (size_t)((uint64_t)x * 0x9E3779B97F4A7C15u >> 32) & (at_.size() - 1);
+    for (; at_[i]; i = (i + 1) & (at_.size() - 1))
+      if (at_[i] == x) return true;
+    at_[i] = x;
+    return false;
+  }
+
+ private:
+  std::vector<uintptr_t> at_;
+};
+
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // ---- norm ----
@@ -671,7 +693,8 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
   if (!y.step_device && y.step < 1) return ROT_EINVAL;
   return guarded([&]() -> int {
     std::vector<Entry> of[4][2];
-    std::vector<const void*> written;
+    Written written(6 * (size_t)count);
+    bool some = false;
     uint64_t words = 0;
     int64_t room = kMostElements;
     for (int32_t i = 0; i < count; ++i) {
@@ -695,7 +718,8 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
       for (const void* p : {(const void*)t.p, (const void*)t.m, (const void*)t.v,
                             (const void*)t.m_scale, (const void*)t.v_scale,
                             (const void*)t.master})
-        if (p) written.push_back(p);
+        if (p && written.again(p)) return ROT_EINVAL;
+      some = true;
       const int kept = t.p_type == ROT_TYPE_F32    ? kF32
                        : t.p_type == ROT_TYPE_F16 ? kF16Master
                        : t.master                  ? kBf16Master
@@ -707,11 +731,11 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
       auto fits = [&](const void* p, int es) { return aligned(p, std::min(16, lane * es)); };
       e.whole = fits(t.p, type_bytes(t.p_type)) && fits(t.g, type_bytes(t.g_type)) &&
                 fits(t.m, state) && fits(t.v, state) && fits(t.master, 4);
-      of[kept][eight].push_back(e);
+      std::vector<Entry>& list = of[kept][eight];
+      if (list.empty()) list.reserve(count - i);
+      list.push_back(e);
     }
-    std::sort(written.begin(), written.end());
-    if (std::adjacent_find(written.begin(), written.end()) != written.end()) return ROT_EINVAL;
-    if (written.empty()) return ROT_OK;
+    if (!some) return ROT_OK;
     const int dev = check_device();
     if (dev != ROT_OK) return dev;
     Hyper h;
