@@ -291,6 +291,14 @@ __device__ __forceinline__ void random_of(const Hyper& h, const Now& c, uint64_t
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
 
+// Two numbers in bfloat16, each rounded by 16 bits (of the second the upper):
+// added below the last place kept, and cut off there.
+__device__ __forceinline__ uint32_t rounded_bf16(float2 x, uint32_t random) {
+  uint32_t r;
+  asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(r) : "f"(x.y), "f"(x.x), "r"(random));
+  return r;
+}
+
 __device__ __forceinline__ float root(float x) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -410,26 +418,10 @@ __device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const He
     put_some<4, N, FULL>(e.v, i, left, words_of<N>(v));
   }
   if constexpr (KEPT == kBf16Random) {
-    // (a NaN stays one without an addition to its bits, as infinity does)
-    float top = top_of(p[0].x, p[0].y, 0.f);
-#pragma unroll
-    for (int k = 1; k < H; ++k) top = top_of(p[k].x, p[k].y, top);
-    const bool odd = !(top < __int_as_float(0x7f800000));
     Piece<H> q;
 #pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const uint32_t a = __float_as_uint(p[k].x), b = __float_as_uint(p[k].y);
-      q.w[k] = __byte_perm(a + (w[2 * k] >> 16), b + (w[2 * k + 1] >> 16), 0x7632);
-    }
-    if (odd) {
-#pragma unroll
-      for (int k = 0; k < H; ++k) {
-        const bool fx = fabsf(p[k].x) < __int_as_float(0x7f800000);
-        const bool fy = fabsf(p[k].y) < __int_as_float(0x7f800000);
-        q.w[k] = __byte_perm(__float_as_uint(p[k].x) + (fx ? w[2 * k] >> 16 : 0u),
-                           __float_as_uint(p[k].y) + (fy ? w[2 * k + 1] >> 16 : 0u), 0x7632);
-      }
-    }
+    for (int k = 0; k < H; ++k)
+      q.w[k] = rounded_bf16(p[k], __byte_perm(w[2 * k], w[2 * k + 1], 0x7632));
     put_some<2, N, FULL>(e.p, i, left, q);
   } else if constexpr (KEPT == kF32) {
     put_some<4, N, FULL>(e.p, i, left, words_of<N>(p));

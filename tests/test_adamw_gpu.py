@@ -260,6 +260,18 @@ def test_special_values():
         if bits == 8:
             assert torch.equal(torch.isnan(x["m"][0].dequantize()), odd)
             assert torch.equal(torch.isnan(x["v"][0].dequantize()), odd)
+        # bfloat16 parameters without a master, aligned and not
+        for shift in (0, 1):
+            y = lists([512], BF16, F32, False, bits, 11, shift)
+            for at, bad in ((5, float("nan")), (130, float("inf")), (131, float("-inf"))):
+                y["g"][0][at] = bad
+            y["p"][0][200], y["p"][0][201] = float("inf"), float("-inf")
+            keep = y["p"][0].clone()
+            call(y, 4)
+            odd[[5, 130, 131]] = True
+            assert torch.equal(torch.isnan(y["p"][0]), odd)
+            assert y["p"][0][200].item() == float("inf") and y["p"][0][201].item() == float("-inf")
+            assert torch.isfinite(y["p"][0][~odd]).sum() == 512 - 5 and (y["p"][0] != keep).sum() > 300
         # a tensor of zero gradients and states moves by its decay alone
         z = lists([300], F32, F32, False, 32, 12)
         z["g"][0].zero_()
