@@ -683,6 +683,8 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
     if (!(x >= 0.0 && x < 1.0)) return ROT_EINVAL;
   if (!std::isfinite(y.scale) || (y.norm && !(y.max_norm > 0.0))) return ROT_EINVAL;
   if (!y.step_device && y.step < 1) return ROT_EINVAL;
+  if (!aligned(y.lr_device, 4) || !aligned(y.step_device, 8) || !aligned(y.norm, 4))
+    return ROT_EINVAL;
   return guarded([&]() -> int {
     std::vector<Entry> of[4][2];
     Written written(6 * (size_t)count);
@@ -772,7 +774,7 @@ uint64_t rot_gradient_norm_work_bytes(int32_t count) {
 
 int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm, void* work,
                       uint64_t work_bytes, void* stream) {
-  if (count < 0 || (count > 0 && !gradients) || !norm || !work ||
+  if (count < 0 || (count > 0 && !gradients) || !norm || !aligned(norm, 4) || !work ||
       (reinterpret_cast<uintptr_t>(work) & 255) ||
       work_bytes < rot_gradient_norm_work_bytes(count))
     return ROT_EINVAL;

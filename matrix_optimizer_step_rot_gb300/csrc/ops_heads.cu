@@ -56,6 +56,8 @@ bool bad_in(const rot_heads* h, int64_t batch, int64_t tokens) {
 }
 HeadStrides strides(const rot_heads* h) { return {h->batch_stride, h->token_stride, h->head_stride}; }
 
+bool misaligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes; }
+
 struct Given {
   const rot_heads *x, *dy, *out;
   const void* w;
@@ -80,7 +82,7 @@ int set_up(HeadArgs& a, const Given (&g)[2], int64_t batch, int64_t tokens, int6
     if (some) {
       const void* all[3] = {v.x->data, v.out->data, grad ? v.dy->data : v.x->data};
       for (const void* p : all)
-        if (!p || reinterpret_cast<uintptr_t>(p) % es) return ROT_EINVAL;
+        if (!p || misaligned(p, es)) return ROT_EINVAL;
     }
     HeadSide& sd = a.side[i];
     sd.x = v.x->data, sd.xs = strides(v.x);
@@ -91,10 +93,11 @@ int set_up(HeadArgs& a, const Given (&g)[2], int64_t batch, int64_t tokens, int6
   }
   if (!r) return ROT_OK;
   if (r->rotated < 0 || r->rotated > dim || r->rotated % 2 || std::isnan(r->magnitude) ||
-      (r->rotated > 0 && !r->turns))
+      (r->rotated > 0 && !r->turns) || misaligned(r->turns, 8))
     return ROT_EINVAL;
-  if (r->positions && (r->position_bytes != 4 && r->position_bytes != 8)) return ROT_EINVAL;
-  if (r->positions && (r->position_batch_stride < 0 || r->position_token_stride < 0))
+  if (r->positions && ((r->position_bytes != 4 && r->position_bytes != 8) ||
+                       misaligned(r->positions, r->position_bytes) ||
+                       r->position_batch_stride < 0 || r->position_token_stride < 0))
     return ROT_EINVAL;
   a.rotated = (int)r->rotated, a.turns = r->turns;
   a.positions = r->positions, a.position_bytes = r->position_bytes;
@@ -141,7 +144,9 @@ int rot_head_norm_forward(const rot_heads* q, const void* q_weight, const rot_he
                           int32_t wtype, int64_t batch, int64_t tokens, int64_t dim, int32_t type,
                           float eps, const rot_rotary* rotary, void* stream) {
   HeadArgs a;
-  if ((wtype != ROT_TYPE_F32 && wtype != type) || !(eps >= 0.f)) return ROT_EINVAL;
+  if ((wtype != ROT_TYPE_F32 && wtype != type) || !(eps >= 0.f) ||
+      misaligned(q_weight, type_bytes(wtype)) || misaligned(k_weight, type_bytes(wtype)))
+    return ROT_EINVAL;
   const int e = set_up(a, {{q, nullptr, q_out, q_weight}, {k, nullptr, k_out, k_weight}}, batch,
                        tokens, dim, type, rotary, false, true, false);
   if (e != ROT_OK) return e;
@@ -169,7 +174,10 @@ int rot_head_norm_backward(const rot_heads* dq, const rot_heads* q, const void* 
                            int64_t dim, int32_t type, float eps, const rot_rotary* rotary,
                            void* work, uint64_t work_bytes, void* stream) {
   HeadArgs a;
-  if ((wtype != ROT_TYPE_F32 && wtype != type) || !(eps >= 0.f)) return ROT_EINVAL;
+  if ((wtype != ROT_TYPE_F32 && wtype != type) || !(eps >= 0.f) ||
+      misaligned(q_weight, type_bytes(wtype)) || misaligned(k_weight, type_bytes(wtype)) ||
+      misaligned(dq_weight, 4) || misaligned(dk_weight, 4))
+    return ROT_EINVAL;
   const int e = set_up(a, {{q, dq, dq_out, q_weight}, {k, dk, dk_out, k_weight}}, batch, tokens,
                        dim, type, rotary, true, true, true);
   if (e != ROT_OK) return e;

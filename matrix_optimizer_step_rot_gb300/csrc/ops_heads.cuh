@@ -15,8 +15,8 @@
 // token's angles are worked out once, a pair to a lane, and shared through
 // shared memory, where the weights lie, too.  Warps stay for several tokens.
 // Rows come by asynchronous copies a few passes ahead; a lane copies and reads
-// its own runs alone, so that no lane waits for another's.  (Single elements,
-// which such copies do not take: the next pass's in registers.)
+// its own runs alone, so that no lane waits for another's.  (Single 16-bit
+// elements, which such copies do not take: the next pass's in registers.)
 #pragma once
 
 #include <algorithm>
@@ -136,7 +136,7 @@ __device__ __forceinline__ void pairs_of(const Piece<T, V>& ra, const Piece<T, V
     else
       a.p[0] = two_of(ra.w[0], T()).x, b.p[0] = two_of(rb.w[0], T()).x;
   } else {
-    static_assert(V % 4 == 0, "a pack comes from one run");
+    static_assert(V % 4 == 0 || !IL, "a pack comes from one run");
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       if constexpr (!IL && sizeof(T) == 4) {
@@ -197,6 +197,9 @@ __device__ __forceinline__ Piece<float, V> floats_at(const float* w) {
   Piece<float, V> r;
   if constexpr (V == 1) {
     r.w[0] = __float_as_uint(w[0]);
+  } else if constexpr (V == 2) {
+    const uint2 f = *reinterpret_cast<const uint2*>(w);
+    r.w[0] = f.x, r.w[1] = f.y;
   } else {
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
@@ -285,7 +288,7 @@ struct HeadRow {
     if (!there) return r;
     if constexpr (V == 1 && sizeof(T) == 2) {
       r.w[0] = *(const uint16_t*)p;
-    } else if constexpr (V == 1) {
+    } else if constexpr (Piece<T, V>::N == 1) {
       r.w[0] = *(const uint32_t*)p;
     } else if constexpr (Piece<T, V>::N == 2) {
       const uint2 x = *(const uint2*)p;
@@ -300,7 +303,7 @@ struct HeadRow {
     if (!there) return;
     if constexpr (V == 1 && sizeof(T) == 2)
       *(uint16_t*)p = (uint16_t)r.w[0];
-    else if constexpr (V == 1)
+    else if constexpr (Piece<T, V>::N == 1)
       *(uint32_t*)p = r.w[0];
     else if constexpr (Piece<T, V>::N == 2)
       *(uint2*)p = make_uint2(r.w[0], r.w[1]);
@@ -334,7 +337,8 @@ struct HeadRow {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
                      : "memory");
       else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from),
+                     "n"(kRunBytes < 4 ? 4 : kRunBytes), "r"(bytes)
                      : "memory");
     };
 #pragma unroll
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps, head_blocks(MODE, NU))
 
   // what is fetched: kAhead passes before it is worked on
   using Row = HeadRow<T, V, NU, DENSE>;
-  constexpr bool kRing = V > 1;
+  constexpr bool kRing = Row::kRunBytes >= 4;
   constexpr int kArrays = MODE == kNormGrad ? 2 : 1, kStage = kArrays * Row::kSlot;
   char* ring = reinterpret_cast<char*>(dyn + (2 + kHeadWarps) * q.dim) +
                warp * kHeadAhead * kStage + lane * Row::kRunBytes;
@@ -681,6 +685,7 @@ int launch_heads_as(HeadArgs& q, int64_t tokens, bool il, cudaStream_t s) {
   for (int n = 1; n <= std::min(q.passes, 16); ++n) {
     const int chunk = (q.passes + n - 1) / n;
     const int64_t items = tokens * ((q.passes + chunk - 1) / chunk);
+    if (n > 1 && items > int64_t(1) << 31) break;  // (they are counted in 32 bits)
     const int64_t cost =
         (items + most * kHeadWarps - 1) / (most * kHeadWarps) * (chunk + (q.rotated > 0));
     if (cost < best) best = cost, q.chunk = chunk;
@@ -692,19 +697,21 @@ int launch_heads_as(HeadArgs& q, int64_t tokens, bool il, cudaStream_t s) {
   q.step.chunk = (int)(step % q.chunks);
   q.step.t = step / q.chunks % q.tokens;
   q.step.b = step / q.chunks / q.tokens;
-  constexpr int ring = V == 1 ? 0 : kHeadWarps * kHeadAhead * HeadRow<T, V, NU, DENSE>::kSlot *
+  constexpr int ring = V * sizeof(T) < 4 ? 0 : kHeadWarps * kHeadAhead * HeadRow<T, V, NU, DENSE>::kSlot *
                                         (MODE == kNormGrad ? 2 : 1);
   const int smem = (int)sizeof(float) * (2 + kHeadWarps) * q.dim + ring;
   auto k = heads_kernel<T, V, NU, IL, DENSE, MODE>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      (int)sizeof(float) * (2 + kHeadWarps) * ROT_MAX_HEAD_DIM + ring);
-  if (attr != cudaSuccess) return ROT_ECUDA;
+  if (smem > 48 << 10 &&  // (of the current device: each time)
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return ROT_ECUDA;
+  }
   return launch_behind(k, (unsigned)q.blocks, 32 * kHeadWarps, (size_t)smem, s, q, (int)il);
 }
 
-// (dense rows without a look at which lanes have what: 16384 tokens of 16 and 8
-// heads of 128 in bfloat16, norm and rotation, DENSE_A us; without DENSE_B)
+// Rows of which every lane has two runs, without a look at which lanes have
+// what: 16384 tokens of 16 and 8 heads of 128 in bfloat16, norm and rotation,
+// 37.2 us; with that look 38.9.
 template <class T, int V, bool IL, HeadsMode MODE>
 int launch_heads_rows(HeadArgs& q, int64_t tokens, cudaStream_t s) {
   if (q.units == 1 << q.log_group && q.dim == 2 * V * q.units)
@@ -745,6 +752,14 @@ int launch_heads(HeadArgs& q, int64_t tokens, bool il, cudaStream_t s) {
       plan_units<4>(q, il);
       return q.units > 32 ? launch_heads_as<T, 4, 2, false, false, MODE>(q, tokens, il, s)
                           : launch_heads_as<T, 4, 1, false, false, MODE>(q, tokens, il, s);
+    }
+  }
+  if constexpr (V == 8) {  // 4-byte runs (dim 100: halves of 50)
+    if (!il && heads_align(q, 4, sizeof(T), il)) {
+      plan_units<2>(q, il);
+      if (q.units <= 32) return launch_heads_as<T, 2, 1, false, false, MODE>(q, tokens, il, s);
+      if (q.units <= 64) return launch_heads_as<T, 2, 2, false, false, MODE>(q, tokens, il, s);
+      return launch_heads_as<T, 2, 4, false, false, MODE>(q, tokens, il, s);
     }
   }
   plan_units<1>(q, il);

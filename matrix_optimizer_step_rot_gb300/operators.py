@@ -205,8 +205,8 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, *, factor: float = 1
     f = base ** (-torch.arange(0, rotated, 2, dtype=torch.float64) / max(rotated, 1))
     if original_length is None:
         return f / factor
-    if not 0 < low < high:
-        raise ValueError("low, high: expected 0 < low < high")
+    if not (original_length > 0 and 0 < low < high):
+        raise ValueError("original_length, low, high: expected a length above 0 and 0 < low < high")
     turns = f * original_length / (2 * math.pi)
     if by_index:  # (turns fall with the index as a power of the base)
         keep = torch.log(turns / low) / math.log(high / low)

@@ -64,17 +64,19 @@ SHARED = [dict(batch=-1), dict(tokens=-1), dict(batch=1 << 20, tokens=1 << 20), 
           dict(type=E4M3), dict(type=-1), dict(q=None), dict(q=heads(-1)), dict(q=heads(65537)), dict(q=heads(data=0)),
           dict(q=heads(data=P + 1)), dict(q=heads(token=-1)), dict(q=heads(head=1 << 60)), dict(q=heads(3)),
           dict(k=heads(3)), dict(k=None), rotary(rotated=-2), rotary(rotated=17), rotary(rotated=34),
-          rotary(turns=0), rotary(magnitude=NAN), rotary(position_bytes=2), rotary(position_token_stride=-1),
+          rotary(turns=0), rotary(turns=P + 4), rotary(positions=P + 4), rotary(magnitude=NAN),
+          rotary(positions=P + 2, position_bytes=4), rotary(position_bytes=2), rotary(position_token_stride=-1),
           rotary(position_batch_stride=-1)]
 REFUSED = {
     "rot_rotate": SHARED + [dict(q_out=None), dict(q_out=heads(data=0)), dict(q_out=heads(head=31)),
                             dict(q_out=heads(token=127)), dict(q_out=heads(batch=0)), dict(q_out=heads(token=0)),
                             dict(q_out=heads(3)), dict(k_out=None), dict(k_out=heads(1)), dict(rotary=None)],
-    "rot_head_norm_forward": SHARED + [dict(q_weight=0), dict(k_weight=0), dict(q_out=heads(head=16)), dict(q_out=None),
+    "rot_head_norm_forward": SHARED + [dict(q_weight=0), dict(k_weight=0), dict(q_weight=P + 2), dict(k_weight=P + 1), dict(q_out=heads(head=16)), dict(q_out=None),
                                        dict(wtype=F16), dict(wtype=9), dict(eps=-1.0), dict(eps=NAN)],
     "rot_head_norm_backward": SHARED + [dict(dq=None), dict(dq=heads(3)), dict(dq=heads(data=P + 1)), dict(dk=None),
                                         dict(dk=heads(1)), dict(q_weight=0), dict(k_weight=0), dict(dq_weight=0),
-                                        dict(dk_weight=0), dict(dq_out=heads(head=16)), dict(wtype=F16),
+                                        dict(dk_weight=0), dict(dq_weight=P + 2), dict(dk_weight=P + 1),
+                                        dict(q_weight=P + 2), dict(dq_out=heads(head=16)), dict(wtype=F16),
                                         dict(eps=-1.0), dict(work=0), dict(work=P + 16), dict(work_bytes=1024),
                                         dict(k=None, dk=None, k_weight=0, dk_out=None)],
 }
@@ -138,7 +140,8 @@ def test_adamw_tensor_refusals(change):
 @pytest.mark.parametrize("change", [
     dict(lr=-1.0), dict(lr=NAN), dict(eps=-1.0), dict(eps=NAN), dict(weight_decay=-1.0), dict(weight_decay=NAN),
     dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=NAN), dict(scale=NAN), dict(scale=INF), dict(step=0),
-    dict(step=-3), dict(max_norm=0.0), dict(max_norm=-1.0), dict(max_norm=NAN), dict(count=-1)])
+    dict(step=-3), dict(max_norm=0.0), dict(max_norm=-1.0), dict(max_norm=NAN), dict(count=-1),
+    dict(norm=P + 2), dict(lr_device=P + 1), dict(step_device=P + 4)])
 def test_adamw_hyper_refusals(change):
     assert adamw(TENSOR, **change) == B.ROT_EINVAL
 
@@ -165,7 +168,7 @@ def norm(*tensors, count=None, out=P, work=P, work_bytes=1 << 20):
 
 def test_gradient_norm_refusals():
     good = (P, 100, F32)
-    for call in (lambda: norm(good, count=-1), lambda: norm(good, out=0), lambda: norm(good, work=0),
+    for call in (lambda: norm(good, count=-1), lambda: norm(good, out=0), lambda: norm(good, out=P + 2), lambda: norm(good, work=0),
                  lambda: norm(good, work=P + 16), lambda: norm(good, work_bytes=64), lambda: norm((0, 100, F32)),
                  lambda: norm((P + 2, 100, F32)), lambda: norm((P + 1, 100, BF16)), lambda: norm((P, -1, F32)),
                  lambda: norm((P, (1 << 40) + 1, F32)), lambda: norm((P, 1 << 40, F32), (P, 1, F32)),
@@ -202,7 +205,7 @@ def test_frequencies():
     h = ops.rotary_frequencies(8, factor=4.0, original_length=2 * 2 * math.pi / 0.01, by_index=True)
     assert h[2].item() == pytest.approx(0.01 * (0.5 + 0.5 / 4), rel=1e-12)
     for bad in (dict(rotated=7), dict(rotated=-2), dict(rotated=8, base=0.0), dict(rotated=8, factor=0.0),
-                dict(rotated=8, original_length=10, low=2.0, high=1.0)):
+                dict(rotated=8, original_length=10, low=2.0, high=1.0), dict(rotated=8, original_length=0)):
         with pytest.raises(ValueError):
             ops.rotary_frequencies(**bad)
 

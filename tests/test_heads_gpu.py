@@ -113,6 +113,13 @@ CASES = [
     (1, 4, 65, 33, 16, 16, False, BF16, "plain", "int64"),
     (1, 4, 65, 33, 8, 8, True, BF16, "plain", "int64"),
     (1, 300, 1, 0, 128, 0, False, BF16, "plain", "start"),
+    (2, 31, 5, 2, 100, 100, False, BF16, "plain", "int64"),
+    (1, 31, 5, 2, 196, 196, False, F16, "fused", "int64"),
+    (1, 31, 3, 1, 500, 500, False, BF16, "plain", "int64"),
+    (2, 40, 3, 2, 22, 20, False, F16, "first", "int64"),
+    (1, 40, 9, 5, 128, 128, False, BF16, "plain", "int64"),  # groups past the last head
+    (1, 2900, 9, 5, 128, 128, True, F16, "fused", "int64"),
+    (1, 700, 1, 1, 256, 128, False, BF16, "first", "int32"),
     (2, 2500, 16, 8, 128, 128, False, BF16, "fused", "int64"),
     (1, 3000, 3, 3, 40, 20, True, F16, "fused", "int32"),
 ]
