@@ -278,6 +278,16 @@ __device__ __forceinline__ float group_sum(float x, int size) {
   return x;
 }
 
+__device__ __forceinline__ float2 group_sum2(float2 x, int size) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < size) {
+      const float y = __shfl_xor_sync(0xffffffffu, x.x, o);
+      x = add2(x, make_float2(y, __shfl_xor_sync(0xffffffffu, x.y, o)));
+    }
+  return x;
+}
+
 // A lane's runs of one row.  DENSE: every lane has both runs of a head (its
 // group may be past the last head: what such a group works on is not used).
 template <class T, int V, int NU, bool DENSE>
@@ -548,18 +558,8 @@ __global__ void __launch_bounds__(32 * kHeadWarps, head_blocks(MODE, NU))
         if constexpr (MODE == kNormGrad) pairs_of<T, V, IL>(rd.a[n], rd.b[n], ga[n], gb[n]);
       }
       fetch();
-      float rstd = 1.f;
       Vec<V> wa[NU], wb[NU];
-      if constexpr (MODE != kRotate) {
-        E sum = all_of<E>(0.f);
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int i = 0; i < P; ++i)
-            sum = fma2(a[n].p[i], a[n].p[i], fma2(b[n].p[i], b[n].p[i], sum));
-        float ss = total(sum);
-        ss = group_sum(ss, size);
-        rstd = live ? rsqrtf(ss * inv + q.eps) : 0.f;  // (eps may be 0)
+      auto weights = [&]() {
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           // (what is not there is read elsewhere, and 0 elements multiply it)
@@ -567,18 +567,44 @@ __global__ void __launch_bounds__(32 * kHeadWarps, head_blocks(MODE, NU))
           const Piece<float, V> rb = floats_at<V>(w + (DENSE || u[n].has_b ? u[n].b : 0));
           pairs_of<float, V, IL>(ra, rb, wa[n], wb[n]);
         }
+      };
+      // (two sums each, so that an addition need not wait for the last)
+      E squares = all_of<E>(0.f), squares2 = squares, along = squares, along2 = squares;
+      if constexpr (MODE != kRotate) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n)
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            squares = fma2(a[n].p[i], a[n].p[i], squares);
+            squares2 = fma2(b[n].p[i], b[n].p[i], squares2);
+          }
+        squares = add2(squares, squares2);
       }
       if constexpr (MODE == kNormGrad) {
-        E along = all_of<E>(0.f);
+        // both sums in one go: that of x^2 gives r, that of g w x is the one of
+        // g w hat over r
+        weights();
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           turn<V, IL>(u[n], c[n], s[n], ns[n], ga[n], gb[n]);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            a[n].p[i] = mul2(a[n].p[i], all_of<E>(rstd));
-            b[n].p[i] = mul2(b[n].p[i], all_of<E>(rstd));
+            along = fma2(mul2(ga[n].p[i], wa[n].p[i]), a[n].p[i], along);
+            along2 = fma2(mul2(gb[n].p[i], wb[n].p[i]), b[n].p[i], along2);
           }
-          auto sums = [&](Vec<V>& da, Vec<V>& db) {
+        }
+        along = add2(along, along2);
+        const float2 sums = group_sum2(make_float2(total(squares), total(along)), size);
+        const float r = live ? rsqrtf(sums.x * inv + q.eps) : 0.f;  // (eps may be 0)
+        const float k = -(sums.y * inv * r * r);
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            a[n].p[i] = mul2(a[n].p[i], all_of<E>(r));
+            b[n].p[i] = mul2(b[n].p[i], all_of<E>(r));
+          }
+          auto add = [&](Vec<V>& da, Vec<V>& db) {
             if (DENSE && !live) return;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -587,33 +613,30 @@ __global__ void __launch_bounds__(32 * kHeadWarps, head_blocks(MODE, NU))
             }
           };
           if (at.second)
-            sums(dwa[1][n], dwb[1][n]);
+            add(dwa[1][n], dwb[1][n]);
           else
-            sums(dwa[0][n], dwb[0][n]);
+            add(dwa[0][n], dwb[0][n]);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            ga[n].p[i] = mul2(ga[n].p[i], wa[n].p[i]);
-            gb[n].p[i] = mul2(gb[n].p[i], wb[n].p[i]);
-            along = fma2(ga[n].p[i], a[n].p[i], fma2(gb[n].p[i], b[n].p[i], along));
+            const E ka = mul2(mul2(ga[n].p[i], wa[n].p[i]), all_of<E>(r));
+            const E kb = mul2(mul2(gb[n].p[i], wb[n].p[i]), all_of<E>(r));
+            a[n].p[i] = fma2(a[n].p[i], all_of<E>(k), ka);
+            b[n].p[i] = fma2(b[n].p[i], all_of<E>(k), kb);
           }
         }
-        float m = total(along);
-        m = group_sum(m, size) * -inv;
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            a[n].p[i] = mul2(fma2(a[n].p[i], all_of<E>(m), ga[n].p[i]), all_of<E>(rstd));
-            b[n].p[i] = mul2(fma2(b[n].p[i], all_of<E>(m), gb[n].p[i]), all_of<E>(rstd));
-          }
       } else {
+        float r = 1.f;
+        if constexpr (MODE == kNorm) {
+          r = rsqrtf(group_sum(total(squares), size) * inv + q.eps);
+          weights();
+        }
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
           if constexpr (MODE == kNorm) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-              a[n].p[i] = mul2(mul2(a[n].p[i], all_of<E>(rstd)), wa[n].p[i]);
-              b[n].p[i] = mul2(mul2(b[n].p[i], all_of<E>(rstd)), wb[n].p[i]);
+              a[n].p[i] = mul2(mul2(a[n].p[i], all_of<E>(r)), wa[n].p[i]);
+              b[n].p[i] = mul2(mul2(b[n].p[i], all_of<E>(r)), wb[n].p[i]);
             }
           }
           turn<V, IL>(u[n], c[n], s[n], ns[n], a[n], b[n]);
