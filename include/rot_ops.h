@@ -370,9 +370,9 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
 uint64_t rot_gradient_norm_work_bytes(int32_t count);
 
 /* norm (one float32) = sqrt of the sum of the squares of all elements of the
- * tensors (n consecutive elements of `type` each).  Squares and a block's sums
- * are float32, the blocks' sum float64: elements near 2^64 give infinity, and
- * those below 2^-75 count as 0.
+ * tensors (n consecutive elements of `type` each).  Squares and a
+ * thread's sums of 32 are float32, sums of those float64: elements near 2^64
+ * give infinity, and those below 2^-75 count as 0.
  * Errors: ROT_EINVAL (count < 0, null pointers, n < 0, more than 2^40 elements
  * in all, misaligned elements, unknown types, workspace). */
 typedef struct rot_gradient {

@@ -47,7 +47,7 @@ struct Entry {
 struct Hyper {
   float lr, beta1, rest1, beta2, rest2, eps, decay;  // decay: 1 - lr weight_decay
   float step_size, inv_root;                         // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
-  float log1, log2, weight_decay, scale, max_norm;
+  float log1, log2, weight_decay, scale, max_norm, one;
   const float* lr_device;
   const int64_t* step_device;
   const float* norm;
@@ -299,10 +299,40 @@ __device__ __forceinline__ uint32_t rounded_bf16(float2 x, uint32_t random) {
   return r;
 }
 
-__device__ __forceinline__ float root(float x) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+// x + y of products that keep their own rounding.  `one` comes with the
+// parameters: a plain sum is made one instruction with a product before it.
+__device__ __forceinline__ float2 plus2(float2 x, float one, float2 y) {
+  return fma2(x, both(one), y);
+}
+
+// The roots of x, which are 0 or positive: r = s - (s^2 - x) / (2 s), Heron's
+// step on an approximation s from the reciprocal root.  s is within two last
+// places, the difference is exact (in one rounding) and its quotient small, so
+// that r is the nearest number but where the root lies within 2^-20 of a last
+// place of the middle of two.  Where an x is too small for that (the
+// difference would not be exact below 2^-100) or not finite, by the library.
+// top: the largest.
+template <int H>
+__device__ __forceinline__ void roots(const float2 (&x)[H], float2 (&r)[H], float& top) {
+  float low = 0x1p127f;
+  top = 0.f;
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    float2 y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x[k].x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x[k].y));
+    const float2 s = mul2(x[k], y);
+    r[k] = fma2(fma2(s, s, mul2(x[k], both(-1.f))), mul2(y, both(-0.5f)), s);
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(low) : "f"(low), "f"(x[k].x), "f"(x[k].y));
+    top = top_of(r[k].x, r[k].y, top);
+  }
+  if (low >= 0x1p-100f && top < __int_as_float(0x7f800000)) return;
+  top = 0.f;
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    r[k] = make_float2(__fsqrt_rn(x[k].x), __fsqrt_rn(x[k].y));
+    top = top_of(r[k].x, r[k].y, top);
+  }
 }
 __device__ __forceinline__ float inverse(float x) {
   float r;
@@ -375,10 +405,16 @@ __device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const He
   }
 #pragma unroll
   for (int k = 0; k < H; ++k) {
+    // (every step rounds as the formula's float32 steps do: what comes next is
+    // rounded to 3 bits at places that an error of one last place may cross)
     g[k] = mul2(g[k], both(c.scale));
-    m[k] = fma2(m[k], both(ms), mul2(g[k], both(h.rest1)));
-    v[k] = fma2(v[k], both(h.beta2), mul2(mul2(g[k], both(h.rest2)), g[k]));
-    r[k] = make_float2(root(v[k].x), root(v[k].y));
+    m[k] = plus2(mul2(m[k], both(ms)), h.one, mul2(g[k], both(h.rest1)));
+    v[k] = plus2(mul2(v[k], both(h.beta2)), h.one, mul2(mul2(g[k], both(h.rest2)), g[k]));
+  }
+  float top;
+  roots(v, r, top);
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
     const float2 under = fma2(r[k], both(c.inv_root), both(h.eps));
     const float2 u = mul2(m[k], both(-c.step_size));
     p[k] = fma2(u, make_float2(inverse(under.x), inverse(under.y)), mul2(p[k], both(c.decay)));
@@ -392,7 +428,7 @@ __device__ __forceinline__ void step_lane(const Hyper& h, const Now& c, const He
     uint32_t part[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) part[k] = (w[k] & 0xffffu) * 16u + 8u;
-    uint32_t t = byte8_of(__float_as_uint(top_of(m))) | byte8_of(__float_as_uint(top_of(r))) << 16;
+    uint32_t t = byte8_of(__float_as_uint(top_of(m))) | byte8_of(__float_as_uint(top)) << 16;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
     const uint32_t tm = t & 0xffffu, tv = t >> 16;
@@ -482,7 +518,7 @@ __device__ __forceinline__ void step_warp(const Hyper& h, const Now& c, const He
 }
 
 template <Kept KEPT, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(threads_of(EIGHT), EIGHT ? 11 : 2)
+__global__ void __launch_bounds__(threads_of(EIGHT), EIGHT ? KEPT == kBf16Random ? 10 : 11 : 2)
     adamw_kernel(const __grid_constant__ Table<CAP> a) {
   const Hyper& h = a.h;
   const int of = tensor_of(a.first, a.count, blockIdx.x);
@@ -584,7 +620,7 @@ struct Square {
 };
 constexpr int kSquares = 1000, kSquareChunk = 8192, kSquareBlocks = 1024;
 struct SquareTable {
-  float* part;
+  double* part;
   int32_t count;
   uint32_t chunks;
   uint32_t first[kSquares];
@@ -618,11 +654,11 @@ __device__ __forceinline__ float squares(const Square& e, int64_t i0, int64_t en
 
 // A block sums the squares of a run of chunks.
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ SquareTable a) {
-  __shared__ float red[kWarps];
+  __shared__ double red[kWarps];
   wait_for_prior();
   const uint32_t c0 = (uint32_t)((uint64_t)a.chunks * blockIdx.x / gridDim.x);
   const uint32_t c1 = (uint32_t)((uint64_t)a.chunks * (blockIdx.x + 1) / gridDim.x);
-  float sum = 0.f;
+  double sum = 0.0;  // (a thread's 32 elements of a chunk are summed in float32)
   int t = tensor_of(a.first, a.count, c0);
   for (uint32_t c = c0; c < c1; ++c) {
     while (t + 1 < a.count && a.first[t + 1] <= c) ++t;
@@ -636,7 +672,8 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
     else
       sum += squares<__half>(e, i0, end);
   }
-  sum = warp_sum(sum);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -646,12 +683,12 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
 }
 
 // The root of the parts' sum, in a fixed order.
-__global__ void __launch_bounds__(1024) norm_root_kernel(const float* part, int parts,
+__global__ void __launch_bounds__(1024) norm_root_kernel(const double* part, int parts,
                                                          float* norm) {
   __shared__ double red[32];
   wait_for_prior();
   double sum = 0.0;
-  for (int p = threadIdx.x; p < parts; p += 1024) sum += (double)part[p];
+  for (int p = threadIdx.x; p < parts; p += 1024) sum += part[p];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
@@ -744,7 +781,7 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
     h.step_size = (float)(y.lr / (1.0 - std::pow(y.beta1, t)));
     h.inv_root = (float)(1.0 / std::sqrt(1.0 - std::pow(y.beta2, t)));
     h.log1 = (float)std::log(y.beta1), h.log2 = (float)std::log(y.beta2);
-    h.scale = (float)y.scale, h.max_norm = (float)y.max_norm;
+    h.scale = (float)y.scale, h.max_norm = (float)y.max_norm, h.one = 1.f;
     h.lr_device = y.lr_device, h.step_device = y.step_device, h.norm = y.norm;
     h.step = (uint64_t)y.step;
     uint32_t k0 = (uint32_t)y.seed, k1 = (uint32_t)(y.seed >> 32);
@@ -769,7 +806,7 @@ int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_ada
 uint64_t rot_gradient_norm_work_bytes(int32_t count) {
   if (count < 0) return 0;
   const uint64_t launches = std::max<uint64_t>(1, ((uint64_t)count + kSquares - 1) / kSquares);
-  return align256(4ull * kSquareBlocks * launches);
+  return align256(8ull * kSquareBlocks * launches);
 }
 
 int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm, void* work,
@@ -794,7 +831,7 @@ int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm,
     const unsigned most = (unsigned)std::min(kSquareBlocks, 6 * sm_count());
     for (int32_t at = 0; at < count;) {
       SquareTable t;
-      t.part = static_cast<float*>(work) + parts;
+      t.part = static_cast<double*>(work) + parts;
       t.count = 0;
       uint64_t chunks = 0;
       double bytes = 0.0;
@@ -815,7 +852,7 @@ int rot_gradient_norm(const rot_gradient* gradients, int32_t count, float* norm,
       parts += (int)blocks;
     }
     ProfScope prof(ROT_PROF_ELEMENTWISE, 0.0, s);
-    return launch_behind(norm_root_kernel, 1, 1024, 0, s, (const float*)work, parts, norm);
+    return launch_behind(norm_root_kernel, 1, 1024, 0, s, (const double*)work, parts, norm);
   });
 }
 
