@@ -6,6 +6,11 @@
 // tensor, found by bisection in the tensors' first chunks.  A lane takes four
 // or eight consecutive elements: whole calls of the generator, and 16 lanes
 // share a scale.
+//
+// 352 million elements: float32 with the norm before it 1586 us (7.1 TB/s);
+// bfloat16 with 8-bit states 702 us (5.0 TB/s), where 57 instructions an element
+// bound it (the generator takes 10 of them); 205 million with float32 masters,
+// 8-bit states and the norm 591 us (6.3 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -19,8 +24,11 @@ namespace ops {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the gradients' squares
-// A block's threads, the elements that a lane takes at once and how often, and
-// the blocks per SM that the registers are made to fit.
+// A block's threads, the elements that a lane takes at once and how often.
+// (8-bit states, 352 million elements in bfloat16: 64 threads 690 us, 128 747,
+// 256 1030; eight turns 690 us, two 747, sixteen 683.  The blocks per SM at the
+// kernel are those whose registers spill least: one more or less is 1 to 8%
+// slower.)
 constexpr int threads_of(bool eight) { return eight ? 64 : 256; }
 constexpr int lane_elements(bool eight) { return eight ? 8 : 4; }
 constexpr int times_of(bool eight) { return eight ? 8 : 4; }

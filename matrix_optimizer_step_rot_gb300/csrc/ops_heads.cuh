@@ -17,6 +17,11 @@
 // Rows come by asynchronous copies a few passes ahead; a lane copies and reads
 // its own runs alone, so that no lane waits for another's.  (Single 16-bit
 // elements, which such copies do not take: the next pass's in registers.)
+//
+// 16384 tokens of 16 and 8 heads of 128 in bfloat16: rotation 34.5 us, norm and
+// rotation 34.1 (5.9 TB/s of 201 MB), backward 54.7 (5.5 TB/s of 302 MB), of
+// which the join is 3.  With queries and keys on warps of their own (angles
+// twice) and one pass of register loads ahead: 48, 66 and 141.
 #pragma once
 
 #include <algorithm>
@@ -32,7 +37,8 @@ enum HeadsMode { kRotate = 0, kNorm = 1, kNormGrad = 2 };
 constexpr int kHeadWarps = 4;     // per block
 constexpr int kHeadParts = 1024;  // most blocks of a backward pass: its partial sums
 // Blocks per SM that stay, and that the registers are made to fit; passes that
-// are on their way.
+// are on their way.  (Forward 6 blocks, of 80 registers: 39.7 us; 4 with 4
+// passes: 34.8.  Backward 4 blocks, of 128 registers, spill: 82 us; 2: 66.)
 constexpr int head_blocks(HeadsMode mode, int runs) {
   return mode == kNormGrad ? (runs > 2 ? 2 : 3) : (runs > 2 ? 3 : 5);
 }
@@ -705,7 +711,7 @@ int launch_heads_as(HeadArgs& q, int64_t tokens, bool il, cudaStream_t s) {
   // a token's passes to one warp, or to as many as end first, a token's angles
   // counted as a pass (few tokens, or a few more than there are warps)
   int64_t best = INT64_MAX;
-  for (int n = 1; n <= std::min(q.passes, 16); ++n) {
+  for (int n = 1; n <= q.passes; n += n < 16 ? 1 : n) {
     const int chunk = (q.passes + n - 1) / n;
     const int64_t items = tokens * ((q.passes + chunk - 1) / chunk);
     if (n > 1 && items > int64_t(1) << 31) break;  // (they are counted in 32 bits)

@@ -120,6 +120,10 @@ CASES = [
     (1, 40, 9, 5, 128, 128, False, BF16, "plain", "int64"),  # groups past the last head
     (1, 2900, 9, 5, 128, 128, True, F16, "fused", "int64"),
     (1, 700, 1, 1, 256, 128, False, BF16, "first", "int32"),
+    (1, 1, 300, 7, 512, 512, False, F32, "plain", "int64"),  # one token's heads over many warps
+    (1, 2, 1000, 1, 40, 20, True, BF16, "odd", "int64"),
+    (1, 1, 4000, 500, 128, 128, False, BF16, "plain", "start"),
+    (3, 700, 1, 1, 128, 128, False, BF16, "plain", "int64"),  # a few more tokens than warps
     (2, 2500, 16, 8, 128, 128, False, BF16, "fused", "int64"),
     (1, 3000, 3, 3, 40, 20, True, F16, "fused", "int32"),
 ]
@@ -403,6 +407,34 @@ def test_streams_and_graphs():
     assert all(torch.equal(a, b) for a, b in zip(fresh, captured))
     second.replay()
     assert all(torch.equal(a, b) for a, b in zip(fresh, again))
+
+
+def test_two_threads_at_once():
+    """Calls of two threads, each on a stream of its own: the same bits as alone."""
+    import threading
+
+    w, rotary = torch.rand(128, generator=gen(12), device="cuda"), rotary_of(128, True)
+    xs = [torch.randn(200, 6, 128, generator=gen(30 + i), device="cuda").bfloat16() for i in range(2)]
+
+    def work(x, stream=None):
+        y = ops.head_norm(x, w, x, w, rotary=rotary, start=9, stream=stream)
+        return [*y, *ops.head_norm_backward(y[0], x, w, y[1], x, w, rotary=rotary, start=9, stream=stream)]
+
+    want, got = [work(x) for x in xs], [None, None]
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i] = work(xs[i], s)
+        s.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(a, b) for p, q in zip(want, got) for a, b in zip(p, q))
 
 
 def test_refusals():
