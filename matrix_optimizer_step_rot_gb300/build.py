@@ -68,7 +68,7 @@ def _torch_command():
            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
            TORCH_SRC, "-o", TORCH_EXT + ".tmp", "-L", os.path.join(root, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     newest = max(map(os.path.getmtime, [TORCH_SRC, *_headers()]))
     if os.path.exists(TORCH_EXT) and os.path.exists(TORCH_STAMP) \
             and open(TORCH_STAMP).read() == _torch_stamp(cmd) and os.path.getmtime(TORCH_EXT) > newest:
