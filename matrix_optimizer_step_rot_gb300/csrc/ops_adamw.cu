@@ -7,10 +7,10 @@
 // or eight consecutive elements: whole calls of the generator, and 16 lanes
 // share a scale.
 //
-// 352 million elements: float32 with the norm before it 1586 us (7.1 TB/s);
-// bfloat16 with 8-bit states 702 us (5.0 TB/s), where 57 instructions an element
+// 352 million elements: float32 with the norm before it 1585 us (7.1 TB/s);
+// bfloat16 with 8-bit states 705 us (5.0 TB/s), where 57 instructions an element
 // bound it (the generator takes 10 of them); 205 million with float32 masters,
-// 8-bit states and the norm 591 us (6.3 TB/s).
+// 8-bit states and the norm 592 us (6.3 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

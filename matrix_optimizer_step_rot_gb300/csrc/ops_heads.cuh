@@ -18,8 +18,8 @@
 // its own runs alone, so that no lane waits for another's.  (Single 16-bit
 // elements, which such copies do not take: the next pass's in registers.)
 //
-// 16384 tokens of 16 and 8 heads of 128 in bfloat16: rotation 34.5 us, norm and
-// rotation 34.1 (5.9 TB/s of 201 MB), backward 54.7 (5.5 TB/s of 302 MB), of
+// 16384 tokens of 16 and 8 heads of 128 in bfloat16: rotation 34.9 us, norm and
+// rotation 34.0 (5.9 TB/s of 201 MB), backward 54.8 (5.5 TB/s of 302 MB), of
 // which the join is 3.  With queries and keys on warps of their own (angles
 // twice) and one pass of register loads ahead: 48, 66 and 141.
 #pragma once
