@@ -491,7 +491,8 @@ def gradient_norm(grads: Sequence[torch.Tensor], *, stream=None) -> torch.Tensor
     contiguous tensors of any types and shapes, in two launches for up to a
     thousand of them."""
     if stream is not None:
-        return _on(stream, lambda: gradient_norm(grads), list(grads))
+        grads = list(grads)  # (read twice)
+        return _on(stream, lambda: gradient_norm(grads), grads)
     return (_native or _load()).gradient_norm(grads)
 
 
@@ -512,12 +513,13 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequ
     the random rounding's, whose other half is the step: calls of the same step
     need different ones.  State and masters that are given twice are refused."""
     if stream is not None:
+        params, grads, m, v = list(params), list(grads), list(m), list(v)  # (read twice)
+        masters = None if masters is None else list(masters)
         return _on(stream, lambda: adamw(params, grads, m, v, step, lr=lr, beta1=beta1,
                                          beta2=beta2, eps=eps, weight_decay=weight_decay,
                                          masters=masters, norm=norm, max_norm=max_norm,
                                          scale=scale, seed=seed),
-                   list(params), list(grads), list(m), list(v), masters and list(masters), norm,
-                   step, lr)
+                   params, grads, m, v, masters, norm, step, lr)
     on = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
     (_native or _load()).adamw(params, grads, m, v, masters, 1 if on[0] else step,
                                step if on[0] else None, 0.0 if on[1] else lr,

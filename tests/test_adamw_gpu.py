@@ -428,6 +428,22 @@ def test_streams_and_graphs():
                 assert all(torch.equal(p, q) for p, q in zip(a.moments(i), b.moments(i)))
 
 
+def test_lists_that_can_be_read_once():
+    """Generators, on the current stream and on another one."""
+    x = lists([500, 70], BF16, F32, True, 8, 15)
+    want, norm = cloned(x), ops.gradient_norm(x["g"])
+    call(want, 3)
+    s = torch.cuda.Stream()
+    for stream in (None, s):
+        y = cloned(x)
+        s.wait_stream(torch.cuda.current_stream())
+        assert torch.equal(ops.gradient_norm((g for g in x["g"]), stream=stream), norm)
+        ops.adamw(iter(y["p"]), iter(y["g"]), iter(y["m"]), iter(y["v"]), 3, masters=iter(y["master"]), seed=SEED,
+                  stream=stream, **HYPER)
+        torch.cuda.current_stream().wait_stream(s)
+        assert same(y, want) and not torch.equal(y["p"][0], x["p"][0])
+
+
 def test_optimizer_object():
     p = [torch.randn(7, 33, generator=gen(1), device="cuda"), torch.randn(50, generator=gen(2), device="cuda").half()]
     opt = AdamW([t.clone() for t in p], lr=1e-2, weight_decay=0.1)
