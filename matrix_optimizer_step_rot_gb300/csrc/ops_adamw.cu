@@ -313,13 +313,14 @@ __device__ __forceinline__ float2 plus2(float2 x, float one, float2 y) {
   return fma2(x, both(one), y);
 }
 
-// The roots of x, which are 0 or positive: r = s - (s^2 - x) / (2 s), Heron's
-// step on an approximation s from the reciprocal root.  s is within two last
-// places, the difference is exact (in one rounding) and its quotient small, so
-// that r is the nearest number but where the root lies within 2^-20 of a last
-// place of the middle of two.  Where an x is too small for that (the
-// difference would not be exact below 2^-100) or not finite, by the library.
-// top: the largest.
+// The roots of x, which are 0 or positive, to the nearest number: Newton's
+// iteration with the residual in one rounding (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", IBM Journal of
+// Research and Development 34, 1990), r = s - (s^2 - x) / (2 s).  s, x times an
+// approximate reciprocal root, is within two last places; the residual is
+// exact, and its quotient good to 2^-20 of a last place.  Where an x is too
+// small for that (the residual would not be exact below 2^-100) or not finite,
+// the library's function.  top: the largest.
 template <int H>
 __device__ __forceinline__ void roots(const float2 (&x)[H], float2 (&r)[H], float& top) {
   float low = 0x1p127f;

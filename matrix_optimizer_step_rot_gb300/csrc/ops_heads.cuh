@@ -1,7 +1,6 @@
 // Rotary positions and the norm of queries and keys (include/rot_ops.h): one
 // kernel for the rotation, the norm with it, and the norm's backward pass.
-// Bound by HBM: each element is read once (twice two arrays backward) and
-// written once.
+// Bound by HBM: every array is read once and written once.
 //
 // A row is one head of one token.  A group of 2^k lanes takes it, a lane two
 // runs of V elements: those whose elements turn together.  For pairs (i, i +

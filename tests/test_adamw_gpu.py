@@ -304,6 +304,37 @@ def test_extreme_scales_in_8_bits():
     assert ((m[:128].double() / 3e38 - 1).abs() <= 2.0 ** -3).all()
 
 
+def test_moments_in_8_bits_are_the_float32_steps_rounded_once():
+    """Every float32 step of m, v and the root is the correctly rounded one
+    (torch's products, sums and roots on this device), so that each code and
+    scale is exactly the rounding of it: 2^20 gradients from 2^-40 to 2^40, some
+    chosen so that both terms of m cancel."""
+    n, t, beta1, beta2 = 1 << 20, 12, 0.9, 0.999
+    g = gen(16)
+    x = lists([n], F32, BF16, False, 8, 16)
+    size = torch.exp2(torch.randint(-40, 41, (n // 128,), generator=g, device="cuda").float()).repeat_interleave(128)
+    x["g"][0].copy_(x["g"][0].float() * size)
+    old = x["m"][0].dequantize()
+    x["g"][0][:: 7] = (-9.0 * old[:: 7]).to(BF16)
+    root = x["v"][0].dequantize()
+    grad = x["g"][0].float()
+    call(x, t, beta1=beta1, beta2=beta2)
+    m = beta1 * old + (1 - beta1) * grad
+    v = beta2 * (root * root) + (1 - beta2) * grad * grad
+    part = torch.from_numpy((ref.words(0, n, t, SEED) & 0xFFFF) * 16 + 8).cuda()
+    assert (m == 0).sum() > 100
+    for name, want in (("m", m), ("v", v.sqrt())):
+        top, k = torch.frexp(want.view(-1, 128).abs().amax(1))
+        e = (k - 9 + (top > 0.875).int()).repeat_interleave(128)
+        bits = torch.ldexp(want, -e - 120).view(torch.int32).long() & 0xFFFFFFFF
+        code = (((bits & 0x7FFFFFFF) + part) >> 20) | (bits >> 24 & 0x80)
+        if name == "v":
+            code = torch.where((want > 0) & (code == 0), 1, code)
+        got = x[name][0]
+        assert torch.equal(got.scale.int(), e[::128] + 127), name
+        assert torch.equal(got.data.view(torch.uint8).long(), code), name
+
+
 def test_random_rounding_keeps_the_average():
     """600 steps without gradients: v falls by beta2 each, its root by 0.26 in
     all, in steps of 0.0005 of it, where the nearest E4M3 number is itself.  The
