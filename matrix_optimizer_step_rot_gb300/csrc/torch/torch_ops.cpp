@@ -616,7 +616,8 @@ struct List {
   PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(keep.ptr(), i); }
 };
 const Tensor& tensor_of(PyObject* o, const char* name) {
-  if (!THPVariable_Check(o)) fail(std::string(name) + ": expected tensors, got " + Py_TYPE(o)->tp_name);
+  if (!THPVariable_CheckExact(o) && !THPVariable_Check(o))
+    fail(std::string(name) + ": expected tensors, got " + Py_TYPE(o)->tp_name);
   return THPVariable_Unpack(o);
 }
 
