@@ -314,8 +314,8 @@ int rot_fp8_linear_backward(int64_t tokens, int64_t inner, int64_t outer, const 
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * in float32, p read from and written to `master` where that is given (p then
- * receives its value, rounded to nearest).  A norm that is not finite and a
- * device step below 1 leave every tensor as it was.
+ * receives its value, rounded to nearest).  A product |scale| norm that is not
+ * finite in float32 and a device step below 1 leave every tensor as it was.
  *
  * States in 8 bits: m and sqrt(v) as E4M3 numbers, under one power-of-two
  * scale for every 128 consecutive elements (a byte e for 2^(e - 127), 255 for
@@ -365,6 +365,18 @@ typedef struct rot_adamw_hyper {
  * not above 0). */
 int rot_adamw_step(const rot_adamw_tensor* tensors, int32_t count, const rot_adamw_hyper* hyper,
                    void* stream);
+
+/* The same with t counted on the device: `taken` (one int64) holds the steps
+ * taken so far, t is one more, and the word moves on to t unless the norm keeps
+ * the step from being taken; hyper's step and step_device are not looked at.
+ * The corrections 1 - beta^t are float64, rounded as rot_adamw_step's of a step
+ * given by the host.  A call of no tensors counts, too.
+ * work: ROT_ADAMW_COUNT_BYTES of device memory.
+ * Errors: as rot_adamw_step, plus null or misaligned (8 bytes; work 16) taken
+ * and work. */
+#define ROT_ADAMW_COUNT_BYTES 32
+int rot_adamw_step_counted(const rot_adamw_tensor* tensors, int32_t count,
+                           const rot_adamw_hyper* hyper, int64_t* taken, void* work, void* stream);
 
 /* Workspace bytes of rot_gradient_norm (256-byte aligned device memory). */
 uint64_t rot_gradient_norm_work_bytes(int32_t count);

@@ -162,6 +162,8 @@ _SIGS = {
                                       _vp, _u64, _vp]),
     "rot_adamw_step": (_i32, [ctypes.POINTER(rot_adamw_tensor), _i32,
                               ctypes.POINTER(rot_adamw_hyper), _vp]),
+    "rot_adamw_step_counted": (_i32, [ctypes.POINTER(rot_adamw_tensor), _i32,
+                                      ctypes.POINTER(rot_adamw_hyper), _vp, _vp, _vp]),
     "rot_gradient_norm_work_bytes": (_u64, [_i32]),
     "rot_gradient_norm": (_i32, [ctypes.POINTER(rot_gradient), _i32, _vp, _vp, _u64, _vp]),
     "rot_item_work": (_i32, [ctypes.POINTER(rot_shape), _i32, ctypes.POINTER(_u64)]),

@@ -46,6 +46,7 @@ namespace {
   X(rot_head_norm_work_bytes) \
   X(rot_head_norm_backward)   \
   X(rot_adamw_step)           \
+  X(rot_adamw_step_counted)   \
   X(rot_gradient_norm_work_bytes) \
   X(rot_gradient_norm)
 
@@ -655,7 +656,7 @@ void* state_of(PyObject* o, const char* name, int64_t n, Current& device, uint8_
 
 void adamw(const py::object& params, const py::object& grads, const py::object& m,
            const py::object& v, const py::object& masters, int64_t step,
-           const MaybeTensor& step_device, double lr, const MaybeTensor& lr_device, double beta1,
+           const MaybeTensor& step_device, bool counts, double lr, const MaybeTensor& lr_device, double beta1,
            double beta2, double eps, double weight_decay, const MaybeTensor& norm, double max_norm,
            double scale, uint64_t seed) {
   const List ps(params, "params"), gs(grads, "grads"), m1(m, "m"), v1(v, "v");
@@ -696,7 +697,15 @@ void adamw(const py::object& params, const py::object& grads, const py::object& 
   h.lr_device = word_of<float>(lr_device, "lr", at::kFloat, device);
   h.step_device = word_of<int64_t>(step_device, "step", at::kLong, device);
   h.norm = word_of<float>(norm, "norm", at::kFloat, device);
-  check(lib.rot_adamw_step(list.data(), (int32_t)n, &h, stream()), "rot_adamw_step");
+  if (!counts) {
+    check(lib.rot_adamw_step(list.data(), (int32_t)n, &h, stream()), "rot_adamw_step");
+    return;
+  }
+  if (!step_device) fail("counts: expected a step on the device");
+  Tensor work = bytes(ROT_ADAMW_COUNT_BYTES, *step_device);
+  check(lib.rot_adamw_step_counted(list.data(), (int32_t)n, &h, step_device->data_ptr<int64_t>(),
+                                   work.data_ptr(), stream()),
+        "rot_adamw_step_counted");
 }
 
 Tensor gradient_norm(const py::object& grads) {

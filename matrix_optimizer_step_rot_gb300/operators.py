@@ -501,15 +501,17 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequ
           eps: float = 1e-8, weight_decay: float = 0.0,
           masters: Optional[Sequence[Optional[torch.Tensor]]] = None,
           norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, scale: float = 1.0,
-          seed: int = 0, stream=None) -> None:
+          seed: int = 0, counts: bool = False, stream=None) -> None:
     """One AdamW step of all `params`, in place, with their states and masters:
     contiguous tensors of any shapes; float32 (and bfloat16, rounded at random)
     parameters, or 16-bit ones with a float32 master; gradients of any type;
     states as adamw_state() makes them.  Gradients are multiplied by `scale`,
     and clipped to max_norm where `norm` (gradient_norm()'s of them before
-    `scale`) is given; a norm that is not finite leaves everything as it was.
-    step counts from 1; it and lr may be tensors of one element on the device
-    (int64, float32), which a captured call reads when it is replayed.  seed:
+    `scale`) is given; where |scale| norm is not finite everything stays as it
+    was.  step counts from 1; it and lr may be tensors of one element on the
+    device (int64, float32), which a captured call reads when it is replayed.
+    counts: step, a tensor, holds the steps taken so far, this call is the one
+    after them, and it moves step on unless the norm has it not taken.  seed:
     the random rounding's, whose other half is the step: calls of the same step
     need different ones.  State and masters that are given twice are refused."""
     if stream is not None:
@@ -518,10 +520,10 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequ
         return _on(stream, lambda: adamw(params, grads, m, v, step, lr=lr, beta1=beta1,
                                          beta2=beta2, eps=eps, weight_decay=weight_decay,
                                          masters=masters, norm=norm, max_norm=max_norm,
-                                         scale=scale, seed=seed),
+                                         scale=scale, seed=seed, counts=counts),
                    params, grads, m, v, masters, norm, step, lr)
     on = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
     (_native or _load()).adamw(params, grads, m, v, masters, 1 if on[0] else step,
-                               step if on[0] else None, 0.0 if on[1] else lr,
+                               step if on[0] else None, counts, 0.0 if on[1] else lr,
                                lr if on[1] else None, beta1, beta2, eps, weight_decay, norm,
                                max_norm, scale, _word(seed, "seed"))

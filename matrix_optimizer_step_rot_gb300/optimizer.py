@@ -66,13 +66,15 @@ class RotatedAdam:
 
 class AdamW:
     """AdamW over the parameters that RotatedAdam does not take (vectors,
-    embeddings; operators.adamw): keeps their moments and counts the steps.
+    embeddings; operators.adamw): keeps their moments and counts the steps taken
+    (`count`).  Only the device knows whether a norm lets a step be taken, so from
+    the first step with one the count is a tensor there.
 
     bits: 32 or 8, of the moments.  masters: float32 masters of 16-bit
     parameters (float16 always has one; bfloat16 without is rounded at random).
     seed: the random rounding's; instances that step in the same run need
-    different ones.  captured: the step's number is kept on the device, so that
-    a captured step() counts on when it is replayed."""
+    different ones.  captured: the count is on the device from the start, so
+    that a captured step() counts on when it is replayed."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, beta1: float = 0.9,
                  beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, *,
@@ -84,22 +86,26 @@ class AdamW:
         self.masters = [p.float() if keep.get(p.dtype, False) else None for p in self.params]
         self.lr, self.hyper = lr, dict(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
         self.seed = seed
-        self.count = 0
-        if captured:
-            device = self.params[0].device if self.params else "cuda"
-            self.count = torch.zeros(1, dtype=torch.int64, device=device)
+        self.count = self._on_device(0) if captured else 0
+
+    def _on_device(self, count: int) -> torch.Tensor:
+        device = self.params[0].device if self.params else "cuda"
+        return torch.full((1,), count, dtype=torch.int64, device=device)
 
     def step(self, grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
              max_norm: float = 1.0, scale: float = 1.0, stream=None) -> None:
         """One step; norm, max_norm, scale as operators.adamw."""
-        if stream is not None:
+        count = self.count
+        if norm is not None and not isinstance(count, torch.Tensor):
             with torch.cuda.stream(stream):
-                self.count += 1
-        else:
-            self.count += 1
-        ops.adamw(self.params, grads, self.m, self.v, self.count, lr=self.lr,
+                # (captured like this, a step has its number for good)
+                if torch.cuda.is_available() and not torch.cuda.is_current_stream_capturing():
+                    count = self._on_device(count)
+        counts = isinstance(count, torch.Tensor)
+        ops.adamw(self.params, grads, self.m, self.v, count if counts else count + 1, lr=self.lr,
                   masters=self.masters, norm=norm, max_norm=max_norm, scale=scale, seed=self.seed,
-                  stream=stream, **self.hyper)
+                  counts=counts, stream=stream, **self.hyper)
+        self.count = count if counts else count + 1  # (of a call that was not refused)
 
     def moments(self, item: int) -> Tuple[torch.Tensor, torch.Tensor]:
         """(m, v) of a parameter in float32."""
