@@ -83,7 +83,7 @@ class AdamW:
         states = [ops.adamw_state(p, bits=bits) for p in self.params]
         self.m, self.v = [s[0] for s in states], [s[1] for s in states]
         keep = {torch.float16: True, torch.bfloat16: masters}
-        self.masters = [p.float() if keep.get(p.dtype, False) else None for p in self.params]
+        self.masters = [p.detach().float() if keep.get(p.dtype, False) else None for p in self.params]
         self.lr, self.hyper = lr, dict(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
         self.seed = seed
         self.count = self._on_device(0) if captured else 0

@@ -43,3 +43,15 @@ def test_the_device_count_is_refused_where_it_cannot_be():
     for step in (1, 3.0):
         with pytest.raises((ValueError, TypeError)):
             ops.adamw([], [], [], [], step, lr=0.1, counts=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_masters_keep_no_graph_of_their_parameters(dtype):
+    """(A live graph of a leaf holds its gradient's node, and with it the stream that a captured backward pass would
+    then have to use.)"""
+    w = torch.randn(5, 7).to(dtype).requires_grad_()
+    opt = AdamW([w], masters=True)
+    master = opt.masters[0]
+    assert not master.requires_grad and master.grad_fn is None and master.dtype == torch.float32
+    assert torch.equal(master, w.detach().float()) and opt.params[0] is w
+    assert not any(t.requires_grad for t in (opt.m[0], opt.v[0]))

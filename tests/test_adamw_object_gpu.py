@@ -128,3 +128,30 @@ def test_a_refused_step_leaves_everything(captured):
     for opt in (a, b):
         opt.step(gradients(1), norm=norm)
     assert int(a.count) == 1 and same(a, b)
+
+
+def test_a_training_step_captured_while_the_object_lives():
+    """Forward and backward pass and the step in one graph, with masters of leaves that require gradients."""
+    x = torch.randn(16, 32, generator=gen(1), device="cuda").half()
+    first = torch.randn(32, generator=gen(2), device="cuda").half()
+    w, u = (first.clone().requires_grad_() for _ in range(2))
+    a, b = (AdamW([t], lr=1e-2, captured=True) for t in (w, u))
+
+    def step(w, opt):
+        (grad,) = torch.autograd.grad((x * w).float().square().mean(), w)
+        opt.step([grad], norm=ops.gradient_norm([grad]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for opt, leaf in ((a, w), (b, u)):
+            step(leaf, opt)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(w, a)
+    for k in range(3):
+        graph.replay()
+        step(u, b)
+    assert a.count.item() == 4 and torch.equal(w, u) and torch.equal(a.masters[0], b.masters[0])
+    assert not torch.equal(w, first)
