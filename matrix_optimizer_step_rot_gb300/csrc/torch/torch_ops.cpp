@@ -660,10 +660,10 @@ void adamw(const py::object& params, const py::object& grads, const py::object& 
            double beta2, double eps, double weight_decay, const MaybeTensor& norm, double max_norm,
            double scale, uint64_t seed) {
   const List ps(params, "params"), gs(grads, "grads"), m1(m, "m"), v1(v, "v");
-  const bool has_masters = !masters.is_none();
-  const List ms(has_masters ? masters : params, "masters");
+  std::optional<List> ms;
+  if (!masters.is_none()) ms.emplace(masters, "masters");
   const Py_ssize_t n = ps.size;
-  if (gs.size != n || m1.size != n || v1.size != n || ms.size != n)
+  if (gs.size != n || m1.size != n || v1.size != n || (ms && ms->size != n))
     fail("grads, m, v, masters: expected an entry for each parameter");
   Current device;
   std::vector<rot_adamw_tensor> list(n);
@@ -682,8 +682,8 @@ void adamw(const py::object& params, const py::object& grads, const py::object& 
     if (!t.m_scale != !t.v_scale && t.n > 0)
       fail("m, v: one in 8 bits, the other not");
     t.master = nullptr;
-    if (has_masters && ms[i] != Py_None) {
-      const Tensor& w = tensor_of(ms[i], "masters");
+    if (ms && (*ms)[i] != Py_None) {
+      const Tensor& w = tensor_of((*ms)[i], "masters");
       if (w.scalar_type() != at::kFloat) fail("masters: expected float32 tensors");
       t.master = static_cast<float*>(flat(w, "masters", t.n, device));
       if (t.p_type == ROT_TYPE_F32) fail("masters: a float32 parameter has none");

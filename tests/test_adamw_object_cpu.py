@@ -55,3 +55,13 @@ def test_masters_keep_no_graph_of_their_parameters(dtype):
     assert not master.requires_grad and master.grad_fn is None and master.dtype == torch.float32
     assert torch.equal(master, w.detach().float()) and opt.params[0] is w
     assert not any(t.requires_grad for t in (opt.m[0], opt.v[0]))
+
+
+def test_parameters_that_can_be_read_once_are_read_once():
+    """Without masters: past the lists' lengths, so that what is refused is where the tensors are."""
+    w = torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.adamw(iter([w]), iter([w]), iter([w]), iter([w]), 1, lr=0.1)
+    for masters in ([], [None, None], iter([])):
+        with pytest.raises(ValueError, match="an entry for each parameter"):
+            ops.adamw([w], [w], [w], [w], 1, lr=0.1, masters=masters)

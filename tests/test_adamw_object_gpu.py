@@ -155,3 +155,17 @@ def test_a_training_step_captured_while_the_object_lives():
         step(u, b)
     assert a.count.item() == 4 and torch.equal(w, u) and torch.equal(a.masters[0], b.masters[0])
     assert not torch.equal(w, first)
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_lists_that_can_be_read_once_without_masters(other):
+    stream = torch.cuda.Stream() if other else None
+    p, q, g = parameters(), parameters(), gradients(1)
+    states = [[ops.adamw_state(t) for t in p] for _ in range(2)]
+    ops.adamw(p, g, [s[0] for s in states[0]], [s[1] for s in states[0]], 1, lr=1e-2)
+    if other:
+        stream.wait_stream(torch.cuda.current_stream())
+    ops.adamw(iter(q), iter(g), (s[0] for s in states[1]), (s[1] for s in states[1]), 1, lr=1e-2, stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(p, q))
+    assert all(torch.equal(a, b) for x, y in zip(*states) for a, b in zip(x, y))
