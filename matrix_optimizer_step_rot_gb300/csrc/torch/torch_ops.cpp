@@ -608,6 +608,7 @@ struct List {
   List(const py::object& o, const char* name) {
     PyObject* p = PySequence_Fast(o.ptr(), "");
     if (!p) {
+      if (!PyErr_ExceptionMatches(PyExc_TypeError)) throw py::error_already_set();  // (its own)
       PyErr_Clear();
       fail(std::string(name) + ": expected a list");
     }

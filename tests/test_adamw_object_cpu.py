@@ -65,3 +65,18 @@ def test_parameters_that_can_be_read_once_are_read_once():
     for masters in ([], [None, None], iter([])):
         with pytest.raises(ValueError, match="an entry for each parameter"):
             ops.adamw([w], [w], [w], [w], 1, lr=0.1, masters=masters)
+
+
+def test_an_error_of_the_callers_generator_is_passed_on():
+    def broken():
+        yield torch.zeros(8)
+        raise KeyError("the caller's own")
+
+    w = torch.zeros(8)
+    with pytest.raises(KeyError, match="the caller's own"):
+        ops.gradient_norm(broken())
+    with pytest.raises(KeyError, match="the caller's own"):
+        ops.adamw([w], broken(), [w], [w], 1, lr=0.1)
+    for bad in (3, None, object()):
+        with pytest.raises(ValueError, match="expected a list"):
+            ops.gradient_norm(bad)
