@@ -163,6 +163,15 @@ Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const Tensor& like) {
 Tensor floats(at::IntArrayRef sizes, const Tensor& like) { return fresh(sizes, at::kFloat, like); }
 Tensor bytes(uint64_t n, const Tensor& like) { return fresh({(int64_t)n}, at::kByte, like); }
 
+// A tensor that was there has been written: what autograd has saved of it no
+// longer is what it holds.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const MaybeTensor& t) {
+  if (t) written(*t);
+}
+
 // ------------------------------------------------------------------ dropout
 Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset,
                const MaybeTensor& residual, const MaybeTensor& out) {
@@ -172,6 +181,7 @@ Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset,
   check(lib.rot_dropout(a.p, a.ld, r.p, r.ld, o.p, o.ld, a.rows, a.cols, type_of(x), p, seed,
                         offset, stream()),
         "rot_dropout");
+  written(out);
   return y;
 }
 
@@ -258,6 +268,7 @@ std::tuple<Tensor, Tensor, MaybeTensor> policy_loss(
                             z.cols, type_of(logits), (float)clip_low, (float)clip_high,
                             (float)kl_coef, (float)grad_scale, stream()),
         "rot_policy_loss");
+  if (grad) written(out);
   return {loss, logp, d};
 }
 
@@ -371,6 +382,7 @@ Tensor fp8_matmul(const Tensor& ad, const Tensor& as, int64_t ar, const Tensor& 
                          need ? work.data_ptr() : nullptr, need,
                          reinterpret_cast<int32_t*>(status), stream()),
         "rot_fp8_gemm");
+  written(out);
   return c;
 }
 
@@ -421,6 +433,7 @@ std::tuple<Tensor, Tensor> fp8_linear_backward(const Tensor& dy, const Tensor& x
                                     need ? work.data_ptr() : nullptr, need,
                                     reinterpret_cast<int32_t*>(status), stream()),
         "rot_fp8_linear_backward");
+  written(dw);
   return {dx, g};
 }
 
@@ -512,6 +525,7 @@ std::tuple<Tensor, MaybeTensor> rotate(const Tensor& q, const MaybeTensor& k, co
   check(lib.rot_rotate(&a, &b, k ? &c : nullptr, k ? &d : nullptr, s.batch, s.tokens, s.dim,
                        type_of(q), r.p, inverse, stream()),
         "rot_rotate");
+  written(out), written(k_out);
   return {y, z};
 }
 
@@ -546,6 +560,7 @@ std::tuple<Tensor, MaybeTensor> head_norm(const Tensor& q, const Tensor& q_weigh
                                   type_of(q_weight), s.batch, s.tokens, s.dim, type_of(q),
                                   (float)eps, r.p, stream()),
         "rot_head_norm_forward");
+  written(out), written(k_out);
   return {y, z};
 }
 
@@ -582,6 +597,7 @@ std::tuple<Tensor, MaybeTensor, Tensor, MaybeTensor> head_norm_backward(
                                    s.tokens, s.dim, type_of(dq), (float)eps, r.p, work.data_ptr(),
                                    need, stream()),
         "rot_head_norm_backward");
+  written(out), written(k_out);
   return {y, z, dw, dv};
 }
 
@@ -700,13 +716,20 @@ void adamw(const py::object& params, const py::object& grads, const py::object& 
   h.norm = word_of<float>(norm, "norm", at::kFloat, device);
   if (!counts) {
     check(lib.rot_adamw_step(list.data(), (int32_t)n, &h, stream()), "rot_adamw_step");
-    return;
+  } else {
+    if (!step_device) fail("counts: expected a step on the device");
+    Tensor work = bytes(ROT_ADAMW_COUNT_BYTES, *step_device);
+    check(lib.rot_adamw_step_counted(list.data(), (int32_t)n, &h,
+                                     step_device->data_ptr<int64_t>(), work.data_ptr(), stream()),
+          "rot_adamw_step_counted");
+    written(*step_device);
   }
-  if (!step_device) fail("counts: expected a step on the device");
-  Tensor work = bytes(ROT_ADAMW_COUNT_BYTES, *step_device);
-  check(lib.rot_adamw_step_counted(list.data(), (int32_t)n, &h, step_device->data_ptr<int64_t>(),
-                                   work.data_ptr(), stream()),
-        "rot_adamw_step_counted");
+  // (the moments are the optimizer's own: no graph has them; a counter takes
+  // 12 ns, of a hundred vectors' 14 us a call)
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    written(THPVariable_Unpack(ps[i]));
+    if (list[i].master) written(THPVariable_Unpack((*ms)[i]));
+  }
 }
 
 Tensor gradient_norm(const py::object& grads) {

@@ -16,7 +16,8 @@ device; a tensor of more than two dimensions is rows of its last one.  There is
 no other path than the library's, and no part in torch's autograd: results do
 not require gradients, whatever the inputs do, and the backward functions are
 calls of their own, as the optimizer step is (examples/policy_step.py has them
-together).  The first 8-bit product on a device
+together); but what a call writes in place (moments aside) has its version
+counter moved on, so that a backward pass of torch that saved it fails.  The first 8-bit product on a device
 allocates its status word: let it run before a stream capture.
 """
 

@@ -47,6 +47,8 @@ class RotatedAdam:
                    self.state.data_ptr(), self.work.data_ptr(), b1, b2, eps, lr, refresh,
                    self.precision if precision is None else int(precision), self.rank_rtol,
                    self._stream(stream))
+        # (what autograd has saved of them no longer is what they hold)
+        torch.autograd.graph.increment_version([w for w in W if not w.is_inference()])
 
     def export(self, item: int, which: int) -> torch.Tensor:
         m, n = self.plan.shapes[item]
