@@ -9,6 +9,7 @@
 // The library's entry points come as addresses (bind), so that the one library
 // the process has loaded is the one that runs.
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -505,10 +506,38 @@ Rotation rotation_of(const MaybeTensor& turns, double magnitude, bool interleave
   return o;
 }
 
+// An output must not lie in what other rows are read from or written to: the
+// order of a call's rows is not fixed.  in_place: it may be that tensor itself.
+// (Parts of one buffer that are not dense are held apart by the caller, but for
+// their first elements.)
+void apart(const MaybeTensor& out, const char* name, const MaybeTensor& other,
+           const char* other_name, bool in_place) {
+  if (!out || !other || !out->defined() || !other->defined()) return;
+  const Tensor &a = *out, &b = *other;
+  if (a.numel() == 0 || b.numel() == 0) return;
+  bool over = a.data_ptr() == b.data_ptr();
+  if (over && in_place && a.sizes() == b.sizes()) {
+    over = false;
+    for (int64_t d = 0; d < a.dim(); ++d) over |= a.size(d) > 1 && a.stride(d) != b.stride(d);
+    if (!over) return;
+  }
+  if (over || at::get_overlap_status(a, b) == at::MemOverlapStatus::Partial)
+    fail(std::string(name) + ": overlaps " + other_name);
+}
+void outputs_apart(const MaybeTensor& out, const MaybeTensor& k_out, const MaybeTensor& q,
+                   const MaybeTensor& k) {
+  if (!out && !k_out) return;
+  apart(out, "out", q, "its input", true), apart(k_out, "k_out", k, "its input", true);
+  apart(out, "out", k, "the other side's input", false);
+  apart(k_out, "k_out", q, "the other side's input", false);
+  apart(out, "out", k_out, "k_out", false);
+}
+
 std::tuple<Tensor, MaybeTensor> rotate(const Tensor& q, const MaybeTensor& k, const Tensor& turns,
                                        double magnitude, bool interleaved,
                                        const MaybeTensor& positions, int64_t start, bool inverse,
                                        const MaybeTensor& out, const MaybeTensor& k_out) {
+  outputs_apart(out, k_out, q, k);
   const rot_heads a = heads_of(q, "q", q);
   if (!k && k_out) fail("k_out: there is no k");
   Tensor y = out ? *out : fresh(q.sizes(), q.scalar_type(), q);
@@ -539,6 +568,7 @@ std::tuple<Tensor, MaybeTensor> head_norm(const Tensor& q, const Tensor& q_weigh
                                           bool interleaved, const MaybeTensor& positions,
                                           int64_t start, const MaybeTensor& out,
                                           const MaybeTensor& k_out) {
+  outputs_apart(out, k_out, q, k);
   const rot_heads a = heads_of(q, "q", q);
   if (k.has_value() != k_weight.has_value()) fail("k, k_weight: expected both or neither");
   if (!k && k_out) fail("k_out: there is no k");
@@ -569,6 +599,8 @@ std::tuple<Tensor, MaybeTensor, Tensor, MaybeTensor> head_norm_backward(
     const MaybeTensor& k, const MaybeTensor& k_weight, double eps, const MaybeTensor& turns,
     double magnitude, bool interleaved, const MaybeTensor& positions, int64_t start,
     const MaybeTensor& out, const MaybeTensor& k_out) {
+  outputs_apart(out, k_out, dq, dk);
+  outputs_apart(out, k_out, q, k);
   const rot_heads a = heads_of(dq, "dq", dq), b = like_heads(q, "q", dq, dq);
   if (k.has_value() != k_weight.has_value() || k.has_value() != dk.has_value())
     fail("dk, k, k_weight: expected all or none");

@@ -247,7 +247,8 @@ def rotate(q: torch.Tensor, rotary: Rotary, k: Optional[torch.Tensor] = None, *,
     transposed view), a head's elements next to one another.  positions (int64
     or int32): one for each token, or [tokens] for all batch entries; without,
     token t is at start + t.  out, k_out: written instead of new tensors; may be
-    q and k."""
+    q and k themselves, each its own, and nothing else that the call reads or
+    writes."""
     if stream is not None:
         return _on(stream, lambda: rotate(q, rotary, k, positions=positions, start=start, out=out,
                                           k_out=k_out), q, rotary, k, positions, out, k_out)
