@@ -25,10 +25,10 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the gradients' squares
 // A block's threads, the elements that a lane takes at once and how often.
-// (8-bit states, 352 million elements in bfloat16: 64 threads 690 us, 128 747,
-// 256 1030; eight turns 690 us, two 747, sixteen 683.  The blocks per SM at the
-// kernel are those whose registers spill least: one more or less is 1 to 8%
-// slower.)
+// (8-bit states, 352 million elements in bfloat16: 64 threads 703 us, 128 917,
+// 256 1519; eight turns 703 us, two 820, sixteen 688; an embedding of 205 million
+// with masters and the norm 592 us, 663, 938; 604, 596.  Blocks per SM: one more
+// is 5 and 12% slower, one fewer 1% faster and 4% slower.)
 constexpr int threads_of(bool eight) { return eight ? 64 : 256; }
 constexpr int lane_elements(bool eight) { return eight ? 8 : 4; }
 constexpr int times_of(bool eight) { return eight ? 8 : 4; }
@@ -316,19 +316,22 @@ __device__ __forceinline__ uint32_t rounded_bf16(float2 x, uint32_t random) {
 }
 
 // x + y of products that keep their own rounding.  `one` comes with the
-// parameters: a plain sum is made one instruction with a product before it.
+// parameters: with a plain sum behind a product the moments' codes were not
+// those of steps rounded one by one.
 __device__ __forceinline__ float2 plus2(float2 x, float one, float2 y) {
   return fma2(x, both(one), y);
 }
 
-// The roots of x, which are 0 or positive, to the nearest number: Newton's
-// iteration with the residual in one rounding (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", IBM Journal of
-// Research and Development 34, 1990), r = s - (s^2 - x) / (2 s).  s, x times an
-// approximate reciprocal root, is within two last places; the residual is
-// exact, and its quotient good to 2^-20 of a last place.  Where an x is too
-// small for that (the residual would not be exact below 2^-100) or not finite,
-// the library's function.  top: the largest.
+// The roots of x, which are 0 or positive, to the nearest number but where they
+// lie within 2^-20 of a last place of the middle of two (39 of 2^25 significands
+// and exponents): Newton's iteration with the residual in one rounding
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", IBM Journal of Research and Development 34, 1990), r = s - (s^2 -
+// x) / (2 s).  s, x times an approximate reciprocal root, is within two last
+// places; the residual is exact, and its quotient good to 2^-20 of a last place.
+// Where an x of the lane is too small for that (the residual would not be exact
+// below 2^-100; 0 is among them) or not finite, the library's function.  top:
+// the largest.
 template <int H>
 __device__ __forceinline__ void roots(const float2 (&x)[H], float2 (&r)[H], float& top) {
   float low = 0x1p127f;

@@ -36,8 +36,10 @@ enum HeadsMode { kRotate = 0, kNorm = 1, kNormGrad = 2 };
 constexpr int kHeadWarps = 4;     // per block
 constexpr int kHeadParts = 1024;  // most blocks of a backward pass: its partial sums
 // Blocks per SM that stay, and that the registers are made to fit; passes that
-// are on their way.  (Forward 6 blocks, of 80 registers: 39.7 us; 4 with 4
-// passes: 34.8.  Backward 4 blocks, of 128 registers, spill: 82 us; 2: 66.)
+// are on their way.  (16384 tokens, norm and rotation 34.2 us and 54.8 backward:
+// forward 6 blocks, of 80 registers, 41.0 us, 4 34.8; backward 4 blocks, of 128
+// registers, spill, 84 us, 2 66; 2 passes on their way 34.8 and 55.5 us, 4 34.3
+// and 54.9.)
 constexpr int head_blocks(HeadsMode mode, int runs) {
   return mode == kNormGrad ? (runs > 2 ? 2 : 3) : (runs > 2 ? 3 : 5);
 }
@@ -754,7 +756,7 @@ int launch_heads_as(HeadArgs& q, int64_t tokens, bool il, cudaStream_t s) {
 
 // Rows of which every lane has two runs, without a look at which lanes have
 // what: 16384 tokens of 16 and 8 heads of 128 in bfloat16, norm and rotation,
-// 37.2 us; with that look 38.9.
+// 34.2 us; with that look 34.7, backward 54.8 and 55.8.
 template <class T, int V, bool IL, HeadsMode MODE>
 int launch_heads_rows(HeadArgs& q, int64_t tokens, cudaStream_t s) {
   if (q.units == 1 << q.log_group && q.dim == 2 * V * q.units)

@@ -17,8 +17,11 @@ no other path than the library's, and no part in torch's autograd: results do
 not require gradients, whatever the inputs do, and the backward functions are
 calls of their own, as the optimizer step is (examples/policy_step.py has them
 together); but what a call writes in place (moments aside) has its version
-counter moved on, so that a backward pass of torch that saved it fails.  The first 8-bit product on a device
-allocates its status word: let it run before a stream capture.
+counter moved on, so that a backward pass of torch that saved it fails.  New
+tensors come from torch's CUDA allocator without its dispatcher: dispatch modes
+do not see them, and deterministic mode does not fill them before they are
+written.  The first 8-bit product on a device allocates its status word: let it
+run before a stream capture.
 """
 
 from __future__ import annotations
@@ -219,7 +222,10 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, *, factor: float = 1
 
 def rotary_table(frequencies, *, magnitude: float = 1.0, interleaved: bool = False,
                  device="cuda") -> Rotary:
-    """A Rotary from radians per position (numbers, or a tensor; float64)."""
+    """A Rotary from radians per position (numbers, or a tensor; float64).  The
+    turns hold the 53 bits of a float64 quotient: an angle at position p is off
+    by at most p 2^-52 of its frequency, and by nothing that grows with p beyond
+    that."""
     if isinstance(frequencies, torch.Tensor):
         frequencies = frequencies.double().tolist()
     words = []

@@ -69,14 +69,15 @@ class RotatedAdam:
 class AdamW:
     """AdamW over the parameters that RotatedAdam does not take (vectors,
     embeddings; operators.adamw): keeps their moments and counts the steps taken
-    (`count`).  Only the device knows whether a norm lets a step be taken, so from
-    the first step with one the count is a tensor there.
+    (`count`).  Only the device knows whether a norm lets a step be taken, so
+    from the first step with one the count is a tensor there.
 
     bits: 32 or 8, of the moments.  masters: float32 masters of 16-bit
     parameters (float16 always has one; bfloat16 without is rounded at random).
     seed: the random rounding's; instances that step in the same run need
-    different ones.  captured: the count is on the device from the start, so
-    that a captured step() counts on when it is replayed."""
+    different ones (0 unless told otherwise).  captured: the count is on the
+    device from the start, so that a captured step() counts on when it is
+    replayed."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, beta1: float = 0.9,
                  beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, *,
@@ -85,7 +86,8 @@ class AdamW:
         states = [ops.adamw_state(p, bits=bits) for p in self.params]
         self.m, self.v = [s[0] for s in states], [s[1] for s in states]
         keep = {torch.float16: True, torch.bfloat16: masters}
-        self.masters = [p.detach().float() if keep.get(p.dtype, False) else None for p in self.params]
+        self.masters = [p.detach().float() if keep.get(p.dtype, False) else None
+                        for p in self.params]
         self.lr, self.hyper = lr, dict(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
         self.seed = seed
         self.count = self._on_device(0) if captured else 0
