@@ -705,9 +705,9 @@ void* state_of(PyObject* o, const char* name, int64_t n, Current& device, uint8_
 
 void adamw(const py::object& params, const py::object& grads, const py::object& m,
            const py::object& v, const py::object& masters, int64_t step,
-           const MaybeTensor& step_device, bool counts, double lr, const MaybeTensor& lr_device, double beta1,
-           double beta2, double eps, double weight_decay, const MaybeTensor& norm, double max_norm,
-           double scale, uint64_t seed) {
+           const MaybeTensor& step_device, bool counts, double lr, const MaybeTensor& lr_device,
+           double beta1, double beta2, double eps, double weight_decay, const MaybeTensor& norm,
+           double max_norm, double scale, uint64_t seed) {
   const List ps(params, "params"), gs(grads, "grads"), m1(m, "m"), v1(v, "v");
   std::optional<List> ms;
   if (!masters.is_none()) ms.emplace(masters, "masters");

@@ -521,7 +521,8 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequ
     counts: step, a tensor, holds the steps taken so far, this call is the one
     after them, and it moves step on unless the norm has it not taken.  seed:
     the random rounding's, whose other half is the step: calls of the same step
-    need different ones.  State and masters that are given twice are refused."""
+    need different ones.  What is written must not overlap (one tensor twice is
+    refused, views a part on are not noticed)."""
     if stream is not None:
         params, grads, m, v = list(params), list(grads), list(m), list(v)  # (read twice)
         masters = None if masters is None else list(masters)
